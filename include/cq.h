@@ -333,6 +333,150 @@ int32_t cq_w4a16_matmul(const uint16_t *x, const int32_t *qweight, const uint16_
                         int64_t out, int64_t in, float *y, void *stream);
 
 /*
+ * Running the packed checkpoint: the linear layer over the GPTQ-v1 tensors, the paged key/value
+ * cache and the attention that reads it (model card, "Quantization configuration": 16-bit
+ * activations; "Calibration and evaluation data": windows of 256 tokens, which these operators
+ * carry through layers that are quantized already).  The conventions above hold: device pointers,
+ * the caller's stream and workspace, argument errors before anything is enqueued.  Strides and
+ * leading dimensions are in elements.
+ */
+
+/* Element types. */
+#define CQ_BF16 0
+#define CQ_F16 1
+#define CQ_F32 2
+
+/* Activations: max(z, 0); z / (1 + e^-z); z (1 + erf(z / sqrt 2)) / 2; and its tanh form
+ * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2. */
+#define CQ_ACT_NONE 0
+#define CQ_ACT_RELU 1
+#define CQ_ACT_SILU 2
+#define CQ_ACT_GELU 3
+#define CQ_ACT_GELU_TANH 4
+
+/*
+ * Linear layer over the GPTQ-v1 tensors with its epilogue:
+ *        z[m][c] = sum_g s[g][c] sum_{k in g} x[m][k] (u[k][c] - 8) + bias[c],
+ *        y[m][o] = act(z[m][o]) + residual[m][o]                        (gated = 0)
+ *        y[m][o] = act(z[m][o]) z[m][out + o] + residual[m][o]          (gated = 1)
+ * each group's sum in fp32 on the matrix cores (exact products), its scale one fp32 fma, the
+ * epilogue in fp32 and one rounding into y's type.
+ *   x         x_type (CQ_BF16 or CQ_F16) [M] rows of `in`, ldx apart; 16-byte aligned, ldx a
+ *             multiple of 8.
+ *   qweight   int32 [in/8][cols], scales uint16 [in/128][cols] binary16 bits, as packed by
+ *             cq_pack_gptq_v1; cols = out, or 2 out when gated (the gate's out columns first).
+ *   bias      nullable, x_type [cols].
+ *   residual  nullable, x_type [M] rows of `out`, ldr apart; it may be y itself where both have
+ *             the same type and leading dimension.
+ *   y         out, y_type (x_type or CQ_F32) [M] rows of `out`, ldy apart.
+ * in a positive multiple of 128; cols < 2^31, in <= 2^24, M < 2^31; M == 0 or out == 0 enqueues
+ * nothing.
+ */
+int32_t cq_w4a16_linear(const void *x, int64_t ldx, int32_t x_type, const int32_t *qweight, const uint16_t *scales,
+                        const void *bias, const void *residual, int64_t ldr, int32_t activation, int32_t gated,
+                        int64_t M, int64_t out, int64_t in, void *y, int64_t ldy, int32_t y_type, void *stream);
+
+/*
+ * Block tables and slot maps of a paged cache, built on the GPU from the requests' lengths.
+ * Pages hold page_size tokens.  Request r holds ctx_len[r] tokens in the pages
+ * block_table[r][0 .. ceil(ctx_len[r] / page_size)) and receives new_len[r] more.  In request order,
+ * each takes the pages it needs beyond those from the end of the list free_pages[0 .. n_free), in
+ * block order.  A request whose lengths are negative, or longer than max_pages pages, is invalid
+ * (status 2) and takes nothing; from the first valid request on whose pages or tokens no longer
+ * fit (n_free pages, max_tokens tokens), valid requests are refused (status 1).
+ *   ctx_len, new_len  int32 [n_requests].
+ *   free_pages        int32 [free_capacity]; n_free int32 [1] (clamped to 0 .. free_capacity).
+ *   block_table       int32 rows of max_pages, table_stride apart; in and out: the entries of the
+ *                     pages taken are written, the others kept.
+ *   cu_q              out, int32 [n_requests + 1]: prefix sums of the new tokens served.
+ *   kv_len            out, int32 [n_requests]: ctx_len + new_len where served, else max(ctx_len, 0).
+ *   slots             out, int32 [max_tokens]: page * page_size + offset of each new token, requests
+ *                     back to back; -1 from cu_q[n_requests] on (and where the token's page, one
+ *                     held before, is entered as negative or gives a slot beyond 2^31 - 1).
+ *   positions         out, int32 [max_tokens]: the token's position in its request; 0 past the end.
+ *   status            out, int32 [n_requests]: 0 served, 1 refused, 2 invalid.
+ *   n_left            out, int32 [1]: the pages left, free_pages[0 .. n_left); not n_free itself.
+ * The call may be repeated: its inputs (block_table's taken entries apart) are left alone, so the
+ * outputs must not overlap them.  0 <= n_requests <= CQ_MAX_REQUESTS, 0 <= max_tokens,
+ * page_size >= 1, max_pages >= 1, max_pages * page_size < 2^31, table_stride >= max_pages.
+ */
+#define CQ_MAX_REQUESTS 4096
+int32_t cq_kv_block_map(const int32_t *ctx_len, const int32_t *new_len, int32_t n_requests, int32_t page_size,
+                        const int32_t *free_pages, const int32_t *n_free, int32_t free_capacity,
+                        int32_t *block_table, int64_t table_stride, int32_t max_pages, int32_t max_tokens,
+                        int32_t *cu_q, int32_t *kv_len, int32_t *slots, int32_t *positions, int32_t *status,
+                        int32_t *n_left, void *stream);
+
+/*
+ * New keys and values into the pages of the cache.
+ *   k, v              16-bit elements [n_tokens][kv_heads][head_dim]: *_token_stride and
+ *                     *_head_stride apart, head_dim contiguous.
+ *   k_cache, v_cache  in and out, [n_pages][kv_heads][page_size][head_dim]: page_stride, head_stride
+ *                     and row_stride apart (the same for both), head_dim contiguous.
+ *   slots             int32 [n_tokens]; a token whose slot is outside [0, n_pages * page_size) is
+ *                     not written.  No slot may occur twice.
+ * n_tokens, n_pages >= 0; kv_heads, page_size, head_dim >= 1; strides >= 0, those of the cache
+ * at least what the layout's order needs is the caller's care.
+ */
+int32_t cq_kv_cache_write(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                          int64_t v_token_stride, int64_t v_head_stride, void *k_cache, void *v_cache,
+                          int64_t page_stride, int64_t head_stride, int64_t row_stride, int32_t n_pages,
+                          int32_t page_size, int32_t kv_heads, int32_t head_dim, const int32_t *slots,
+                          int32_t n_tokens, void *stream);
+
+/*
+ * Attention of new tokens over a paged cache.  Request r has the n = cu_q[r + 1] - cu_q[r] packed
+ * query tokens from cu_q[r] on and kv_len[r] cached tokens, the new ones last: its i-th query token
+ * stands at position p = kv_len[r] - n + i and sees the keys j < kv_len[r] with j <= p (causal) and
+ * j > p - window (window > 0).  Query head h reads key/value head h / (heads / kv_heads).
+ *        out = sum_j softmax_j(scale q . k_j) v_j,    lse = log sum_j exp(scale q . k_j)
+ * over the keys seen; a token that sees none, or belongs to no request, gets out = 0, lse = -inf.
+ * What a masked key or value holds (an unwritten slot, an infinity, a NaN) has no effect on the row
+ * that does not see it.  Scores, softmax statistics and sums are fp32; the weights are rounded to the
+ * 16-bit type for their product with V on the matrix cores.
+ *   type              CQ_BF16 or CQ_F16: q, k_cache, v_cache and out.
+ *   q, out            [n_tokens][heads][head_dim], strides as given, head_dim contiguous.
+ *   k_cache, v_cache  as for cq_kv_cache_write.
+ *   block_table       int32 rows of max_pages, table_stride apart: position j is in page
+ *                     block_table[r][j / page_size]; keys of a page outside [0, n_pages) or past
+ *                     max_pages count as masked.
+ *   cu_q, kv_len      int32 [n_requests + 1], [n_requests], cu_q non-decreasing.
+ *   max_q, max_kv     bounds of n and kv_len, from the host: they set how the work is divided.  Query
+ *                     tokens past max_q are not computed (their out is left as it is); kv_len may
+ *                     exceed max_kv, at a loss of speed.
+ *   lse               out, nullable, float [n_tokens][heads].
+ *   workspace         cq_paged_attention_workspace_size(...) bytes for the same sizes (none: may be
+ *                     NULL).
+ * q, k_cache, v_cache and out 16-byte aligned, all strides multiples of 8; head_dim a multiple of 8 up
+ * to CQ_MAX_HEAD_DIM; heads a multiple of kv_heads; window > 0 needs causal; scale finite.
+ */
+#define CQ_MAX_HEAD_DIM 256
+typedef struct cq_paged_attention_args {
+    const void *q;
+    const void *k_cache;
+    const void *v_cache;
+    const int32_t *block_table;
+    const int32_t *cu_q;
+    const int32_t *kv_len;
+    void *out;
+    float *lse;
+    int64_t q_token_stride, q_head_stride;
+    int64_t out_token_stride, out_head_stride;
+    int64_t page_stride, head_stride, row_stride;
+    int64_t table_stride;
+    int32_t type;
+    int32_t n_tokens, n_requests, max_q, max_kv;
+    int32_t heads, kv_heads, head_dim;
+    int32_t page_size, n_pages, max_pages;
+    int32_t causal, window;
+    float scale;
+} cq_paged_attention_args;
+size_t cq_paged_attention_workspace_size(int32_t n_tokens, int32_t n_requests, int32_t max_q, int32_t max_kv,
+                                         int32_t heads, int32_t kv_heads, int32_t head_dim);
+int32_t cq_paged_attention(const cq_paged_attention_args *args, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/*
  * Separately normalized environment diagonals from calibration activations
  * (CliffQuant README, "What CliffQuant changes": each channel's sensitivity
  * weighted by its activations, per calibration environment, each environment

@@ -36,6 +36,10 @@ __all__ = [
     "cq_heldout_workspace_size", "cq_heldout_compare", "heldout_compare", "cq_diagonals_workspace_size",
     "cq_environment_diagonals", "environment_diagonals", "cq_w4a16_matmul", "w4a16_matmul", "EXPORTED_SYMBOLS",
     "cq_probe_valu_fma", "probe_valu_fma",
+    "BF16", "F16", "F32", "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "MAX_REQUESTS",
+    "MAX_HEAD_DIM", "PagedAttentionArgs", "cq_w4a16_linear", "w4a16_linear", "cq_kv_block_map", "kv_block_map",
+    "cq_kv_cache_write", "kv_cache_write", "cq_paged_attention_workspace_size", "cq_paged_attention",
+    "paged_attention",
 ]
 
 GROUP = 128
@@ -43,6 +47,12 @@ MAX_GROUP = 256
 EXHAUSTIVE, CANDIDATE, BOUNDED = 0, 1, 2
 ABSMAX, POOLED_WMSE = 0, 1
 FLAG_BAD_INPUT, FLAG_NEAR_TIE, FLAG_EXACT_TIE, FLAG_FALLBACK, FLAG_FP64_SWEEP = 1, 2, 4, 8, 16
+BF16, F16, F32 = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
+MAX_REQUESTS = 4096
+MAX_HEAD_DIM = 256
+_TYPES = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
+_ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH}
 _METHODS = {"exhaustive": EXHAUSTIVE, "candidate": CANDIDATE, "bounded": BOUNDED}
 EXPORTED_SYMBOLS = ("cq_abi_version", "cq_status_string", "cq_workspace_size", "cq_quantize_groups",
                     "cq_quantize_groups_spec", "cq_quantize_groups_noalloc",
@@ -51,7 +61,8 @@ EXPORTED_SYMBOLS = ("cq_abi_version", "cq_status_string", "cq_workspace_size", "
                     "cq_proxy_workspace_size",
                     "cq_proxy_worst_env_wmse", "cq_proxy_worst_env_wmse_multi", "cq_heldout_workspace_size",
                     "cq_heldout_compare", "cq_diagonals_workspace_size", "cq_environment_diagonals",
-                    "cq_w4a16_matmul", "cq_probe_valu_fma")
+                    "cq_w4a16_matmul", "cq_probe_valu_fma", "cq_w4a16_linear", "cq_kv_block_map",
+                    "cq_kv_cache_write", "cq_paged_attention_workspace_size", "cq_paged_attention")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lib = None
@@ -61,6 +72,18 @@ class CQError(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {cq_status_string(status)} (status {status})")
         self.status = status
+
+
+class PagedAttentionArgs(ctypes.Structure):
+    """cq_paged_attention_args of cq.h: device pointers as integers, strides in elements."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k_cache", "v_cache", "block_table", "cu_q", "kv_len", "out",
+                                               "lse")] + \
+               [(n, ctypes.c_int64) for n in ("q_token_stride", "q_head_stride", "out_token_stride",
+                                              "out_head_stride", "page_stride", "head_stride", "row_stride",
+                                              "table_stride")] + \
+               [(n, ctypes.c_int32) for n in ("type", "n_tokens", "n_requests", "max_q", "max_kv", "heads",
+                                              "kv_heads", "head_dim", "page_size", "n_pages", "max_pages",
+                                              "causal", "window")] + [("scale", ctypes.c_float)]
 
 
 def library_path() -> str:
@@ -120,6 +143,16 @@ def load():
         lib.cq_heldout_compare.argtypes = [P, P, I64, P, I32, P, I32, ctypes.c_double, P, P, P, P, P, SZ, P]
         lib.cq_probe_valu_fma.restype = I32
         lib.cq_probe_valu_fma.argtypes = [I32, I32, I32, P, P, ctypes.POINTER(ctypes.c_double), P]
+        lib.cq_w4a16_linear.restype = I32
+        lib.cq_w4a16_linear.argtypes = [P, I64, I32, P, P, P, P, I64, I32, I32, I64, I64, I64, P, I64, I32, P]
+        lib.cq_kv_block_map.restype = I32
+        lib.cq_kv_block_map.argtypes = [P, P, I32, I32, P, P, I32, P, I64, I32, I32, P, P, P, P, P, P, P]
+        lib.cq_kv_cache_write.restype = I32
+        lib.cq_kv_cache_write.argtypes = [P, I64, I64, P, I64, I64, P, P, I64, I64, I64, I32, I32, I32, I32, P, I32, P]
+        lib.cq_paged_attention_workspace_size.restype = SZ
+        lib.cq_paged_attention_workspace_size.argtypes = [I32] * 7
+        lib.cq_paged_attention.restype = I32
+        lib.cq_paged_attention.argtypes = [ctypes.POINTER(PagedAttentionArgs), P, SZ, P]
         _lib = lib
     return _lib
 
@@ -135,6 +168,15 @@ def _p(t):
         raise ValueError("arrays passed to the library must live on the GPU")
     if not t.is_contiguous():
         raise ValueError("arrays passed to the library must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t):
+    """Device pointer of a strided CUDA/HIP tensor (None -> NULL); its strides are passed beside it."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda:
+        raise ValueError("arrays passed to the library must live on the GPU")
     return t.data_ptr()
 
 
@@ -314,6 +356,41 @@ def cq_heldout_compare(pa, pb, n_groups, module_offsets, n_modules, boot_idx, n_
                                      _stream(stream)), "cq_heldout_compare")
 
 
+def cq_w4a16_linear(x, ldx, x_type, qweight, scales, bias, residual, ldr, activation, gated, M, out, inp, y, ldy,
+                    y_type, stream=None):
+    """x, residual and y may be strided rows (their leading dimensions are arguments)."""
+    _check(load().cq_w4a16_linear(_rows(x), ldx, x_type, _p(qweight), _p(scales), _p(bias), _rows(residual), ldr,
+                                  activation, gated, M, out, inp, _rows(y), ldy, y_type, _stream(stream)),
+           "cq_w4a16_linear")
+
+
+def cq_kv_block_map(ctx_len, new_len, n_requests, page_size, free_pages, n_free, free_capacity, block_table,
+                    table_stride, max_pages, max_tokens, cu_q, kv_len, slots, positions, status, n_left, stream=None):
+    _check(load().cq_kv_block_map(_p(ctx_len), _p(new_len), n_requests, page_size, _p(free_pages), _p(n_free),
+                                  free_capacity, _rows(block_table), table_stride, max_pages, max_tokens, _p(cu_q),
+                                  _p(kv_len), _p(slots), _p(positions), _p(status), _p(n_left), _stream(stream)),
+           "cq_kv_block_map")
+
+
+def cq_kv_cache_write(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, k_cache, v_cache,
+                      page_stride, head_stride, row_stride, n_pages, page_size, kv_heads, head_dim, slots, n_tokens,
+                      stream=None):
+    _check(load().cq_kv_cache_write(_rows(k), k_token_stride, k_head_stride, _rows(v), v_token_stride, v_head_stride,
+                                    _rows(k_cache), _rows(v_cache), page_stride, head_stride, row_stride, n_pages,
+                                    page_size, kv_heads, head_dim, _p(slots), n_tokens, _stream(stream)),
+           "cq_kv_cache_write")
+
+
+def cq_paged_attention_workspace_size(n_tokens: int, n_requests: int, max_q: int, max_kv: int, heads: int,
+                                      kv_heads: int, head_dim: int) -> int:
+    return load().cq_paged_attention_workspace_size(n_tokens, n_requests, max_q, max_kv, heads, kv_heads, head_dim)
+
+
+def cq_paged_attention(args: PagedAttentionArgs, workspace=None, stream=None):
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().cq_paged_attention(args, _p(workspace), ws_bytes, _stream(stream)), "cq_paged_attention")
+
+
 # ---------------------------------------------------------------- helpers
 def _workspace(nbytes: int, device):
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
@@ -468,6 +545,172 @@ def proxy_worst_env_wmse_multi(w, d_eval, scales, module_offsets, d_period=None,
         cq_proxy_worst_env_wmse_multi(w, d_eval, d_period, E, n, n_pol, scales, module_offsets, n_modules, mm,
                                       macro, pg, ws, stream)
     return pg, mm, macro
+
+
+def _empty(shape, dtype, like, stream):
+    """An output (or workspace) in the memory pool of the stream that the kernels run on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _one_device(first, **others):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, the first array on {first.device}")
+
+
+def _int32(**arrays):
+    for name, t in arrays.items():
+        if t.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32")
+
+
+def w4a16_linear(x, qweight, scales, bias=None, residual=None, activation="none", gated=False, out_dtype=None,
+                 out=None, stream=None):
+    """y [M, out] = act(x W + bias) + residual over GPTQ-v1 tensors; gated: qweight holds the gate's
+    columns, then as many others, and y = act(x Wg + bg) * (x Wu + bu) + residual.
+
+    x is bfloat16 or float16 [M, in] (rows may be strided: 16-byte aligned, stride a multiple of
+    8), qweight int32 [in/8, cols], scales int16 or float16 [in/128, cols]; bias [cols] and residual
+    [M, out] have x's type.  activation: "none", "relu", "silu", "gelu" or "gelu_tanh".  The result
+    has x's type, or float32 with out_dtype=torch.float32, or goes into ``out`` (which may be the
+    residual itself)."""
+    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("x must be bfloat16 or float16 [M, in]")
+    M, inp = x.shape
+    if qweight.dim() != 2 or qweight.dtype != torch.int32 or qweight.shape[0] * 8 != inp or inp % GROUP:
+        raise ValueError("qweight must be int32 [in/8, cols], in a multiple of 128")
+    cols = qweight.shape[1]
+    if scales.shape != (inp // GROUP, cols) or scales.element_size() != 2:
+        raise ValueError("scales must be 16-bit [in/128, cols]")
+    if gated and cols % 2:
+        raise ValueError("gated needs an even number of columns")
+    n = cols // 2 if gated else cols
+    if bias is not None and (bias.shape != (cols,) or bias.dtype != x.dtype):
+        raise ValueError("bias must be [cols], of x's type")
+    if residual is not None and (residual.shape != (M, n) or residual.dtype != x.dtype):
+        raise ValueError("residual must be [M, out], of x's type")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
+    _one_device(x, qweight=qweight, scales=scales, bias=bias, residual=residual, out=out)
+    if out is None:
+        out = _empty((M, n), out_dtype or x.dtype, x, stream)
+    elif out.shape != (M, n) or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out must be [M, out], of the type asked for")
+    if out.dtype not in (x.dtype, torch.float32):
+        raise ValueError("the result has x's type or float32")
+    for name, t in (("x", x), ("residual", residual), ("out", out)):
+        if t is not None and t.stride(1) != 1 and t.shape[1] > 1:
+            raise ValueError(f"the rows of {name} must be contiguous")
+    cq_w4a16_linear(x, _ld(x), _TYPES[x.dtype], qweight, scales, bias, residual,
+                    0 if residual is None else _ld(residual), _ACTIVATIONS[activation], int(gated), M, n, inp,
+                    out, _ld(out), _TYPES[out.dtype], stream)
+    return out
+
+
+def _ld(t):
+    """Leading dimension of a row-major matrix; that of a single row is its length."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _step(t, dim):
+    """Stride of a dimension; that of a single entry is never used, and 0."""
+    return t.stride(dim) if t.shape[dim] > 1 else 0
+
+
+def kv_block_map(ctx_len, new_len, free_pages, n_free, block_table, page_size, max_tokens, stream=None):
+    """Block tables and slot maps of a paged cache from the requests' lengths.
+
+    ctx_len, new_len int32 [R]: tokens held and to come; free_pages int32 [capacity] of which the
+    first n_free (int32 [1]) are free, taken from the end; block_table int32 [R, max_pages], updated in
+    place.  Returns a dict of int32 tensors: cu_q [R + 1], kv_len [R], slots and positions
+    [max_tokens] (slot -1 past the last token), status [R] (0 served, 1 refused for want of pages
+    or tokens, 2 invalid) and n_left [1]."""
+    R = ctx_len.numel()
+    _int32(ctx_len=ctx_len, new_len=new_len, free_pages=free_pages, n_free=n_free, block_table=block_table)
+    if new_len.numel() != R or n_free.numel() != 1 or block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("ctx_len and new_len must be [R], n_free [1], block_table [R, max_pages]")
+    if block_table.stride(1) != 1 and block_table.shape[1] > 1:
+        raise ValueError("the rows of block_table must be contiguous")
+    _one_device(ctx_len, new_len=new_len, free_pages=free_pages, n_free=n_free, block_table=block_table)
+    sizes = (R + 1, R, max_tokens, max_tokens, R, 1)
+    cu, kv, slots, pos, status, left = _empty(sum(sizes), torch.int32, ctx_len, stream).split(sizes)
+    cq_kv_block_map(ctx_len, new_len, R, page_size, free_pages, n_free, free_pages.numel(), block_table,
+                    _ld(block_table), block_table.shape[1], max_tokens, cu, kv, slots,
+                    pos, status, left, stream)
+    return {"cu_q": cu, "kv_len": kv, "slots": slots, "positions": pos, "status": status, "n_left": left}
+
+
+def _cache_shape(k_cache, v_cache):
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or \
+            any(k_cache.shape[i] > 1 and v_cache.stride(i) != k_cache.stride(i) for i in range(4)):
+        raise ValueError("k_cache and v_cache must be [pages, kv_heads, page_size, head_dim], strided alike")
+    if k_cache.dtype not in (torch.bfloat16, torch.float16) or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must be bfloat16 or float16")
+    if k_cache.stride(3) != 1:
+        raise ValueError("head_dim must be contiguous")
+
+
+def kv_cache_write(k, v, k_cache, v_cache, slots, stream=None):
+    """Writes k, v [T, kv_heads, head_dim] (strided views allowed) into the caches
+    [pages, kv_heads, page_size, head_dim] at slots int32 [T] (page * page_size + offset; a
+    negative slot is skipped)."""
+    _cache_shape(k_cache, v_cache)
+    T = slots.numel()
+    _int32(slots=slots)
+    want = (T, k_cache.shape[1], k_cache.shape[3])
+    if k.shape != want or v.shape != want or k.dtype != k_cache.dtype or v.dtype != k_cache.dtype:
+        raise ValueError("k and v must be [T, kv_heads, head_dim] of the caches' type, slots int32 [T]")
+    if k.stride(2) != 1 or v.stride(2) != 1:
+        raise ValueError("head_dim must be contiguous")
+    _one_device(k_cache, v_cache=v_cache, k=k, v=v, slots=slots)
+    cq_kv_cache_write(k, _step(k, 0), _step(k, 1), v, _step(v, 0), _step(v, 1), k_cache, v_cache, _step(k_cache, 0),
+                      _step(k_cache, 1), _step(k_cache, 2), k_cache.shape[0], k_cache.shape[2], want[1], want[2],
+                      slots, T, stream)
+
+
+def paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_kv, scale=None, causal=True, window=0,
+                    out=None, lse=None, workspace=None, stream=None):
+    """Attention of packed new tokens over a paged cache, the new tokens' keys in it already.
+
+    q [T, heads, head_dim] (a strided view allowed), caches [pages, kv_heads, page_size, head_dim],
+    block_table int32 [R, max_pages], cu_q int32 [R + 1], kv_len int32 [R] (the new tokens
+    included); max_q and max_kv are the host's bounds of the requests' new and cached tokens.
+    scale defaults to 1/sqrt(head_dim).  Returns out [T, heads, head_dim] of q's type; ``lse``, if
+    given, is a contiguous float32 [T, heads] to fill."""
+    _cache_shape(k_cache, v_cache)
+    if q.dim() != 3 or q.dtype != k_cache.dtype or q.shape[2] != k_cache.shape[3] or q.stride(2) != 1:
+        raise ValueError("q must be [T, heads, head_dim] of the caches' type, head_dim contiguous")
+    _int32(block_table=block_table, cu_q=cu_q, kv_len=kv_len)
+    T, H, D = q.shape
+    R = kv_len.numel()
+    if cu_q.numel() != R + 1 or block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("cu_q must be [R + 1], kv_len [R], block_table [R, max_pages]")
+    if block_table.stride(1) != 1 and block_table.shape[1] > 1:
+        raise ValueError("the rows of block_table must be contiguous")
+    if lse is not None and (lse.shape != (T, H) or lse.dtype != torch.float32):
+        raise ValueError("lse must be float32 [T, heads]")
+    _one_device(q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, cu_q=cu_q, kv_len=kv_len, out=out,
+                lse=lse)
+    if out is None:
+        out = _empty((T, H, D), q.dtype, q, stream)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.stride(2) != 1:
+        raise ValueError("out must be [T, heads, head_dim] of q's type, head_dim contiguous")
+    Hkv = k_cache.shape[1]
+    need = cq_paged_attention_workspace_size(T, R, max_q, max_kv, H, Hkv, D)
+    if need and workspace is None:
+        workspace = _empty(need, torch.uint8, q, stream)
+    cq_paged_attention(PagedAttentionArgs(
+        _rows(q), _rows(k_cache), _rows(v_cache), _rows(block_table), _p(cu_q), _p(kv_len), _rows(out), _p(lse),
+        _step(q, 0), _step(q, 1), _step(out, 0), _step(out, 1), _step(k_cache, 0), _step(k_cache, 1),
+        _step(k_cache, 2), _ld(block_table), _TYPES[q.dtype], T, R, max_q, max_kv, H,
+        Hkv, D, k_cache.shape[2], k_cache.shape[0], block_table.shape[1], int(causal), window,
+        D ** -0.5 if scale is None else scale), workspace, stream)
+    return out
 
 
 def environment_diagonals(x, stream=None):

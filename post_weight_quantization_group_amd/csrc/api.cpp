@@ -6,6 +6,7 @@
 
 #include "cq.h"
 #include "launch.h"
+#include "serve_args.h"
 
 namespace {
 
@@ -366,6 +367,121 @@ int32_t cq_w4a16_matmul(const uint16_t* x, const int32_t* qweight, const uint16_
     if (!x || !qweight || !scales || !y) return CQ_EINVAL;
     if (!aligned(x, 16) || !aligned(qweight, 4) || !aligned(scales, 2) || !aligned(y, 4)) return CQ_EINVAL;
     return hip_status(cqk::launch_w4a16(x, qweight, scales, M, out, in, y, (hipStream_t)stream));
+}
+
+int32_t cq_w4a16_linear(const void* x, int64_t ldx, int32_t x_type, const int32_t* qweight, const uint16_t* scales,
+                        const void* bias, const void* residual, int64_t ldr, int32_t activation, int32_t gated,
+                        int64_t M, int64_t out, int64_t in, void* y, int64_t ldy, int32_t y_type, void* stream) {
+    if ((x_type != CQ_BF16 && x_type != CQ_F16) || (y_type != x_type && y_type != CQ_F32)) return CQ_EINVAL;
+    if (activation < CQ_ACT_NONE || activation > CQ_ACT_GELU_TANH || (gated != 0 && gated != 1)) return CQ_EINVAL;
+    if (M < 0 || out < 0 || in <= 0 || in % CQ_GROUP != 0) return CQ_EINVAL;
+    if (M > INT32_MAX || out > (gated ? INT32_MAX / 2 : INT32_MAX) || in > (int64_t)1 << 24) return CQ_EINVAL;
+    if (M == 0 || out == 0) return CQ_OK;
+    if (!x || !qweight || !scales || !y) return CQ_EINVAL;
+    if (ldx < in || ldx % 8 != 0 || ldy < out || (residual && ldr < out)) return CQ_EINVAL;
+    if (!aligned(x, 16) || !aligned(qweight, 4) || !aligned(scales, 2) || !aligned(bias, 2) || !aligned(residual, 2) ||
+        !aligned(y, y_type == CQ_F32 ? 4 : 2))
+        return CQ_EINVAL;
+    cqk::LinearArgs a{};
+    a.x = (const uint16_t*)x; a.qw = qweight; a.scales = scales;
+    a.bias = (const uint16_t*)bias; a.residual = (const uint16_t*)residual; a.y = y;
+    a.M = M; a.out = out; a.in = in; a.ldx = ldx; a.ldr = ldr; a.ldy = ldy;
+    a.x_f16 = x_type == CQ_F16; a.y_f32 = y_type == CQ_F32; a.act = activation; a.gated = gated;
+    return hip_status(cqk::launch_linear(a, (hipStream_t)stream));
+}
+
+int32_t cq_kv_block_map(const int32_t* ctx_len, const int32_t* new_len, int32_t n_requests, int32_t page_size,
+                        const int32_t* free_pages, const int32_t* n_free, int32_t free_capacity, int32_t* block_table,
+                        int64_t table_stride, int32_t max_pages, int32_t max_tokens, int32_t* cu_q, int32_t* kv_len,
+                        int32_t* slots, int32_t* positions, int32_t* status, int32_t* n_left, void* stream) {
+    if (n_requests < 0 || n_requests > CQ_MAX_REQUESTS || page_size < 1 || max_pages < 1 || max_tokens < 0)
+        return CQ_EINVAL;
+    if ((int64_t)max_pages * page_size > INT32_MAX || table_stride < max_pages || free_capacity < 0) return CQ_EINVAL;
+    if (!n_free || !n_left || n_left == n_free || !cu_q) return CQ_EINVAL;
+    if (n_requests > 0 && (!ctx_len || !new_len || !block_table || !kv_len || !status)) return CQ_EINVAL;
+    if (n_requests > 0 && (kv_len == ctx_len || kv_len == new_len || status == ctx_len || status == new_len))
+        return CQ_EINVAL;
+    if ((free_capacity > 0 && !free_pages) || (max_tokens > 0 && (!slots || !positions))) return CQ_EINVAL;
+    const void* all[] = {ctx_len, new_len, free_pages, n_free, block_table, cu_q, kv_len, slots, positions, status,
+                         n_left};
+    for (const void* p : all)
+        if (!aligned(p, 4)) return CQ_EINVAL;
+    cqk::BlockMapArgs a{};
+    a.ctx = ctx_len; a.add = new_len; a.free_pages = free_pages; a.n_free = n_free; a.table = block_table;
+    a.cu = cu_q; a.kv_len = kv_len; a.slots = slots; a.positions = positions; a.status = status; a.n_left = n_left;
+    a.table_stride = table_stride; a.R = n_requests; a.page = page_size; a.free_cap = free_capacity;
+    a.max_pages = max_pages; a.max_tokens = max_tokens;
+    return hip_status(cqk::launch_block_map(a, (hipStream_t)stream));
+}
+
+int32_t cq_kv_cache_write(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                          int64_t v_token_stride, int64_t v_head_stride, void* k_cache, void* v_cache,
+                          int64_t page_stride, int64_t head_stride, int64_t row_stride, int32_t n_pages,
+                          int32_t page_size, int32_t kv_heads, int32_t head_dim, const int32_t* slots,
+                          int32_t n_tokens, void* stream) {
+    if (n_tokens < 0 || n_pages < 0 || kv_heads < 1 || page_size < 1 || head_dim < 1) return CQ_EINVAL;
+    if ((k_token_stride | k_head_stride | v_token_stride | v_head_stride | page_stride | head_stride | row_stride) < 0)
+        return CQ_EINVAL;
+    if (n_tokens == 0 || n_pages == 0) return CQ_OK;
+    if (!k || !v || !k_cache || !v_cache || !slots) return CQ_EINVAL;
+    if (!aligned(k, 2) || !aligned(v, 2) || !aligned(k_cache, 2) || !aligned(v_cache, 2) || !aligned(slots, 4))
+        return CQ_EINVAL;
+    cqk::CacheWriteArgs a{};
+    a.k = (const uint16_t*)k; a.v = (const uint16_t*)v; a.kc = (uint16_t*)k_cache; a.vc = (uint16_t*)v_cache;
+    a.slots = slots; a.k_tok = k_token_stride; a.k_head = k_head_stride; a.v_tok = v_token_stride;
+    a.v_head = v_head_stride; a.c_page = page_stride; a.c_head = head_stride; a.c_row = row_stride;
+    a.n_slots = (int64_t)n_pages * page_size; a.T = n_tokens; a.H = kv_heads; a.D = head_dim; a.page = page_size;
+    return hip_status(cqk::launch_cache_write(a, (hipStream_t)stream));
+}
+
+static bool attention_sizes_ok(int32_t T, int32_t R, int32_t max_q, int32_t max_kv, int32_t H, int32_t Hkv, int32_t D) {
+    return T >= 0 && R >= 0 && max_q >= 0 && max_kv >= 0 && Hkv >= 1 && H >= Hkv && H % Hkv == 0 && H <= 65535 &&
+           D >= 8 && D <= CQ_MAX_HEAD_DIM && D % 8 == 0 && (int64_t)T * H <= INT32_MAX && R <= 65535;
+}
+
+size_t cq_paged_attention_workspace_size(int32_t n_tokens, int32_t n_requests, int32_t max_q, int32_t max_kv,
+                                         int32_t heads, int32_t kv_heads, int32_t head_dim) {
+    if (!attention_sizes_ok(n_tokens, n_requests, max_q, max_kv, heads, kv_heads, head_dim)) return 0;
+    return (size_t)cqk::attention_ws(n_requests, n_tokens, max_q, max_kv, heads, kv_heads, head_dim) * 4u;
+}
+
+int32_t cq_paged_attention(const cq_paged_attention_args* args, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+    if (!args) return CQ_EINVAL;
+    const cq_paged_attention_args& p = *args;
+    if (p.type != CQ_BF16 && p.type != CQ_F16) return CQ_EINVAL;
+    if (!attention_sizes_ok(p.n_tokens, p.n_requests, p.max_q, p.max_kv, p.heads, p.kv_heads, p.head_dim))
+        return CQ_EINVAL;
+    if (p.page_size < 1 || p.n_pages < 0 || p.max_pages < 0 || p.table_stride < p.max_pages) return CQ_EINVAL;
+    if ((int64_t)p.max_pages * p.page_size > INT32_MAX) return CQ_EINVAL;
+    if ((p.causal != 0 && p.causal != 1) || p.window < 0 || (p.window > 0 && !p.causal)) return CQ_EINVAL;
+    if (!(p.scale - p.scale == 0.0f)) return CQ_EINVAL;
+    if ((p.q_token_stride | p.q_head_stride | p.out_token_stride | p.out_head_stride | p.page_stride | p.head_stride |
+         p.row_stride) < 0 ||
+        (p.q_token_stride | p.q_head_stride | p.out_token_stride | p.out_head_stride | p.page_stride | p.head_stride |
+         p.row_stride) % 8 != 0)
+        return CQ_EINVAL;
+    if (p.n_tokens == 0) return CQ_OK;
+    if (!p.q || !p.out || !p.cu_q) return CQ_EINVAL;
+    if (p.n_requests > 0 && !p.kv_len) return CQ_EINVAL;
+    if (p.n_pages > 0 && p.max_pages > 0 && p.n_requests > 0 && (!p.k_cache || !p.v_cache || !p.block_table))
+        return CQ_EINVAL;
+    if (!aligned(p.q, 16) || !aligned(p.k_cache, 16) || !aligned(p.v_cache, 16) || !aligned(p.out, 16) ||
+        !aligned(p.block_table, 4) || !aligned(p.cu_q, 4) || !aligned(p.kv_len, 4) || !aligned(p.lse, 4))
+        return CQ_EINVAL;
+    const size_t need = cq_paged_attention_workspace_size(p.n_tokens, p.n_requests, p.max_q, p.max_kv, p.heads,
+                                                          p.kv_heads, p.head_dim);
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, ALIGN))) return CQ_EWORKSPACE;
+    cqk::AttentionArgs a{};
+    a.q = (const uint16_t*)p.q; a.kc = (const uint16_t*)p.k_cache; a.vc = (const uint16_t*)p.v_cache;
+    a.out = (uint16_t*)p.out; a.lse = p.lse; a.table = p.block_table; a.cu = p.cu_q; a.kv_len = p.kv_len;
+    a.q_tok = p.q_token_stride; a.q_head = p.q_head_stride; a.o_tok = p.out_token_stride; a.o_head = p.out_head_stride;
+    a.c_page = p.page_stride; a.c_head = p.head_stride; a.c_row = p.row_stride; a.table_stride = p.table_stride;
+    a.page = p.page_size; a.n_pages = p.n_pages; a.max_pages = p.max_pages;
+    a.R = p.n_requests; a.T = p.n_tokens; a.max_q = p.max_q; a.max_kv = p.max_kv;
+    a.H = p.heads; a.Hkv = p.kv_heads; a.D = p.head_dim; a.causal = p.causal; a.window = p.window;
+    a.f16 = p.type == CQ_F16; a.scale = p.scale; a.ws = (float*)workspace;
+    return hip_status(cqk::launch_attention(a, (hipStream_t)stream));
 }
 
 size_t cq_diagonals_workspace_size(int32_t E, int64_t T, int64_t in) {

@@ -1,0 +1,46 @@
+// 16-bit types and activations of the serving kernels.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace cqk {
+
+template <bool F16>
+__device__ __forceinline__ float to_f32(uint16_t b) {
+    if constexpr (F16) return (float)__builtin_bit_cast(_Float16, b);
+    return __uint_as_float((uint32_t)b << 16);
+}
+
+// Round to nearest even, NaN kept a NaN.
+template <bool F16>
+__device__ __forceinline__ uint16_t from_f32(float x) {
+    if constexpr (F16) return __builtin_bit_cast(uint16_t, (_Float16)x);
+    return __builtin_bit_cast(uint16_t, (__bf16)x);
+}
+
+enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4 };
+
+// z / (1 + exp(-z)): the sigmoid of large negative z is exp(z), which keeps its relative accuracy
+// until it underflows.
+__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
+
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+    if constexpr (ACT == ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
+    if constexpr (ACT == ACT_SILU) return z * sigmoid(z);
+    if constexpr (ACT == ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+    if constexpr (ACT == ACT_GELU_TANH) return z * sigmoid(1.5957691f * (z + 0.044715f * z * z * z));
+    return z;
+}
+
+__device__ __forceinline__ float activate(int act, float z) {
+    switch (act) {
+        case ACT_RELU: return activate<ACT_RELU>(z);
+        case ACT_SILU: return activate<ACT_SILU>(z);
+        case ACT_GELU: return activate<ACT_GELU>(z);
+        case ACT_GELU_TANH: return activate<ACT_GELU_TANH>(z);
+        default: return z;
+    }
+}
+
+}  // namespace cqk

@@ -1,0 +1,298 @@
+"""GPU: attention over the paged cache (cq_paged_attention) against its definition in 64 bits, within the bound
+that oracle.serving.paged_attention derives for each output.  Every slot that no request holds is NaN."""
+import numpy as np
+import pytest
+import torch
+
+import post_weight_quantization_group_amd as cq
+from parity import say
+from serving import Paged, TORCH, close, i32
+
+pytestmark = pytest.mark.gpu
+
+
+def _say(*a):
+    say("attention:", *a)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("H,Hkv,D,page", [(8, 2, 128, 16), (4, 4, 64, 16), (5, 1, 80, 24), (16, 2, 256, 64),
+                                          (2, 1, 8, 1), (32, 1, 96, 8), (6, 2, 200, 128)])
+def test_single_tokens(H, Hkv, D, page, kind):
+    _say("tokens", H, Hkv, D, page, kind)
+    Paged([(1, 1), (1, 2), (1, 17), (1, 64), (1, 65), (1, 300)], H, Hkv, D, page, kind).check(cq)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("lens", [[(1, 1)], [(5, 5), (3, 40), (1, 9)], [(33, 33), (0, 20), (64, 130)], [(130, 200)],
+                                  [(257, 300), (2, 2)]])
+@pytest.mark.parametrize("H,Hkv,D,page", [(8, 2, 128, 16), (3, 3, 64, 8), (2, 1, 256, 48)])
+def test_chunks(lens, H, Hkv, D, page, kind):
+    _say("chunks", lens, H, Hkv, D, page, kind)
+    Paged(lens, H, Hkv, D, page, kind, seed=len(lens)).check(cq)
+
+
+@pytest.mark.parametrize("D", [8, 16, 24, 40, 64, 72, 96, 120, 128, 136, 160, 192, 248, 256])
+def test_head_dims(D):
+    _say("head dim", D)
+    Paged([(40, 70), (1, 90)], 4, 2, D, 16, "bf16", seed=D).check(cq)
+    Paged([(1, 70), (1, 90)], 4, 2, D, 16, "f16", seed=D).check(cq)
+
+
+@pytest.mark.parametrize("group", [1, 2, 3, 7, 8, 16, 17, 33])
+def test_head_groups(group):
+    _say("group", group)
+    Paged([(20, 50), (1, 33)], 2 * group, 2, 64, 16, "bf16", seed=group).check(cq)
+    Paged([(1, 50), (1, 33)], 2 * group, 2, 64, 16, "bf16", seed=group).check(cq)
+
+
+@pytest.mark.parametrize("page", [1, 3, 16, 31, 32, 33, 100, 512])
+def test_pages_that_end_inside_a_tile(page):
+    _say("page", page)
+    Paged([(1, 129), (1, 31)], 4, 1, 64, page, "bf16", seed=page).check(cq)
+    Paged([(70, 129), (1, 31)], 4, 1, 64, page, "bf16", seed=page).check(cq)
+
+
+@pytest.mark.parametrize("window", [1, 2, 16, 50, 1000])
+@pytest.mark.parametrize("lens", [[(1, 200), (1, 3)], [(90, 200), (7, 7)]])
+def test_window(lens, window):
+    _say("window", window, lens)
+    Paged(lens, 4, 2, 128, 16, "f16", seed=window).check(cq, window=window)
+
+
+@pytest.mark.parametrize("lens", [[(1, 200)], [(9, 20), (40, 70)], [(150, 150)]])
+def test_not_causal(lens):
+    _say("not causal", lens)
+    Paged(lens, 4, 2, 64, 16, "bf16").check(cq, causal=False)
+
+
+@pytest.mark.parametrize("scale", [0.0, 1.0, -0.3, 4.0])
+def test_scales(scale):
+    _say("scale", scale)
+    Paged([(1, 90), (50, 60)], 4, 2, 64, 16, "bf16", seed=3).check(cq, scale=scale)
+    Paged([(1, 90), (1, 60)], 4, 2, 64, 16, "bf16", seed=3).check(cq, scale=scale)
+
+
+@pytest.mark.parametrize("lens", [[(1, 5000), (1, 1)], [(1, 20000)], [(3, 4097), (2, 600)], [(100, 2500), (1, 4000)]])
+def test_longer_caches(lens):
+    _say("longer", lens)
+    Paged(lens, 2, 1, 64, 16, "bf16", seed=len(lens)).check(cq)
+
+
+@pytest.mark.parametrize("lens", [[(4, 4), (1, 1)], [(1, 1), (1, 3)], [(200, 200)]])
+def test_rows_that_see_nothing(lens):
+    """Fewer cached tokens than new ones, none at all, and tokens that belong to no request."""
+    p = Paged(lens, 4, 2, 64, 16, "bf16")
+    for kv in ([n - 1 for n, _ in lens], [0] * len(lens), [n // 2 for n, _ in lens]):
+        _say("empty", lens, kv)
+        p.kv_np = np.array(kv)
+        p.kv = i32(kv)
+        p.check(cq)
+        p.check(cq, causal=True, window=2)
+    p.cu_np = np.minimum(p.cu_np, 1)
+    p.cu = i32(p.cu_np)
+    p.check(cq)
+
+
+def test_no_requests_and_no_tokens():
+    p = Paged([(3, 5)], 2, 1, 64, 16, "f16")
+    lse = torch.zeros((3, 2), device="cuda")
+    out = p.run(cq, cu_q=i32([0]), kv_len=i32([]), block_table=p.table[:0], lse=lse)
+    torch.cuda.synchronize()
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    assert p.run(cq, q=p.q[:0], cu_q=i32([0, 0])).shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("lens", [[(1, 40), (1, 70)], [(50, 80), (3, 9)]])
+def test_pages_that_are_not_there(lens):
+    """Entries outside the pool count as masked, and kv_len past the table's columns is cut there."""
+    p = Paged(lens, 4, 2, 64, 8, "bf16")
+    p.table_np[0, 1], p.table_np[0, 3], p.table_np[1, 0] = -1, 1 << 30, p.kc.shape[0]
+    p.table = i32(p.table_np)
+    p.check(cq)
+    p = Paged(lens, 4, 2, 64, 8, "bf16")
+    room = p.table_np.shape[1] * 8
+    r = int(np.argmax(p.kv_np))
+    p.kv = i32([room + 1000 if i == r else k for i, k in enumerate(p.kv_np)])
+    for c, t in ((p.kc_np, p.kc), (p.vc_np, p.vc)):          # the row now sees the whole last page
+        t.copy_(torch.nan_to_num(t, nan=0.5))
+        c[np.isnan(c)] = 0.5
+    p.kv_np[r] = room
+    p.check(cq)
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf, 3e38])
+@pytest.mark.parametrize("lens,first", [([(40, 60)], 50), ([(150, 150)], 64), ([(6, 30)], 27), ([(3, 4)], 2)])
+def test_what_later_tokens_hold_does_not_reach_earlier_rows(lens, first, bad):
+    """Keys and values from position `first` on are not finite: rows before it keep their values."""
+    _say("masked", bad, lens, first)
+    for which in ("k", "v", "kv"):
+        p = Paged(lens, 4, 2, 64, 16, "bf16", seed=first)
+        want, _, tol, _ = p.want()
+        pos = np.arange(first, lens[0][1])
+        for name, c in (("k", p.kc), ("v", p.vc)):
+            if name in which:
+                c[p.table[0, pos // 16].long(), :, torch.from_numpy(pos % 16).cuda()] = bad
+        out = p.run(cq)
+        torch.cuda.synchronize()
+        n, kv = lens[0]
+        clean = first - (kv - n)
+        assert clean > 0
+        close(out[:clean], want[:clean], tol[:clean], which)
+        if "v" in which and bad != 3e38 and "k" not in which:
+            got = out[clean:].float()
+            assert (torch.isnan(got) if np.isnan(bad) else got == bad).all()
+
+
+@pytest.mark.parametrize("lens,window", [([(40, 60)], 8), ([(1, 60)], 8), ([(150, 200)], 70)])
+def test_what_left_the_window_does_not_reach_later_rows(lens, window):
+    p = Paged(lens, 4, 2, 64, 16, "f16", seed=window)
+    want, _, tol, _ = p.want(window=window)
+    n, kv = lens[0]
+    last = (kv - n) + n // 2 - 1 if n > 1 else kv - window - 1  # positions up to here are NaN
+    pos = np.arange(0, last + 1)
+    for c in (p.kc, p.vc):
+        c[p.table[0, pos // 16].long(), :, torch.from_numpy(pos % 16).cuda()] = float("nan")
+    out = p.run(cq, window=window)
+    torch.cuda.synchronize()
+    rows = [i for i in range(n) if kv - n + i - window >= last]
+    assert rows
+    close(out[rows], want[rows], tol[rows])
+
+
+def test_infinite_and_nan_values_that_are_seen():
+    """An infinite value spreads as an infinity, both signs or a NaN as NaN, to the rows that see it."""
+    p = Paged([(60, 60)], 2, 1, 64, 16, "bf16")
+    for (pos, d, v) in ((10, 0, np.inf), (20, 0, -np.inf), (30, 1, np.nan), (5, 2, -np.inf)):
+        p.vc[p.table[0, pos // 16].long(), :, pos % 16, d] = v
+    out = p.run(cq).float()
+    torch.cuda.synchronize()
+    assert torch.isfinite(out[:10, :, 0]).all() and (out[10:20, :, 0] == np.inf).all() and torch.isnan(out[20:, :, 0]).all()
+    assert torch.isfinite(out[:30, :, 1]).all() and torch.isnan(out[30:, :, 1]).all()
+    assert (out[5:, :, 2] == -np.inf).all() and torch.isfinite(out[:, :, 3:]).all()
+
+
+@pytest.mark.parametrize("lens", [[(1, 90), (1, 50)], [(70, 90), (2, 50)]])
+def test_strides_and_orders(lens):
+    """q out of packed q-k-v rows, out into wider rows, the cache token-major, the table wider than needed."""
+    p = Paged(lens, 6, 2, 64, 16, "f16", order="nhd", table_extra=5)
+    T = p.q.shape[0]
+    wide = torch.zeros((T, 10, 64), dtype=torch.float16, device="cuda")
+    wide[:, 2:8] = p.q
+    dest = torch.full((T, 6, 80), 3.0, dtype=torch.float16, device="cuda")
+    bt = torch.full((len(lens), p.table.shape[1] + 3), 1 << 29, dtype=torch.int32, device="cuda")
+    bt[:, : p.table.shape[1]] = p.table
+    p.check(cq, q=wide[:, 2:8], out=dest[:, :, 8:72], block_table=bt[:, : p.table.shape[1]])
+    assert (dest[:, :, :8] == 3).all() and (dest[:, :, 72:] == 3).all()
+
+
+def test_one_allocation_for_both_caches_and_heads_outside():
+    """K and V interleaved per page: [pages, 2, kv_heads, page, D]."""
+    p = Paged([(1, 60), (30, 40)], 4, 2, 64, 16, "bf16")
+    both = torch.stack((p.kc, p.vc), dim=1)
+    p.check(cq, k_cache=both[:, 0], v_cache=both[:, 1])
+
+
+@pytest.mark.parametrize("lens", [[(1, 700)], [(100, 300)]])
+def test_bounds_larger_and_smaller_than_the_lengths(lens):
+    """max_q and max_kv only divide the work: larger bounds, and a kv_len beyond max_kv, change nothing but the
+    order of sums."""
+    p = Paged(lens, 4, 2, 64, 16, "bf16")
+    p.check(cq, max_q=lens[0][0] + 300, max_kv=20000)
+    p.check(cq, max_kv=16)
+
+
+@pytest.mark.parametrize("lens", [[(1, 3000), (1, 100)], [(200, 500), (1, 900)]])
+def test_same_bits_again_and_on_another_stream(lens):
+    p = Paged(lens, 8, 2, 128, 16, "bf16")
+    a = p.run(cq)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    b = p.run(cq, stream=s)
+    s.synchronize()
+    assert torch.equal(a, b) and torch.equal(a, p.run(cq))
+
+
+@pytest.mark.parametrize("lens", [[(1, 3000), (1, 100)], [(100, 200), (1, 900)]])
+def test_replayed_graph(lens):
+    p = Paged(lens, 8, 2, 64, 16, "f16")
+    T, H, D = p.q.shape
+    need = cq.cq_paged_attention_workspace_size(T, len(lens), p.max_q, p.max_kv, H, 2, D)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(p.q)
+    p.run(cq, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        p.run(cq, out=out, workspace=ws)
+    for k in range(4):
+        p.q.copy_(torch.randn_like(p.q))
+        p.kv.copy_(i32([max(1, kv - 7 * k) for _, kv in lens]))
+        eager = p.run(cq)
+        out.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager), k
+
+
+def test_cache_past_32_bit_offsets():
+    """The requests' pages lie past 2^31 elements of a cache of 4 GiB and more."""
+    p = Paged([(1, 40), (20, 30)], 4, 2, 128, 16, "bf16")
+    far = (1 << 31) // (2 * 16 * 128) + 1
+    n = p.kc.shape[0]
+    big = [torch.empty((far + n, 2, 16, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    big[0][far:], big[1][far:] = p.kc, p.vc
+    p.check(cq, k_cache=big[0], v_cache=big[1], block_table=torch.where(p.table >= 0, p.table + far, p.table))
+
+
+def test_the_new_tokens_own_keys_through_the_other_operators():
+    """Block map, cache write and attention in turn: prompts in two chunks, then tokens one by one, against the
+    whole prompts at once."""
+    H, Hkv, D, page, n = 4, 2, 64, 16, [50, 33, 7]
+    torch.manual_seed(0)
+    q, k, v = (torch.randn((sum(n), h, D), device="cuda").half() for h in (H, Hkv, Hkv))
+    start = np.concatenate([[0], np.cumsum(n)])
+    kc, vc = (torch.full((40, Hkv, page, D), float("nan"), dtype=torch.float16, device="cuda") for _ in range(2))
+    table = torch.full((3, 8), -1, dtype=torch.int32, device="cuda")
+    free, left = torch.randperm(40, device="cuda").int(), i32([40])
+    ctx, got = i32([0, 0, 0]), torch.zeros_like(q)
+    for step in ([20, 33, 1], [29, 0, 5], [1, 0, 1]):
+        m = cq.kv_block_map(ctx, i32(step), free, left, table, page, sum(step) + 2)
+        at = np.concatenate([start[r] + int(c) + np.arange(s) for r, (c, s) in enumerate(zip(ctx.tolist(), step))])
+        at = torch.from_numpy(at).cuda()
+        pad = torch.cat([at, at[:2]])                          # two padding tokens, slot -1
+        cq.kv_cache_write(k[pad], v[pad], kc, vc, m["slots"])
+        got[at] = cq.paged_attention(q[at], kc, vc, table, m["cu_q"], m["kv_len"], max(step), 64)
+        ctx, left = m["kv_len"], m["n_left"]
+    torch.cuda.synchronize()
+    assert ctx.tolist() == n and left.tolist() == [40 - 4 - 3 - 1]
+    qd, kd, vd = (t.double().cpu() for t in (q, k, v))
+    for r in range(3):
+        a, b = start[r], start[r + 1]
+        for h in range(H):
+            s = qd[a:b, h] @ kd[a:b, h // 2].T * D ** -0.5
+            s = s.masked_fill(torch.ones_like(s).triu(1).bool(), -np.inf)
+            want = torch.softmax(s, -1) @ vd[a:b, h // 2]
+            w = torch.softmax(s, -1) @ vd[a:b, h // 2].abs()
+            # weights and output rounded to f16, scores within 2^-16 of exact at these sizes
+            assert ((got[a:b, h].double().cpu() - want).abs() <= (2.0 ** -11 + 2.0 ** -14) * w + 2.0 ** -11 * want.abs() + 2.0 ** -24).all()
+
+
+def test_refusals():
+    p = Paged([(1, 20)], 4, 2, 64, 16, "bf16")
+    for kw in (dict(q=p.q.half()), dict(q=p.q[..., :32]), dict(k_cache=p.kc.float()), dict(v_cache=p.vc[:2]),
+               dict(cu_q=p.cu.long()), dict(kv_len=i32([1, 2])), dict(block_table=p.table[0]),
+               dict(lse=torch.zeros((1, 3), device="cuda")), dict(out=torch.zeros((1, 4, 64), device="cuda")),
+               dict(q=p.q.cpu()), dict(q=p.q.transpose(1, 2).contiguous().transpose(1, 2))):
+        with pytest.raises(ValueError):
+            p.run(cq, **kw)
+    for kw in (dict(q=torch.zeros((1, 3, 64), dtype=torch.bfloat16, device="cuda")), dict(window=-1),
+               dict(window=4, causal=False), dict(scale=float("inf")), dict(scale=float("nan")), dict(max_q=-1),
+               dict(q=torch.zeros((3, 4, 68), dtype=torch.bfloat16, device="cuda")[..., :64])):
+        with pytest.raises(cq.CQError):
+            p.run(cq, **kw)
+    odd = Paged([(1, 20)], 2, 1, 8, 16, "bf16")
+    with pytest.raises(cq.CQError):                            # head_dim 4
+        odd.run(cq, q=odd.q[..., :4].contiguous(), k_cache=odd.kc[..., :4].contiguous(),
+                v_cache=odd.vc[..., :4].contiguous())

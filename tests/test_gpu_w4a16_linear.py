@@ -1,0 +1,177 @@
+"""GPU: the linear layer over GPTQ-v1 tensors (cq_w4a16_linear) against its definition in 64 bits, within the
+bound that oracle.serving.w4a16_linear derives for each output."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import post_weight_quantization_group_amd as cq
+from oracle import serving as ref
+from parity import dev, say
+from serving import TORCH, close, t16
+
+pytestmark = pytest.mark.gpu
+
+
+def _weights(rng, cols, inp):
+    codes = rng.integers(-8, 8, (cols, inp)).astype(np.int8)
+    sv = rng.uniform(1e-3, 2e-2, (cols, inp // 128)).astype(np.float16)
+    return oracle.pack_gptq_v1(codes, sv.view(np.uint16), cols, inp)
+
+
+def _check(M, out, inp, x="bf16", y=None, act="none", gated=False, bias=False, res=False, seed=0, offset=0.0):
+    say(f"linear: M={M} out={out} in={inp} {x}->{y or x} {act} gated={gated} bias={bias} res={res}")
+    rng = np.random.default_rng(seed + M + out + inp)
+    cols = 2 * out if gated else out
+    qw, sc = _weights(rng, cols, inp)
+    xt, xn = t16(rng.standard_normal((M, inp)) + offset, x)
+    bt, bn = t16(rng.standard_normal(cols), x) if bias else (None, None)
+    rt, rn = t16(rng.standard_normal((M, out)), x) if res else (None, None)
+    got = cq.w4a16_linear(xt, dev(qw), dev(sc.view(np.int16)), bias=bt, residual=rt, activation=act, gated=gated,
+                          out_dtype=TORCH[y or x])
+    torch.cuda.synchronize()
+    assert got.dtype == TORCH[y or x]
+    want, tol = ref.w4a16_linear(xn, qw, sc, bn, rn, act, gated, y or x)
+    close(got, want, tol)
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 15, 16, 17, 31, 33, 64, 65, 127, 130, 257, 520])
+@pytest.mark.parametrize("out,inp", [(64, 128), (200, 384), (331, 1024)])
+def test_rows_and_shapes(M, out, inp):
+    _check(M, out, inp, x="bf16" if M % 2 else "f16", y="f32", bias=True)
+
+
+@pytest.mark.parametrize("out", [1, 2, 3, 7, 8, 15, 16, 17, 63, 65, 127, 129, 255, 256, 257])
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_odd_widths(M, out):
+    _check(M, out, 256, x="f16", res=True)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M,x,y", [(1, "bf16", "bf16"), (5, "f16", "f32"), (96, "bf16", "f32"), (300, "f16", "f16")])
+def test_epilogues(M, x, y, gated, act):
+    _check(M, 136, 512, x, y, act, gated, bias=True, res=True)
+
+
+@pytest.mark.parametrize("M,out,inp", [(1, 1024, 3584), (4, 809, 4096), (200, 100, 4096), (1024, 1024, 1024),
+                                       (700, 1030, 640)])
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+def test_larger(M, out, inp, x):
+    _check(M, out, inp, x, res=True)
+
+
+@pytest.mark.parametrize("M", [1, 20, 300])
+def test_rows_with_a_common_offset(M):
+    """All activations near 3: the row's sum is 100 times its entries' spread."""
+    _check(M, 72, 512, y="f32", offset=3.0)
+
+
+@pytest.mark.parametrize("M", [1, 24, 200])
+def test_strided_rows_and_residual_in_place(M):
+    rng = np.random.default_rng(M)
+    out, inp = 72, 256
+    qw, sc = _weights(rng, out, inp)
+    xt, xn = t16(rng.standard_normal((M, inp + 64)), "bf16")
+    rt, rn = t16(rng.standard_normal((M, out + 9)), "bf16")
+    view, rest = rt[:, 5:5 + out], rt.clone()
+    cq.w4a16_linear(xt[:, 16:16 + inp], dev(qw), dev(sc.view(np.int16)), residual=view, out=view)
+    torch.cuda.synchronize()
+    want, tol = ref.w4a16_linear(xn[:, 16:16 + inp], qw, sc, None, rn[:, 5:5 + out])
+    close(view, want, tol)
+    assert torch.equal(rt[:, :5], rest[:, :5]) and torch.equal(rt[:, 5 + out:], rest[:, 5 + out:])
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_a_row_of_nan_or_infinity_stays_in_its_row(M):
+    rng = np.random.default_rng(M)
+    qw, sc = _weights(rng, 80, 256)
+    x = rng.standard_normal((M, 256))
+    x[1, 7], x[M - 1, 200] = np.nan, np.inf
+    xt, xn = t16(x, "bf16")
+    got = cq.w4a16_linear(xt, dev(qw), dev(sc.view(np.int16)))
+    torch.cuda.synchronize()
+    clean = [m for m in range(M) if m not in (1, M - 1)]
+    want, tol = ref.w4a16_linear(xn[clean], qw, sc)
+    close(got[clean], want, tol)
+    assert torch.isnan(got[1]).all()
+    codes = oracle.unpack_gptq_v1(qw, sc)[0][:, 200]
+    last = got[M - 1].float().cpu().numpy()
+    assert np.all(np.isnan(last[codes == 0])) and np.all(~np.isfinite(last))
+
+
+def test_memory_behind_the_last_row_and_column_is_left_alone():
+    rng = np.random.default_rng(9)
+    for M, out in ((1, 33), (17, 65), (130, 129), (300, 200)):
+        qw, sc = _weights(rng, out, 128)
+        xt, xn = t16(rng.standard_normal((M, 128)), "f16")
+        buf = torch.full((M + 140, out + 140), 5.0, dtype=torch.float32, device="cuda")
+        cq.w4a16_linear(xt, dev(qw), dev(sc.view(np.int16)), out=buf[:M, :out])
+        torch.cuda.synchronize()
+        close(buf[:M, :out], *ref.w4a16_linear(xn, qw, sc, out_type="f32"))
+        assert (buf[M:] == 5).all() and (buf[:M, out:] == 5).all()
+
+
+def test_repeated_calls_and_another_stream_give_the_same_bits():
+    rng = np.random.default_rng(4)
+    for M in (1, 100, 600):
+        qw, sc = (dev(a) for a in _weights(rng, 200, 1024))
+        xt, _ = t16(rng.standard_normal((M, 1024)), "bf16")
+        a = cq.w4a16_linear(xt, qw, sc.view(torch.int16), activation="gelu")
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        b = cq.w4a16_linear(xt, qw, sc.view(torch.int16), activation="gelu", stream=s)
+        s.synchronize()
+        assert torch.equal(a, b)
+
+
+def test_matches_the_consumer_check():
+    """cq_w4a16_matmul of the same tensors: both within their bounds of the definition, so within their sum."""
+    rng = np.random.default_rng(6)
+    qw, sc = _weights(rng, 96, 512)
+    xt, xn = t16(rng.standard_normal((50, 512)), "bf16")
+    a = cq.w4a16_matmul(xt, dev(qw), dev(sc.view(np.int16)))
+    b = cq.w4a16_linear(xt, dev(qw), dev(sc.view(np.int16)), out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    tol = ref.w4a16_linear(xn, qw, sc, out_type="f32")[1]
+    close(b, a.double().cpu().numpy(), 2 * tol)
+
+
+def test_replayed_graph():
+    rng = np.random.default_rng(8)
+    qw, sc = (dev(a) for a in _weights(rng, 256, 512))
+    sc = sc.view(torch.int16)
+    for M in (1, 300):
+        xt, _ = t16(rng.standard_normal((M, 512)), "f16")
+        out = torch.empty((M, 256), dtype=torch.float16, device="cuda")
+        cq.w4a16_linear(xt, qw, sc, out=out)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            cq.w4a16_linear(xt, qw, sc, out=out)
+        for k in range(4):
+            xt.copy_(t16(rng.standard_normal((M, 512)), "f16")[0])
+            eager = cq.w4a16_linear(xt, qw, sc)
+            out.zero_()
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, eager), (M, k)
+
+
+def test_refusals():
+    qw = torch.zeros((16, 8), dtype=torch.int32, device="cuda")
+    sc = torch.zeros((1, 8), dtype=torch.int16, device="cuda")
+    x = torch.zeros((2, 128), dtype=torch.bfloat16, device="cuda")
+    for kw in (dict(x=x.float()), dict(x=x[:, :64]), dict(qweight=qw[:8]), dict(scales=sc[:, :4]),
+               dict(bias=torch.zeros(7, dtype=x.dtype, device="cuda")), dict(bias=torch.zeros(8, device="cuda")),
+               dict(residual=torch.zeros((2, 8), dtype=torch.float16, device="cuda")), dict(activation="tanh"),
+               dict(out_dtype=torch.float16), dict(out=torch.zeros((2, 7), device="cuda")), dict(x=x.cpu()),
+               dict(x=x.t().contiguous().t())):
+        with pytest.raises(ValueError):
+            cq.w4a16_linear(**dict(dict(x=x, qweight=qw, scales=sc), **kw))
+    wide = torch.zeros((2, 140), dtype=torch.bfloat16, device="cuda")
+    for bad in (wide[:, 4:132], torch.zeros((2, 129), dtype=torch.bfloat16, device="cuda")[:, :128]):
+        with pytest.raises(cq.CQError):                       # rows not 16-byte aligned
+            cq.w4a16_linear(bad, qw, sc)
+    assert cq.w4a16_linear(x[:0], qw, sc).shape == (0, 8)
