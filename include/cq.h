@@ -448,7 +448,8 @@ int32_t cq_kv_cache_write(const void *k, int64_t k_token_stride, int64_t k_head_
  *   workspace         cq_paged_attention_workspace_size(...) bytes for the same sizes (none: may be
  *                     NULL).
  * q, k_cache, v_cache and out 16-byte aligned, all strides multiples of 8; head_dim a multiple of 8 up
- * to CQ_MAX_HEAD_DIM; heads a multiple of kv_heads; window > 0 needs causal; scale finite.
+ * to CQ_MAX_HEAD_DIM; heads a multiple of kv_heads; max_pages * page_size <= 2^30; window > 0 needs
+ * causal; scale finite.
  */
 #define CQ_MAX_HEAD_DIM 256
 typedef struct cq_paged_attention_args {

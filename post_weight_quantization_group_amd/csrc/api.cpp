@@ -453,7 +453,7 @@ int32_t cq_paged_attention(const cq_paged_attention_args* args, void* workspace,
     if (!attention_sizes_ok(p.n_tokens, p.n_requests, p.max_q, p.max_kv, p.heads, p.kv_heads, p.head_dim))
         return CQ_EINVAL;
     if (p.page_size < 1 || p.n_pages < 0 || p.max_pages < 0 || p.table_stride < p.max_pages) return CQ_EINVAL;
-    if ((int64_t)p.max_pages * p.page_size > INT32_MAX) return CQ_EINVAL;
+    if ((int64_t)p.max_pages * p.page_size > (int64_t)1 << 30) return CQ_EINVAL;
     if ((p.causal != 0 && p.causal != 1) || p.window < 0 || (p.window > 0 && !p.causal)) return CQ_EINVAL;
     if (!(p.scale - p.scale == 0.0f)) return CQ_EINVAL;
     if ((p.q_token_stride | p.q_head_stride | p.out_token_stride | p.out_head_stride | p.page_stride | p.head_stride |

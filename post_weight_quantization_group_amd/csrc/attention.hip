@@ -1,63 +1,778 @@
-// Attention of new tokens over a paged cache, the simple form: a wave per (token, head), its lanes
-// over the head's dimensions.
+// Attention of new tokens over a paged cache, for gfx950.
+//
+// Rows are the (token, query head) pairs of one request and one key/value head: row = token i times
+// G + head of the group, so that grouped heads fill a tile together and K and V are read once for
+// all of them.  One pass over the keys with the running maximum and sum of the softmax.
+//
+// Both products run on the matrix cores with the queries as columns:
+//        S^T [keys x rows] = K Q^T,        O^T [D x rows] += V^T P^T.
+// A lane then holds scores of one row only (its column), so the maximum and the sum need one or two
+// exchanges between lanes, and the scores' registers are the second product's B operand as they
+// stand: the order of the keys inside a contraction is free as long as V^T uses the same.  V^T comes
+// out of row-major V in LDS by the transposing read (ds_read_b64_tr_b16: lane 4 j + c of 16 addresses
+// row j, columns 4 c ..; lane i receives column i of the four rows).
+//
+// Lane layouts (checked on gfx950).  32x32x16: lane l holds A[l % 32][8 (l / 32) + e], B[8 (l / 32) +
+// e][l % 32], D[8 (r / 4) + 4 (l / 32) + r % 4][l % 32].  16x16x32: A[l % 16][8 (l / 16) + e], B
+// likewise, D[4 (l / 16) + r][l % 16].
+//
+// A masked key has weight 0, and 0 times an infinity or a NaN in V would be a NaN: keys that no row
+// of the tile sees are loaded as zeros, and where a tile's mask differs between its rows and its V
+// holds anything that is not finite, the product runs on V with those entries zeroed, and a second one
+// counts, per row and column, the infinities and NaNs among the keys that the row does see.
 #include "serve_args.h"
 #include "serve_math.h"
 
 namespace cqk {
 namespace {
 
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+
+constexpr float LN2 = 0.69314718f;
+
 template <bool F16>
-__global__ __launch_bounds__(64) void attention_kernel(AttentionArgs a) {
-    const int t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x;
-    int lo = 0, hi = a.R;  // the request with cu[r] <= t < cu[r + 1]
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu[mid + 1] > t) hi = mid;
-        else lo = mid + 1;
+__device__ __forceinline__ f32x16 mfma32(s16x8 a, s16x8 b, f32x16 c) {
+    if constexpr (F16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+template <bool F16>
+__device__ __forceinline__ f32x4 mfma16(s16x8 a, s16x8 b, f32x4 c) {
+    if constexpr (F16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+template <bool F16>
+__device__ __forceinline__ s16x8 pack8(const float* p) {
+    s16x8 v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (short)from_f32<F16>(p[e]);
+    return v;
+}
+
+template <bool F16>
+__device__ __forceinline__ bool not_finite(uint16_t b) {
+    constexpr uint16_t E = F16 ? 0x7C00 : 0x7F80;
+    return (b & E) == E;
+}
+template <bool F16>
+__device__ __forceinline__ bool any_not_finite(uint4 v) {
+    constexpr uint32_t E = F16 ? 0x7C00u : 0x7F80u;
+    bool bad = false;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= (w[i] & E) == E || (w[i] & (E << 16)) == (E << 16);
+    return bad;
+}
+
+// V with what is not finite as 0, and its counterpart: +inf as 1, -inf as 2^7, NaN as 2^14 (exact in
+// both types), 0 elsewhere.  A tile has at most 64 keys, so the sums of ones over the keys a row sees
+// separate into their counts.
+template <bool F16>
+__device__ __forceinline__ s16x8 finite_part(s16x8 v) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = not_finite<F16>((uint16_t)v[e]) ? (short)0 : v[e];
+    return v;
+}
+template <bool F16>
+__device__ __forceinline__ s16x8 special_part(s16x8 v) {
+    constexpr uint16_t INF = F16 ? 0x7C00 : 0x7F80;
+    const short one = (short)from_f32<F16>(1.0f), p7 = (short)from_f32<F16>(128.0f), p14 = (short)from_f32<F16>(16384.0f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint16_t b = (uint16_t)v[e];
+        v[e] = !not_finite<F16>(b) ? (short)0 : b == INF ? one : b == (INF | 0x8000) ? p7 : p14;
     }
-    const bool mine = lo < a.R && a.cu[lo] <= t;
-    float acc[4] = {0, 0, 0, 0}, q[4] = {0, 0, 0, 0}, m = -INFINITY, l = 0.0f;
-    for (int i = 0; i < 4; ++i)
-        if (lane + 64 * i < a.D) q[i] = to_f32<F16>(a.q[t * a.q_tok + h * a.q_head + lane + 64 * i]);
-    if (mine) {
-        const int n = a.cu[lo + 1] - a.cu[lo];
-        const int64_t room = (int64_t)a.max_pages * a.page;
-        const int64_t kv = a.kv_len[lo] < room ? a.kv_len[lo] : room;
-        const int64_t p = kv - n + (t - a.cu[lo]);
-        int64_t end = kv, begin = 0;
-        if (a.causal && p + 1 < end) end = p + 1;
-        if (a.window && p - a.window + 1 > begin) begin = p - a.window + 1;
-        for (int64_t j = begin; j < end; ++j) {
-            const int pg = a.table[lo * a.table_stride + j / a.page];
-            if (pg < 0 || pg >= a.n_pages) continue;
-            const int64_t at = pg * a.c_page + (h / (a.H / a.Hkv)) * a.c_head + j % a.page * a.c_row;
-            float s = 0.0f;
-            for (int i = 0; i < 4; ++i)
-                if (lane + 64 * i < a.D) s = __builtin_fmaf(q[i], to_f32<F16>(a.kc[at + lane + 64 * i]), s);
-            for (int x = 32; x; x >>= 1) s += __shfl_xor(s, x);
-            s *= a.scale;
-            const float top = fmaxf(m, s);
-            const float keep = __expf(m - top), e = __expf(s - top);
-            l = l * keep + e;
-            for (int i = 0; i < 4; ++i)
-                if (lane + 64 * i < a.D) acc[i] = acc[i] * keep + e * to_f32<F16>(a.vc[at + lane + 64 * i]);
-            m = top;
+    return v;
+}
+__device__ __forceinline__ float special_value(float count) {
+    const int n = (int)count;
+    if (n == 0) return 0.0f;
+    const bool pos = n & 127, neg = (n >> 7) & 127, nan = n >> 14;
+    return nan || (pos && neg) ? __builtin_nanf("") : pos ? INFINITY : -INFINITY;
+}
+
+// What the kernels need beside the arguments, worked out on the host.
+struct Plan {
+    float c;          // |scale| log2 e, at least 1e-37 (so that -inf times it stays -inf)
+    uint32_t flip;    // sign bits of a pair of 16-bit values where scale < 0: applied to q
+    uint32_t magic;   // n / page = (n * magic) >> shift for 0 <= n < 2^31
+    int shift;
+    int splits;       // parts that a row tile's keys are divided into, over workgroups
+    int rows_lo, rows_hi;  // this launch takes the requests with rows_lo < rows <= rows_hi
+    int64_t tiles;         // row tiles in the grid, per key/value head
+    int zero_rest;         // this launch writes the tokens that belong to no request
+};
+
+__device__ __forceinline__ int page_of(const Plan& p, int key) {
+    return (int)(((uint64_t)(uint32_t)key * p.magic) >> p.shift);
+}
+
+// Row tile `tile` of `bm` rows -> its request and its number in it: request r's tiles start at
+// floor(cu[r] G / bm) + r, which leaves room for ceil(n_r G / bm).  Returns false where there is none.
+__device__ __forceinline__ bool find_tile(const AttentionArgs& a, int64_t tile, int G, int bm, int& r, int& first) {
+    int lo = 0, hi = a.R - 1;  // the last request whose tiles start at or before `tile`
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int64_t)a.cu[mid] * G / bm + mid <= tile) lo = mid;
+        else hi = mid - 1;
+    }
+    r = lo;
+    first = (int)(tile - ((int64_t)a.cu[lo] * G / bm + lo)) * bm;
+    return first >= 0;
+}
+
+// One request's rows and keys, as a tile sees them.
+struct Rows {
+    int n, kv, pos0;  // new tokens (at most max_q), keys, position of token 0
+    int t0;           // its packed index
+    int key_begin, key_end;
+};
+__device__ __forceinline__ Rows rows_of(const AttentionArgs& a, int r, int first_row, int bm, int G) {
+    Rows w;
+    w.t0 = min(max(a.cu[r], 0), a.T);
+    const int all = min(max(a.cu[r + 1], w.t0), a.T) - w.t0;
+    const int64_t room = (int64_t)a.max_pages * a.page;
+    const int kv = a.kv_len[r] < 0 ? 0 : a.kv_len[r];
+    w.kv = kv < room ? kv : (int)room;
+    w.pos0 = w.kv - all;
+    w.n = all < a.max_q ? all : a.max_q;
+    const int last = min(w.n * G, first_row + bm) - 1;
+    w.key_end = w.kv;
+    w.key_begin = 0;
+    if (a.causal) w.key_end = min(w.kv, w.pos0 + last / G + 1);
+    if (a.window) w.key_begin = max(0, w.pos0 + first_row / G - a.window + 1);
+    return w;
+}
+
+// Tokens that belong to no request (before the first one's, behind the last one's) get zeros, from the
+// workgroups of the first row tile.
+template <bool F16>
+__device__ void zero_rest(const AttentionArgs& a, int kvh) {
+    const int G = a.H / a.Hkv;
+    const int begin = a.R > 0 ? a.cu[0] : a.T, end = a.R > 0 ? a.cu[a.R] : a.T;
+    for (int t = 0; t < a.T; ++t) {
+        if (t == begin) t = max(t, end);
+        if (t >= a.T) return;
+        for (int i = threadIdx.x; i < G * (a.D / 8); i += 256) {
+            const int h = kvh * G + i / (a.D / 8), d = i % (a.D / 8) * 8;
+            *reinterpret_cast<uint4*>(a.out + t * a.o_tok + (int64_t)h * a.o_head + d) = make_uint4(0, 0, 0, 0);
+            if (a.lse && d == 0) a.lse[(int64_t)t * a.H + h] = -INFINITY;
         }
     }
-    for (int i = 0; i < 4; ++i)
-        if (lane + 64 * i < a.D) a.out[t * a.o_tok + h * a.o_head + lane + 64 * i] = from_f32<F16>(l > 0.0f ? acc[i] / l : 0.0f);
-    if (a.lse && lane == 0) a.lse[(int64_t)t * a.H + h] = l > 0.0f ? m + __logf(l) : -INFINITY;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Few rows (generation): a workgroup takes 16 rows and one part of the keys; its four waves take tiles
+// of 32 keys in turn, each with its own running maximum, and join at the end.  Bound by reading K and V:
+// both go from memory to registers in pieces of 16 bytes a lane, the next tile's while this one is
+// worked on; V passes through the wave's own LDS to be transposed, so the waves never wait for each
+// other.
+template <bool F16, int DP>
+__global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl) {
+    constexpr int BM = 16, BN = 32, KS = DP / 32, DT = DP / 16;
+    constexpr int VS = DP + ((DP / 2) % 64 == 16 || (DP / 2) % 64 == 48 ? 0 : 32);  // rows 16 banks apart (mod 64)
+    constexpr int OS = DP + 4;
+    constexpr int WAVE_BYTES = BN * VS * 2 > BM * OS * 4 ? BN * VS * 2 : BM * OS * 4;
+    __shared__ __align__(16) uint8_t lds[4 * WAVE_BYTES];
+    __shared__ float wave_m[4][BM], wave_l[4][BM];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, quad = lane >> 4;
+    const int G = a.H / a.Hkv;
+    const int kvh = blockIdx.x % a.Hkv;
+    const int64_t tile = blockIdx.x / a.Hkv;
+    const int split = blockIdx.y;
+    if (pl.zero_rest && blockIdx.x < (unsigned)a.Hkv && split == 0) zero_rest<F16>(a, kvh);
+    if (a.R == 0) return;
+    int r, first;
+    if (!find_tile(a, tile, G, BM, r, first)) return;
+    const Rows w = rows_of(a, r, first, BM, G);
+    const int rows = w.n * G;
+    if (first >= rows || rows <= pl.rows_lo || rows > pl.rows_hi) return;
+
+    uint16_t* vl = reinterpret_cast<uint16_t*>(lds + wave * WAVE_BYTES);
+    const int row = first + col, tok = row / G, pos = w.pos0 + tok;
+    const bool live = row < rows;
+    // the keys this lane's row sees: [see_lo, see_hi)
+    const int see_hi = !live ? 0 : a.causal ? min(w.kv, pos + 1) : w.kv;
+    const int see_lo = a.window ? max(0, pos - a.window + 1) : 0;
+    const int same_hi = a.causal ? min(w.kv, w.pos0 + first / G + 1) : w.kv;  // every live row sees keys in
+    const int same_lo = a.window ? max(0, w.pos0 + min(rows - 1, first + BM - 1) / G - a.window + 1) : 0;  // [same_lo, same_hi)
+
+    s16x8 q[KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        const int d = 32 * ks + 8 * quad;
+        if (live && d < a.D) {
+            v = *reinterpret_cast<const uint4*>(a.q + (int64_t)(w.t0 + tok) * a.q_tok + (int64_t)(kvh * G + row % G) * a.q_head + d);
+            v.x ^= pl.flip; v.y ^= pl.flip; v.z ^= pl.flip; v.w ^= pl.flip;
+        }
+        q[ks] = __builtin_bit_cast(s16x8, v);
+    }
+
+    // this part's tiles of 32 keys
+    const int t_begin = w.key_begin / BN, t_end = (w.key_end + BN - 1) / BN;
+    const int per = max(0, (t_end - t_begin + pl.splits - 1) / pl.splits);
+    const int t0 = t_begin + split * per, t1 = min(t_end, t0 + per);
+    const int32_t* table = a.table + r * a.table_stride;
+
+    int page_id[2];
+    auto fetch_ids = [&](int t) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int key = t * BN + 16 * h + col;
+            page_id[h] = -1;
+            if (t < t1 && key >= w.key_begin && key < w.key_end) page_id[h] = table[page_of(pl, key)];
+        }
+    };
+    uint4 kr[2][KS], vr[2][KS];
+    int ok_next[2];
+    auto fetch_kv = [&](int t) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int key = t * BN + 16 * h + col;
+            ok_next[h] = page_id[h] >= 0 && page_id[h] < a.n_pages;
+            const int64_t at = page_id[h] * a.c_page + kvh * a.c_head + (int64_t)(key - page_of(pl, key) * a.page) * a.c_row + 8 * quad;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                kr[h][ks] = vr[h][ks] = make_uint4(0, 0, 0, 0);
+                if (ok_next[h] && 32 * ks + 8 * quad < a.D) {
+                    kr[h][ks] = *reinterpret_cast<const uint4*>(a.kc + at + 32 * ks);
+                    vr[h][ks] = *reinterpret_cast<const uint4*>(a.vc + at + 32 * ks);
+                }
+            }
+        }
+    };
+
+    f32x4 o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] = f32x4{0, 0, 0, 0};
+    float m = -INFINITY, l = 0.0f;
+
+    int t = t0 + wave;
+    fetch_ids(t);
+    fetch_kv(t);
+    fetch_ids(t + 4);
+    for (; t < t1; t += 4) {
+        f32x4 s[2];
+        bool bad = false;
+        const bool mixed = t * BN < same_lo || (t + 1) * BN > same_hi;
+        uint64_t there[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            s[h] = f32x4{0, 0, 0, 0};
+            there[h] = __ballot(ok_next[h]);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                s[h] = mfma16<F16>(__builtin_bit_cast(s16x8, kr[h][ks]), q[ks], s[h]);
+                *reinterpret_cast<uint4*>(vl + (16 * h + col) * VS + 32 * ks + 8 * quad) = vr[h][ks];
+                if (mixed) bad |= any_not_finite<F16>(vr[h][ks]);
+            }
+        }
+        const bool special = mixed && __any(bad);
+        fetch_kv(t + 4);
+        fetch_ids(t + 8);
+        // masks, running maximum
+        float top = -INFINITY;
+        const bool all_there = (there[0] & there[1] & 0xffff) == 0xffff;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (mixed || !all_there) {
+                    const int k = 4 * quad + e, key = t * BN + 16 * h + k;
+                    if (key < see_lo || key >= see_hi || !((there[h] >> k) & 1)) s[h][e] = -INFINITY;
+                }
+                top = fmaxf(top, s[h][e]);
+            }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float m_new = fmaxf(m, top);
+        const float mc = m_new == -INFINITY ? 0.0f : m_new * pl.c;
+        if (__any(m_new > m)) {
+            const float keep = __builtin_amdgcn_exp2f(__builtin_fmaf(m, pl.c, -mc));
+            l *= keep;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[d][e] *= keep;
+            m = m_new;
+        }
+        float p[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                p[4 * h + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][e], pl.c, -mc));
+                l += p[4 * h + e];
+            }
+        const s16x8 pb = pack8<F16>(p);
+        // O^T += V^T P^T: keys in the order 16 h + 4 quad + e
+        const uint16_t* va = vl + (4 * quad + (col >> 2)) * VS + 4 * (col & 3);
+        if (!special) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + 16 * d));
+                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + 16 * VS + 16 * d));
+                o[d] = mfma16<F16>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), pb, o[d]);
+            }
+        } else {
+            float ones[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ones[e] = p[e] == 0.0f ? 0.0f : 1.0f;
+            const s16x8 seen = pack8<F16>(ones);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + 16 * d));
+                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + 16 * VS + 16 * d));
+                const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                o[d] = mfma16<F16>(finite_part<F16>(v), pb, o[d]);
+                const f32x4 n = mfma16<F16>(special_part<F16>(v), seen, f32x4{0, 0, 0, 0});
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[d][e] += special_value(n[e]);
+            }
+        }
+    }
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+
+    // join the four waves
+    float* ol = reinterpret_cast<float*>(lds + wave * WAVE_BYTES);
+    __syncthreads();
+    if (quad == 0) {
+        wave_m[wave][col] = m;
+        wave_l[wave][col] = l;
+    }
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ol[col * OS + 16 * d + 4 * quad + e] = o[d][e];
+    __syncthreads();
+    const int live_rows = min(BM, rows - first);
+    const int64_t part = (tile * a.Hkv + kvh) * pl.splits + split;
+    for (int i = tid; i < live_rows * (DP / 4); i += 256) {
+        const int c = i / (DP / 4), d = i % (DP / 4) * 4;
+        float M = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) M = fmaxf(M, wave_m[x][c]);
+        const float Mc = M == -INFINITY ? 0.0f : M * pl.c;
+        float L = 0.0f;
+        f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(wave_m[x][c], pl.c, -Mc));
+            if (wave_m[x][c] == -INFINITY && !(wave_l[x][c] != wave_l[x][c])) continue;  // this wave saw no key of the row
+            L = __builtin_fmaf(f, wave_l[x][c], L);
+            const f32x4 v = *reinterpret_cast<const f32x4*>(lds + x * WAVE_BYTES + (c * OS + d) * 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(f, v[e], acc[e]);
+        }
+        if (pl.splits > 1) {
+            float* wp = a.ws + part * (BM * (DP + 2));
+            *reinterpret_cast<f32x4*>(wp + c * DP + d) = acc;
+            if (d == 0) {
+                wp[BM * DP + 2 * c] = M * pl.c;
+                wp[BM * DP + 2 * c + 1] = L;
+            }
+        } else {
+            const int rw = first + c;
+            const int64_t tk = w.t0 + rw / G;
+            const int head = kvh * G + rw % G;
+            const bool none = L == 0.0f;
+            if (d < a.D) {
+                uint16_t b[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) b[e] = from_f32<F16>(none ? 0.0f : acc[e] / L);
+                uint2 st = make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
+                *reinterpret_cast<uint2*>(a.out + tk * a.o_tok + (int64_t)head * a.o_head + d) = st;
+            }
+            if (a.lse && d == 0) a.lse[tk * a.H + head] = none ? -INFINITY : (M * pl.c + __log2f(L)) * LN2;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Many rows (prompts): a workgroup takes 128 rows, 32 per wave, and stages tiles of BN keys and
+// values in LDS for all four waves; the next tile is on its way into registers meanwhile.
+template <bool F16, int DP, int BN>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(AttentionArgs a, Plan pl) {
+    constexpr int BM = 128, KS = DP / 16, DT = DP / 32, KT = BN / 32;
+    constexpr int KST = DP + 8;  // rows 4 banks apart
+    constexpr int VS = DP + ((DP / 2) % 64 == 16 || (DP / 2) % 64 == 48 ? 0 : 32);
+    constexpr int PIECES = BN * DP / 8 / 256;  // 16-byte pieces of a tile per thread
+    constexpr int PER_ROW = DP / 8;
+    __shared__ __align__(16) uint16_t kl[BN * KST];
+    __shared__ __align__(16) uint16_t vl[BN * VS];
+    __shared__ int bad_tile[2];
+    __shared__ uint32_t missing_lds[2][KT];  // keys in range whose page is not in the pool
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, half = lane >> 5;
+    const int G = a.H / a.Hkv;
+    const int kvh = blockIdx.x % a.Hkv;
+    const int64_t tile = pl.tiles - 1 - blockIdx.x / a.Hkv;  // the longest rows first
+    const int split = blockIdx.y;
+    if (pl.zero_rest && blockIdx.x < (unsigned)a.Hkv && split == 0) zero_rest<F16>(a, kvh);
+    if (a.R == 0) return;
+    int r, first;
+    if (!find_tile(a, tile, G, BM, r, first)) return;
+    const Rows w = rows_of(a, r, first, BM, G);
+    const int rows = w.n * G;
+    if (first >= rows || rows <= pl.rows_lo || rows > pl.rows_hi) return;
+
+    const int row = first + 32 * wave + col, tok = row / G, pos = w.pos0 + tok;
+    const bool live = row < rows;
+    const int see_hi = !live ? 0 : a.causal ? min(w.kv, pos + 1) : w.kv;
+    const int see_lo = a.window ? max(0, pos - a.window + 1) : 0;
+    // keys that every row of the workgroup sees, and that every (any) row of the wave sees
+    const int last = min(rows, first + BM) - 1;
+    const int same_hi = a.causal ? min(w.kv, w.pos0 + first / G + 1) : w.kv;
+    const int same_lo = a.window ? max(0, w.pos0 + last / G - a.window + 1) : 0;
+    const int wfirst = first + 32 * wave, wlast = min(rows - 1, wfirst + 31);
+    const int wave_hi = wfirst >= rows ? 0 : a.causal ? min(w.kv, w.pos0 + wlast / G + 1) : w.kv;
+    const int wave_lo = a.window ? max(0, w.pos0 + wfirst / G - a.window + 1) : 0;
+    const int wsame_hi = a.causal ? min(w.kv, w.pos0 + wfirst / G + 1) : w.kv;
+    const int wsame_lo = a.window ? max(0, w.pos0 + wlast / G - a.window + 1) : 0;
+
+    s16x8 q[KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        const int d = 16 * ks + 8 * half;
+        if (live && d < a.D) {
+            v = *reinterpret_cast<const uint4*>(a.q + (int64_t)(w.t0 + tok) * a.q_tok + (int64_t)(kvh * G + row % G) * a.q_head + d);
+            v.x ^= pl.flip; v.y ^= pl.flip; v.z ^= pl.flip; v.w ^= pl.flip;
+        }
+        q[ks] = __builtin_bit_cast(s16x8, v);
+    }
+
+    const int t_begin = w.key_begin / BN, t_end = (w.key_end + BN - 1) / BN;
+    const int per = max(0, (t_end - t_begin + pl.splits - 1) / pl.splits);
+    const int t0 = t_begin + split * per, t1 = min(t_end, t0 + per);
+    const int32_t* table = a.table + r * a.table_stride;
+
+    int page_id[PIECES];
+    auto fetch_ids = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int key = t * BN + (tid + 256 * i) / PER_ROW;
+            page_id[i] = -1;
+            if (t < t1 && key >= w.key_begin && key < w.key_end) page_id[i] = table[page_of(pl, key)];
+        }
+    };
+    uint4 kr[PIECES], vr[PIECES];
+    bool ok[PIECES];
+    auto fetch_kv = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int j = (tid + 256 * i) / PER_ROW, d = (tid + 256 * i) % PER_ROW * 8, key = t * BN + j;
+            ok[i] = page_id[i] >= 0 && page_id[i] < a.n_pages;
+            kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+            if (ok[i] && d < a.D) {
+                const int64_t at = page_id[i] * a.c_page + kvh * a.c_head + (int64_t)(key - page_of(pl, key) * a.page) * a.c_row + d;
+                kr[i] = *reinterpret_cast<const uint4*>(a.kc + at);
+                vr[i] = *reinterpret_cast<const uint4*>(a.vc + at);
+            }
+        }
+    };
+
+    f32x16 o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
+    float m = -INFINITY, l = 0.0f;
+
+    if (tid < 2) bad_tile[tid] = 0;
+    if (tid < 2 * KT) missing_lds[tid / KT][tid % KT] = 0;
+    fetch_ids(t0);
+    fetch_kv(t0);
+    fetch_ids(t0 + 1);
+    for (int t = t0; t < t1; ++t) {
+        const int par = t & 1;
+        const bool mixed = t * BN < same_lo || (t + 1) * BN > same_hi;
+        __syncthreads();  // the previous tile has been read
+        {
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                const int j = (tid + 256 * i) / PER_ROW, d = (tid + 256 * i) % PER_ROW * 8;
+                *reinterpret_cast<uint4*>(kl + j * KST + d) = kr[i];
+                *reinterpret_cast<uint4*>(vl + j * VS + d) = vr[i];
+                if (mixed) bad |= any_not_finite<F16>(vr[i]);
+                if (d == 0 && !ok[i] && t * BN + j >= w.key_begin && t * BN + j < w.key_end)
+                    atomicOr(&missing_lds[par][j / 32], 1u << (j % 32));
+            }
+            if (mixed && bad) bad_tile[par] = 1;
+        }
+        __syncthreads();
+        fetch_kv(t + 1);
+        fetch_ids(t + 2);
+        const bool special = mixed && bad_tile[par];
+        uint32_t missing[KT];
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) missing[kt] = missing_lds[par][kt];
+        if (tid == 0) bad_tile[par ^ 1] = 0;
+        if (tid < KT) missing_lds[par ^ 1][tid] = 0;
+        if (t * BN >= wave_hi || (t + 1) * BN <= wave_lo) continue;  // no row of this wave sees the tile
+
+        f32x16 s[KT];
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[kt][e] = 0.0f;
+            const uint16_t* ka = kl + (32 * kt + col) * KST + 8 * half;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+                s[kt] = mfma32<F16>(*reinterpret_cast<const s16x8*>(ka + 16 * ks), q[ks], s[kt]);
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+            if (t * BN < wsame_lo || (t + 1) * BN > wsame_hi || missing[kt]) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int k = 8 * (e >> 2) + 4 * half + (e & 3), key = t * BN + 32 * kt + k;
+                    if (key < see_lo || key >= see_hi || ((missing[kt] >> k) & 1)) s[kt][e] = -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, s[kt][e]);
+        }
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float m_new = fmaxf(m, top);
+        const float mc = m_new == -INFINITY ? 0.0f : m_new * pl.c;
+        if (__any(m_new > m)) {
+            const float keep = __builtin_amdgcn_exp2f(__builtin_fmaf(m, pl.c, -mc));
+            l *= keep;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[d][e] *= keep;
+            m = m_new;
+        }
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                s[kt][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][e], pl.c, -mc));
+                l += s[kt][e];
+            }
+        }
+        const uint16_t* va = vl + (4 * half + ((lane & 15) >> 2)) * VS + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+#pragma unroll
+        for (int ss = 0; ss < BN / 16; ++ss) {
+            float p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = s[ss / 2][8 * (ss % 2) + e];
+            const s16x8 pb = pack8<F16>(p);
+            if (!special) {
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + (16 * ss) * VS + 32 * d));
+                    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + (16 * ss + 8) * VS + 32 * d));
+                    o[d] = mfma32<F16>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), pb, o[d]);
+                }
+            } else {
+                float ones[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ones[e] = p[e] == 0.0f ? 0.0f : 1.0f;
+                const s16x8 seen = pack8<F16>(ones);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + (16 * ss) * VS + 32 * d));
+                    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + (16 * ss + 8) * VS + 32 * d));
+                    const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                    o[d] = mfma32<F16>(finite_part<F16>(v), pb, o[d]);
+                    f32x16 n;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) n[e] = 0.0f;
+                    n = mfma32<F16>(special_part<F16>(v), seen, n);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[d][e] += special_value(n[e]);
+                }
+            }
+        }
+    }
+    l += __shfl_xor(l, 32);
+    if (pl.splits > 1) {
+        float* wp = a.ws + ((tile * a.Hkv + kvh) * pl.splits + split) * (BM * (DP + 2));
+        const int c = 32 * wave + col;
+        if (live) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                    *reinterpret_cast<f32x4*>(wp + c * DP + 32 * d + 2 * e + 4 * half) =
+                        f32x4{o[d][e], o[d][e + 1], o[d][e + 2], o[d][e + 3]};
+            if (half == 0) {
+                wp[BM * DP + 2 * c] = m * pl.c;
+                wp[BM * DP + 2 * c + 1] = l;
+            }
+        }
+        return;
+    }
+    if (live) {
+        const bool none = l == 0.0f;
+        const int head = kvh * G + row % G;
+        uint16_t* out = a.out + (int64_t)(w.t0 + tok) * a.o_tok + (int64_t)head * a.o_head;
+        const float inv = none ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const int dd = 32 * d + 2 * e + 4 * half;
+                if (dd < a.D) {
+                    uint16_t b[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) b[x] = from_f32<F16>(none ? 0.0f : o[d][e + x] * inv);
+                    *reinterpret_cast<uint2*>(out + dd) = make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
+                }
+            }
+        if (a.lse && half == 0) a.lse[(int64_t)(w.t0 + tok) * a.H + head] = none ? -INFINITY : (m * pl.c + __log2f(l)) * LN2;
+    }
+}
+
+// Joins the parts of a row tile: a wave per row.
+template <bool F16, int DP, int BM>
+__global__ __launch_bounds__(256) void join_kernel(AttentionArgs a, Plan pl) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int G = a.H / a.Hkv;
+    const int64_t wg = blockIdx.x;
+    const int c = (int)(wg % (BM / 4)) * 4 + wave;
+    const int kvh = (int)(wg / (BM / 4) % a.Hkv);
+    const int64_t tile = wg / (BM / 4) / a.Hkv;
+    int r, first;
+    if (!find_tile(a, tile, G, BM, r, first)) return;
+    const Rows w = rows_of(a, r, first, BM, G);
+    const int rows = w.n * G, row = first + c;
+    if (row >= rows || rows <= pl.rows_lo || rows > pl.rows_hi) return;
+    const float* wp = a.ws + (tile * a.Hkv + kvh) * pl.splits * (BM * (DP + 2));
+    float M = -INFINITY;
+    for (int s = 0; s < pl.splits; ++s) M = fmaxf(M, wp[s * (BM * (DP + 2)) + BM * DP + 2 * c]);
+    const float Mc = M == -INFINITY ? 0.0f : M;
+    float L = 0.0f, acc[DP / 64 + 1];
+#pragma unroll
+    for (int i = 0; i <= DP / 64; ++i) acc[i] = 0.0f;
+    for (int s = 0; s < pl.splits; ++s) {
+        const float* part = wp + s * (BM * (DP + 2));
+        const float ms = part[BM * DP + 2 * c], ls = part[BM * DP + 2 * c + 1];
+        if (ms == -INFINITY && !(ls != ls)) continue;
+        const float f = __builtin_amdgcn_exp2f(ms - Mc);
+        L = __builtin_fmaf(f, ls, L);
+#pragma unroll
+        for (int i = 0; i <= (DP - 1) / 64; ++i)
+            if (lane + 64 * i < DP) acc[i] = __builtin_fmaf(f, part[c * DP + lane + 64 * i], acc[i]);
+    }
+    const bool none = L == 0.0f;
+    const int64_t tk = w.t0 + row / G;
+    const int head = kvh * G + row % G;
+#pragma unroll
+    for (int i = 0; i <= (DP - 1) / 64; ++i)
+        if (lane + 64 * i < a.D)
+            a.out[tk * a.o_tok + (int64_t)head * a.o_head + lane + 64 * i] = from_f32<F16>(none ? 0.0f : acc[i] / L);
+    if (a.lse && lane == 0) a.lse[tk * a.H + head] = none ? -INFINITY : (M + __log2f(L)) * LN2;
+}
+
+
+// ---------------------------------------------------------------------------------------------
+constexpr int FEW = 64;  // requests of at most so many rows go to few_rows_kernel
+
+struct Parts {
+    int64_t few_tiles, many_tiles;
+    int few_splits, many_splits;  // 0: not launched
+};
+
+int padded_dim(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : D <= 192 ? 192 : 256; }
+
+int splits_for(int64_t groups, int64_t want, int max_kv, int least_keys) {
+    int64_t s = groups < 1 ? 1 : want / groups, most = max_kv / least_keys;
+    if (s > most) s = most;
+    return s < 1 ? 1 : s > 256 ? 256 : (int)s;
+}
+
+Parts divide(int R, int T, int max_q, int max_kv, int H, int Hkv) {
+    const int64_t G = H / Hkv, rows = max_q * G;
+    Parts p{};
+    p.few_tiles = T * G / 16 + R + 1;
+    p.many_tiles = T * G / 128 + R + 1;
+    if (rows <= FEW || (int64_t)R * max_q != T) {
+        const int64_t per = (rows < FEW ? rows + 15 : FEW) / 16;
+        p.few_splits = splits_for(R * per * Hkv, 768, max_kv, 128);
+    }
+    if (rows > FEW) {
+        const int64_t most = R * ((rows + 127) / 128);
+        p.many_splits = splits_for((most < p.many_tiles ? most : p.many_tiles) * Hkv, 512, max_kv, 512);
+    }
+    return p;
+}
+
+template <bool F16, int DP>
+hipError_t launch_dim(const AttentionArgs& a, Plan pl, const Parts& p, hipStream_t st) {
+    pl.zero_rest = 1;
+    if (p.few_splits) {
+        pl.splits = p.few_splits;
+        pl.rows_lo = 0;
+        pl.rows_hi = p.many_splits ? FEW : INT32_MAX;
+        pl.tiles = p.few_tiles;
+        hipLaunchKernelGGL((few_rows_kernel<F16, DP>), dim3((unsigned)(p.few_tiles * a.Hkv), p.few_splits), dim3(256), 0,
+                           st, a, pl);
+        if (p.few_splits > 1)
+            hipLaunchKernelGGL((join_kernel<F16, DP, 16>), dim3((unsigned)(p.few_tiles * a.Hkv * 4)), dim3(256), 0, st, a, pl);
+        pl.zero_rest = 0;
+    }
+    if (p.many_splits) {
+        pl.splits = p.many_splits;
+        pl.rows_lo = p.few_splits ? FEW : 0;
+        pl.rows_hi = INT32_MAX;
+        pl.tiles = p.many_tiles;
+        hipLaunchKernelGGL((many_rows_kernel<F16, DP, (DP <= 128 ? 64 : 32)>),
+                           dim3((unsigned)(p.many_tiles * a.Hkv), p.many_splits), dim3(256), 0, st, a, pl);
+        if (p.many_splits > 1)
+            hipLaunchKernelGGL((join_kernel<F16, DP, 128>), dim3((unsigned)(p.many_tiles * a.Hkv * 32)), dim3(256), 0, st, a,
+                               pl);
+    }
+    return hipGetLastError();
+}
+
+template <bool F16>
+hipError_t launch_type(const AttentionArgs& a, const Plan& pl, const Parts& p, hipStream_t st) {
+    switch (padded_dim(a.D)) {
+        case 64: return launch_dim<F16, 64>(a, pl, p, st);
+        case 96: return launch_dim<F16, 96>(a, pl, p, st);
+        case 128: return launch_dim<F16, 128>(a, pl, p, st);
+        case 192: return launch_dim<F16, 192>(a, pl, p, st);
+        default: return launch_dim<F16, 256>(a, pl, p, st);
+    }
 }
 
 }  // namespace
 
-int64_t attention_ws(int32_t, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
+int64_t attention_ws(int32_t R, int32_t T, int32_t max_q, int32_t max_kv, int32_t H, int32_t Hkv, int32_t D) {
+    const Parts p = divide(R, T, max_q, max_kv, H, Hkv);
+    const int64_t row = padded_dim(D) + 2;
+    const int64_t few = p.few_splits > 1 ? p.few_tiles * Hkv * p.few_splits * 16 * row : 0;
+    const int64_t many = p.many_splits > 1 ? p.many_tiles * Hkv * p.many_splits * 128 * row : 0;
+    return few > many ? few : many;
+}
 
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t st) {
-    const dim3 grid((unsigned)a.T, (unsigned)a.H);
-    if (a.f16) hipLaunchKernelGGL(attention_kernel<true>, grid, dim3(64), 0, st, a);
-    else hipLaunchKernelGGL(attention_kernel<false>, grid, dim3(64), 0, st, a);
-    return hipGetLastError();
+    Plan pl{};
+    pl.c = fmaxf(fabsf(a.scale) * 1.44269504f, 1e-37f);
+    pl.flip = a.scale < 0.0f ? 0x80008000u : 0u;
+    int bits = 0;
+    while (((int64_t)1 << bits) < a.page) ++bits;
+    pl.magic = (uint32_t)((((uint64_t)1 << (31 + bits)) + a.page - 1) / a.page);
+    pl.shift = 31 + bits;
+    const Parts p = divide(a.R, a.T, a.max_q, a.max_kv, a.H, a.Hkv);
+    return a.f16 ? launch_type<true>(a, pl, p, st) : launch_type<false>(a, pl, p, st);
 }
 
 }  // namespace cqk
