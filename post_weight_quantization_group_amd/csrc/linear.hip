@@ -1,46 +1,427 @@
-// Linear layer over GPTQ-v1 tensors with its epilogue, the simple form: a thread per output.
+// Linear layer over GPTQ-v1 tensors with its epilogue, for gfx950:
+//
+//   z[m][c] = sum_g s[g][c] sum_{k in g} x[m][k] (u[k][c] - 8),    y = act(z + b) [* (z' + b')] + r.
+//
+// The products run on the matrix cores, in x's own 16-bit type: the codes u - 8 are exact in both,
+// so are their products with x in fp32, and the sums are fp32.  A qweight word holds eight
+// consecutive k of one column, which is what one lane of the B operand takes: words go from memory to
+// registers and are dequantized there, never through LDS.
+//
+// Lane layouts (checked on gfx950).  16x16x32: lane l holds A[l % 16][8 (l / 16) + e], B[8 (l / 16) +
+// e][l % 16], D[4 (l / 16) + r][l % 16].  32x32x16: A[l % 32][8 (l / 32) + e], B likewise,
+// D[8 (r / 4) + 4 (l / 32) + r % 4][l % 32].
 #include "serve_args.h"
 #include "serve_math.h"
 
 namespace cqk {
 namespace {
 
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
 template <bool F16>
-__device__ float column(const LinearArgs& a, int64_t m, int64_t o, int64_t cols) {
-    float z = 0.0f;
-    for (int64_t g = 0; g < a.in / 128; ++g) {
-        float part = 0.0f;
-        for (int r = 0; r < 16; ++r) {
-            const uint32_t w = (uint32_t)a.qw[(g * 16 + r) * cols + o];
-            const uint16_t* xr = a.x + m * a.ldx + g * 128 + r * 8;
-            for (int j = 0; j < 8; ++j)
-                part = __builtin_fmaf(to_f32<F16>(xr[j]), (float)((int)((w >> (4 * j)) & 15) - 8), part);
-        }
-        z = __builtin_fmaf(to_f32<true>(a.scales[g * cols + o]), part, z);
+__device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
+    if constexpr (F16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+template <bool F16>
+__device__ __forceinline__ f32x16 mfma32(uint4 a, uint4 b, f32x16 c) {
+    if constexpr (F16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// The eight codes of a word as 16 (u - 8) in the 16-bit type: u XOR 8 is u - 8 as a signed 4-bit
+// field, which in the upper half of a byte reads as 16 times its value, converted by one
+// instruction per code (a byte's conversion with sign extension); exact in both types, and the 1/16
+// goes into the group's scale.  15 instructions a word against 21 with the fields shifted down.
+constexpr float CODE_UNIT = 1.0f / 16.0f;
+template <bool F16>
+__device__ __forceinline__ uint4 codes(uint32_t word) {
+    const uint32_t v = word ^ 0x88888888u;
+    const uint32_t even = (v << 4) & 0xF0F0F0F0u, odd = v & 0xF0F0F0F0u;
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float lo = (float)(int8_t)(even >> (8 * j)), hi = (float)(int8_t)(odd >> (8 * j));
+        if constexpr (F16)
+            h[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(lo, hi));
+        else
+            h[j] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
     }
+    return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+__device__ __forceinline__ float scale_of(uint16_t bits) { return (float)__builtin_bit_cast(_Float16, bits); }
+
+// act(z + b) [* (z' + b')] + r of output (m, o) and its store.
+template <bool F16>
+__device__ __forceinline__ void finish(const LinearArgs& a, int64_t m, int64_t o, float z, float up) {
     if (a.bias) z += to_f32<F16>(a.bias[o]);
-    return z;
+    z = activate(a.act, z);
+    if (a.gated) {
+        if (a.bias) up += to_f32<F16>(a.bias[a.out + o]);
+        z *= up;
+    }
+    if (a.residual) z += to_f32<F16>(a.residual[m * a.ldr + o]);
+    if (a.y_f32) reinterpret_cast<float*>(a.y)[m * a.ldy + o] = z;
+    else reinterpret_cast<uint16_t*>(a.y)[m * a.ldy + o] = from_f32<F16>(z);
+}
+
+// Whether four neighbouring outputs from a multiple of 4 on can be moved at once.
+__device__ __forceinline__ bool outputs_in_fours(const LinearArgs& a) {
+    bool ok = a.out % 4 == 0 && a.ldy % 4 == 0 && ((uintptr_t)a.y & (a.y_f32 ? 15 : 7)) == 0;
+    if (a.residual) ok = ok && a.ldr % 4 == 0 && ((uintptr_t)a.residual & 7) == 0;
+    if (a.bias) ok = ok && ((uintptr_t)a.bias & 7) == 0;
+    return ok;
 }
 
 template <bool F16>
-__global__ __launch_bounds__(256) void linear_kernel(LinearArgs a) {
-    const int64_t o = (int64_t)blockIdx.y * 64 + (threadIdx.x & 63), m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (o >= a.out || m >= a.M) return;
+__device__ __forceinline__ f32x4 four(const uint16_t* p) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    return f32x4{to_f32<F16>((uint16_t)v.x), to_f32<F16>((uint16_t)(v.x >> 16)), to_f32<F16>((uint16_t)v.y),
+                 to_f32<F16>((uint16_t)(v.y >> 16))};
+}
+
+// finish() of the outputs (m, o .. o + 3) that exist.
+template <bool F16>
+__device__ __forceinline__ void finish4(const LinearArgs& a, int64_t m, int64_t o, f32x4 z, f32x4 up, bool wide) {
+    if (m >= a.M || o >= a.out) return;
+    if (!wide) {
+        for (int e = 0; e < 4; ++e)
+            if (o + e < a.out) finish<F16>(a, m, o + e, z[0], up[0]), z = z.yzwx, up = up.yzwx;
+        return;
+    }
+    if (a.bias) {
+        z += four<F16>(a.bias + o);
+        if (a.gated) up += four<F16>(a.bias + a.out + o);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] = activate(a.act, z[e]);
+    if (a.gated) z *= up;
+    if (a.residual) z += four<F16>(a.residual + m * a.ldr + o);
+    if (a.y_f32) {
+        *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.y) + m * a.ldy + o) = z;
+    } else {
+        uint32_t b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] = from_f32<F16>(z[e]);
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.y) + m * a.ldy + o) =
+            make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Few rows, or few tiles: a workgroup takes 16 MT rows and 4 x 16 columns (gated: 2 x 16 of the gate and
+// the same of the other half), its W waves every W-th group, and their sums join in LDS in the order
+// of the waves.  For one row the weights' words are all there is to read, and each lane reads 16
+// bytes of them at a time (VEC); x comes straight from memory, no wave needs another's.
+template <bool F16, int MT, int W, bool VEC>
+__global__ __launch_bounds__(64 * W) void few_rows_linear(LinearArgs a, int col_tiles) {
+    __shared__ __align__(16) float sums[W * MT * 16 * 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, quad = lane >> 4;
+    const int64_t ct = blockIdx.x % col_tiles, rt = blockIdx.x / col_tiles;
     const int64_t cols = a.gated ? 2 * a.out : a.out;
-    float z = activate(a.act, column<F16>(a, m, o, cols));
-    if (a.gated) z *= column<F16>(a, m, o + a.out, cols);
-    if (a.residual) z += to_f32<F16>(a.residual[m * a.ldr + o]);
-    if (a.y_f32) ((float*)a.y)[m * a.ldy + o] = z;
-    else ((uint16_t*)a.y)[m * a.ldy + o] = from_f32<F16>(z);
+    const int per = a.gated ? 32 : 64;  // outputs per workgroup
+    const int64_t n0 = ct * per, m0 = rt * (16 * MT);
+    // slot t of lane column `col` is output n0 + local[t] of column half[t]
+    int64_t c[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int64_t o = n0 + (VEC ? (a.gated ? 2 * col + (t & 1) : 4 * col + t) : col + 16 * (a.gated ? t & 1 : t));
+        c[t] = (o < a.out ? o : a.out - 1) + (a.gated && t >= 2 ? a.out : 0);
+        // (past the edge: any column in range; VEC loads whole runs of 4 or 2, which end together with it)
+    }
+    if (VEC) {
+        const int run = a.gated ? 2 : 4;
+        if (n0 + run * col >= a.out) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) c[t] = (a.out - run) + (t & (run - 1)) + (a.gated && t >= 2 ? a.out : 0);
+        }
+    }
+    const uint16_t* xrow[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int64_t m = m0 + 16 * i + col;
+        xrow[i] = a.x + (m < a.M ? m : a.M - 1) * a.ldx + 8 * quad;
+    }
+    const int groups = (int)(a.in / 128);
+    uint32_t wr[4][4];  // [k step][slot]
+    uint4 xr[MT][4];
+    float sc[4];
+    auto fetch = [&](int g) {
+        if (g >= groups) return;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            const int32_t* q = a.qw + ((int64_t)g * 16 + 4 * ks + quad) * cols;
+            if (VEC && !a.gated) {
+                const uint4 v = *reinterpret_cast<const uint4*>(q + c[0]);
+                wr[ks][0] = v.x; wr[ks][1] = v.y; wr[ks][2] = v.z; wr[ks][3] = v.w;
+            } else if (VEC) {
+                const uint2 v = *reinterpret_cast<const uint2*>(q + c[0]), u = *reinterpret_cast<const uint2*>(q + c[2]);
+                wr[ks][0] = v.x; wr[ks][1] = v.y; wr[ks][2] = u.x; wr[ks][3] = u.y;
+            } else {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) wr[ks][t] = (uint32_t)q[c[t]];
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) xr[i][ks] = *reinterpret_cast<const uint4*>(xrow[i] + (int64_t)g * 128 + 32 * ks);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) sc[t] = scale_of(a.scales[(int64_t)g * cols + c[t]]) * CODE_UNIT;
+    };
+    f32x4 acc[MT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
+    fetch(wave);
+    for (int g = wave; g < groups; g += W) {
+        f32x4 part[MT][4];
+        float s[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            s[t] = sc[t];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) part[i][t] = f32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const uint4 b = codes<F16>(wr[ks][t]);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) part[i][t] = mfma16<F16>(xr[i][ks], b, part[i][t]);
+            }
+        fetch(g + W);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][t][e] = __builtin_fmaf(s[t], part[i][t][e], acc[i][t][e]);
+    }
+    // sums[wave][row][slot * 16 + col]
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sums[((wave * MT + i) * 16 + 4 * quad + e) * 64 + 16 * t + col] = acc[i][t][e];
+    __syncthreads();
+    for (int i = tid; i < MT * 16 * per; i += 64 * W) {
+        const int row = i / per, n = i % per;
+        const int64_t m = m0 + row, o = n0 + n;
+        if (m >= a.M || o >= a.out) continue;
+        int at;  // where output n of the tile lies among the 64 slots
+        if (!VEC) at = n;
+        else if (a.gated) at = 16 * (n & 1) + n / 2;
+        else at = 16 * (n & 3) + n / 4;
+        float z = 0.0f, up = 0.0f;
+#pragma unroll
+        for (int x = 0; x < W; ++x) {
+            z += sums[(x * MT * 16 + row) * 64 + at];
+            if (a.gated) up += sums[(x * MT * 16 + row) * 64 + 32 + at];
+        }
+        finish<F16>(a, m, o, z, up);
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Many rows: a workgroup takes 128 rows and 256 columns (gated: 128 of either half), each of its four
+// waves all rows and 64 columns, as 4 x 2 tiles of 32 x 32.  x goes through LDS once for all waves, two
+// groups' tiles in turn, from memory straight into LDS; each wave dequantizes its own columns' words.
+//
+// The accumulators hold z / s_g: at a group's start they are multiplied by s_{g-1} / s_g, and the
+// matrix cores add the group's products on top.  Sums per group beside them, scaled in by an fma,
+// would take another 128 registers and leave one wave per SIMD instead of two.  A scale of 0 leaves the
+// accumulators as they are and its codes as 0.
+constexpr int BIG_M = 128;
+
+template <bool F16, bool PAIR>
+__global__ __launch_bounds__(256, 2) void many_rows_linear(LinearArgs a, int row_tiles, int col_tiles) {
+    __shared__ __align__(16) uint16_t xs[2][BIG_M * 128];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 31,
+              half = lane >> 5;
+    const int64_t cols = a.gated ? 2 * a.out : a.out;
+    const int per = a.gated ? 128 : 256;  // outputs per workgroup
+    // Workgroups go to the eight XCDs in turn: each XCD takes a run of tiles, in bands of 8 row tiles,
+    // so that the tiles it works on at a time share rows of x and columns of W in its L2.
+    int64_t id = blockIdx.x;
+    const int64_t all = (int64_t)row_tiles * col_tiles;
+    {
+        const int64_t base = all / 8, more = all % 8, x = id % 8, j = id / 8;
+        id = x * base + (x < more ? x : more) + j;
+    }
+    const int64_t band = id / (8 * col_tiles), in_band = id % (8 * col_tiles);
+    const int64_t high = row_tiles - band * 8 < 8 ? row_tiles - band * 8 : 8;
+    const int64_t rt = band * 8 + in_band % high, ct = in_band / high;
+    const int64_t m0 = rt * BIG_M, n0 = ct * per + wave * (per / 4);
+    // the lane's two columns: PAIR (not gated, an even number of columns): neighbours
+    int64_t c[2];
+    if (PAIR) {
+        c[0] = n0 + 2 * col < a.out ? n0 + 2 * col : a.out - 2;
+        c[1] = c[0] + 1;
+    } else if (a.gated) {
+        c[0] = n0 + col < a.out ? n0 + col : a.out - 1;
+        c[1] = c[0] + a.out;
+    } else {
+        c[0] = n0 + col < a.out ? n0 + col : a.out - 1;
+        c[1] = n0 + 32 + col < a.out ? n0 + 32 + col : a.out - 1;
+    }
+    const int groups = (int)(a.in / 128);
+
+    // x tile of a group: 16-byte piece p of row r lies at place p XOR (r % 16) of its row, so that the 16
+    // rows a quarter of a wave reads at once lie in different banks.  A wave's load fills 1 KB: four rows.
+    const uint16_t* xp[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = 32 * wave + 4 * i + (lane >> 4);
+        const int64_t m = m0 + row < a.M ? m0 + row : a.M - 1;
+        xp[i] = a.x + m * a.ldx + 8 * ((lane & 15) ^ (row & 15));
+    }
+    auto fetch_x = [&](int g, int buf) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(xp[i] + (int64_t)g * 128),
+                                             (__attribute__((address_space(3))) void*)(&xs[buf][(32 * wave + 4 * i) * 128]),
+                                             16, 0, 0);
+    };
+    uint32_t wn[8][2];
+    uint16_t sn[2];
+    auto fetch_w = [&](int g) {
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+            const int32_t* q = a.qw + ((int64_t)g * 16 + 2 * ks + half) * cols;
+            if (PAIR) {
+                const uint2 v = *reinterpret_cast<const uint2*>(q + c[0]);
+                wn[ks][0] = v.x; wn[ks][1] = v.y;
+            } else {
+                wn[ks][0] = (uint32_t)q[c[0]];
+                wn[ks][1] = (uint32_t)q[c[1]];
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) sn[t] = a.scales[(int64_t)g * cols + c[t]];
+    };
+
+    f32x16 acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][t][e] = 0.0f;
+    float s[2] = {1.0f, 1.0f};
+    fetch_x(0, 0);
+    fetch_w(0);
+    for (int g = 0; g < groups; ++g) {
+        const uint16_t* xt = xs[g & 1];
+        uint32_t w[8][2];
+        float ratio[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const float sg = scale_of(sn[t]);
+            const bool zero = sg == 0.0f;
+            ratio[t] = zero ? 1.0f : s[t] / sg;
+            s[t] = zero ? s[t] : sg;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) w[ks][t] = zero ? 0x88888888u : wn[ks][t];
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();  // this group's x is in LDS, and the other buffer has been read
+        if (g + 1 < groups) {
+            fetch_x(g + 1, (g + 1) & 1);
+            fetch_w(g + 1);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[i][t][e] *= ratio[t];
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+            const uint4 b0 = codes<F16>(w[ks][0]), b1 = codes<F16>(w[ks][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 32 * i + col;
+                const uint4 x = *reinterpret_cast<const uint4*>(xt + row * 128 + 8 * ((2 * ks + half) ^ (row & 15)));
+                acc[i][0] = mfma32<F16>(x, b0, acc[i][0]);
+                acc[i][1] = mfma32<F16>(x, b1, acc[i][1]);
+            }
+        }
+    }
+    // The epilogue, 32 rows at a time through LDS: every thread then has four neighbouring outputs of a
+    // row, and residual and y move in whole lines.
+    const bool wide = outputs_in_fours(a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float* tile = reinterpret_cast<float*>(xs[i & 1]);  // [32][256]
+        if (i == 0) __syncthreads();                        // the last group's x has been read
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            float* to = tile + (8 * (e >> 2) + 4 * half + (e & 3)) * 256 + 64 * wave;
+            const float z0 = acc[i][0][e] * (s[0] * CODE_UNIT), z1 = acc[i][1][e] * (s[1] * CODE_UNIT);
+            if (PAIR) {
+                *reinterpret_cast<float2*>(to + 2 * col) = make_float2(z0, z1);
+            } else {
+                to[col] = z0;
+                to[32 + col] = z1;
+            }
+        }
+        __syncthreads();
+        const int n = 4 * (tid % (per / 4)), lines = 1024 / per;
+        const int at = a.gated ? (n >> 5) * 64 + (n & 31) : n;
+        for (int row = tid / (per / 4); row < 32; row += lines) {
+            const f32x4 z = *reinterpret_cast<const f32x4*>(tile + row * 256 + at);
+            f32x4 up = {0, 0, 0, 0};
+            if (a.gated) up = *reinterpret_cast<const f32x4*>(tile + row * 256 + at + 32);
+            finish4<F16>(a, m0 + 32 * i + row, ct * per + n, z, up, wide);
+        }
+    }
+}
+
+template <bool F16, int MT, int W>
+hipError_t few(const LinearArgs& a, bool vec, hipStream_t st) {
+    const int per = a.gated ? 32 : 64;
+    const int64_t ct = (a.out + per - 1) / per, rt = (a.M + 16 * MT - 1) / (16 * MT);
+    if (ct * rt > INT32_MAX) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(ct * rt));
+    if (vec) hipLaunchKernelGGL((few_rows_linear<F16, MT, W, true>), grid, dim3(64 * W), 0, st, a, (int)ct);
+    else hipLaunchKernelGGL((few_rows_linear<F16, MT, W, false>), grid, dim3(64 * W), 0, st, a, (int)ct);
+    return hipGetLastError();
+}
+
+template <bool F16>
+hipError_t launch_type(const LinearArgs& a, hipStream_t st) {
+    const int per = a.gated ? 128 : 256;
+    const int64_t rt = (a.M + BIG_M - 1) / BIG_M, ct = (a.out + per - 1) / per;
+    const bool aligned16 = ((uintptr_t)a.qw & 15) == 0;
+    if (rt * ct >= 256) {
+        if (rt * ct > INT32_MAX) return hipErrorInvalidValue;
+        const dim3 grid((unsigned)(rt * ct));
+        if (!a.gated && a.out % 2 == 0 && ((uintptr_t)a.qw & 7) == 0)
+            hipLaunchKernelGGL((many_rows_linear<F16, true>), grid, dim3(256), 0, st, a, (int)rt, (int)ct);
+        else
+            hipLaunchKernelGGL((many_rows_linear<F16, false>), grid, dim3(256), 0, st, a, (int)rt, (int)ct);
+        return hipGetLastError();
+    }
+    const bool vec = a.gated ? a.out % 2 == 0 && ((uintptr_t)a.qw & 7) == 0 : a.out % 4 == 0 && aligned16;
+    if (a.M <= 16) return few<F16, 1, 8>(a, vec, st);
+    if (a.M <= 256) return few<F16, 2, 8>(a, vec, st);
+    return few<F16, 4, 4>(a, vec, st);
 }
 
 }  // namespace
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t st) {
-    const dim3 grid((unsigned)((a.M + 3) / 4), (unsigned)((a.out + 63) / 64));
-    if (a.x_f16) hipLaunchKernelGGL(linear_kernel<true>, grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL(linear_kernel<false>, grid, dim3(256), 0, st, a);
-    return hipGetLastError();
+    return a.x_f16 ? launch_type<true>(a, st) : launch_type<false>(a, st);
 }
 
 }  // namespace cqk

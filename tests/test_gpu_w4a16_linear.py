@@ -61,13 +61,40 @@ def test_larger(M, out, inp, x):
     _check(M, out, inp, x, res=True)
 
 
+@pytest.mark.parametrize("M,out,inp,kw", [
+    (4100, 2060, 256, dict(bias=True, res=True)), (2049, 4095, 384, dict(y="f32", act="gelu")),
+    (4097, 2046, 128, dict(x="f16", bias=True, act="silu")), (2050, 2200, 256, dict(gated=True, act="silu", bias=True)),
+    (4200, 1037, 256, dict(x="f16", gated=True, act="gelu_tanh", res=True, y="f32")), (33000, 250, 128, dict(res=True)),
+    (2048, 4096, 512, dict(x="f16")), (8200, 1025, 128, dict(act="relu"))])
+def test_many_tiles(M, out, inp, kw):
+    _check(M, out, inp, **kw)
+
+
+@pytest.mark.parametrize("M,out", [(1, 64), (30, 33), (300, 65), (4100, 2060), (2049, 4097)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_scales_of_zero_and_of_every_size(M, out, gated):
+    """Groups whose scale is 0 (with any codes) among scales from the smallest binary16 value to large ones,
+    of either sign."""
+    rng = np.random.default_rng(M + out)
+    cols, inp = 2 * out if gated else out, 1024
+    codes = rng.integers(-8, 8, (cols, inp)).astype(np.int8)
+    sv = (2.0 ** rng.uniform(-24, 4, (cols, 8)) * rng.choice([-1, 1], (cols, 8))).astype(np.float16)
+    sv[rng.random((cols, 8)) < 0.3] = 0
+    sv[::7, 0], sv[::5, 7], sv[::11], sv[1::11] = 0, 0, 0, np.float16(2.0 ** -24)
+    qw, sc = oracle.pack_gptq_v1(codes, sv.view(np.uint16), cols, inp)
+    xt, xn = t16(rng.standard_normal((M, inp)), "bf16")
+    got = cq.w4a16_linear(xt, dev(qw), dev(sc.view(np.int16)), gated=gated, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    close(got, *ref.w4a16_linear(xn, qw, sc, gated=gated, out_type="f32"))
+
+
 @pytest.mark.parametrize("M", [1, 20, 300])
 def test_rows_with_a_common_offset(M):
     """All activations near 3: the row's sum is 100 times its entries' spread."""
     _check(M, 72, 512, y="f32", offset=3.0)
 
 
-@pytest.mark.parametrize("M", [1, 24, 200])
+@pytest.mark.parametrize("M", [1, 24, 200, 33000])
 def test_strided_rows_and_residual_in_place(M):
     rng = np.random.default_rng(M)
     out, inp = 72, 256
@@ -82,7 +109,7 @@ def test_strided_rows_and_residual_in_place(M):
     assert torch.equal(rt[:, :5], rest[:, :5]) and torch.equal(rt[:, 5 + out:], rest[:, 5 + out:])
 
 
-@pytest.mark.parametrize("M", [3, 40, 300])
+@pytest.mark.parametrize("M", [3, 40, 300, 33000])
 def test_a_row_of_nan_or_infinity_stays_in_its_row(M):
     rng = np.random.default_rng(M)
     qw, sc = _weights(rng, 80, 256)
@@ -102,7 +129,7 @@ def test_a_row_of_nan_or_infinity_stays_in_its_row(M):
 
 def test_memory_behind_the_last_row_and_column_is_left_alone():
     rng = np.random.default_rng(9)
-    for M, out in ((1, 33), (17, 65), (130, 129), (300, 200)):
+    for M, out in ((1, 33), (17, 65), (130, 129), (300, 200), (2100, 4001)):
         qw, sc = _weights(rng, out, 128)
         xt, xn = t16(rng.standard_normal((M, 128)), "f16")
         buf = torch.full((M + 140, out + 140), 5.0, dtype=torch.float32, device="cuda")
@@ -114,7 +141,7 @@ def test_memory_behind_the_last_row_and_column_is_left_alone():
 
 def test_repeated_calls_and_another_stream_give_the_same_bits():
     rng = np.random.default_rng(4)
-    for M in (1, 100, 600):
+    for M in (1, 100, 600, 33000):
         qw, sc = (dev(a) for a in _weights(rng, 200, 1024))
         xt, _ = t16(rng.standard_normal((M, 1024)), "bf16")
         a = cq.w4a16_linear(xt, qw, sc.view(torch.int16), activation="gelu")
@@ -141,7 +168,7 @@ def test_replayed_graph():
     rng = np.random.default_rng(8)
     qw, sc = (dev(a) for a in _weights(rng, 256, 512))
     sc = sc.view(torch.int16)
-    for M in (1, 300):
+    for M in (1, 300, 33000):
         xt, _ = t16(rng.standard_normal((M, 512)), "f16")
         out = torch.empty((M, 256), dtype=torch.float16, device="cuda")
         cq.w4a16_linear(xt, qw, sc, out=out)
