@@ -17,9 +17,9 @@
 // likewise, D[4 (l / 16) + r][l % 16].
 //
 // A masked key has weight 0, and 0 times an infinity or a NaN in V would be a NaN: keys that no row
-// of the tile sees are loaded as zeros, and where a tile's mask differs between its rows and its V
-// holds anything that is not finite, the product runs on V with those entries zeroed, and a second one
-// counts, per row and column, the infinities and NaNs among the keys that the row does see.
+// of the tile sees are loaded as zeros, and where a tile's mask differs between its rows, what is not
+// finite in its V is staged as 0 and read again, key by key, into two bits per output (an infinity of
+// either sign seen; both: NaN) that are applied at the end.
 #include "serve_args.h"
 #include "serve_math.h"
 
@@ -73,33 +73,47 @@ __device__ __forceinline__ bool any_not_finite(uint4 v) {
     for (int i = 0; i < 4; ++i) bad |= (w[i] & E) == E || (w[i] & (E << 16)) == (E << 16);
     return bad;
 }
+template <bool F16>
+__device__ __forceinline__ uint4 finite_part(uint4 v) {
+    s16x8 b = __builtin_bit_cast(s16x8, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) b[e] = not_finite<F16>((uint16_t)b[e]) ? (short)0 : b[e];
+    return __builtin_bit_cast(uint4, b);
+}
 
-// V with what is not finite as 0, and its counterpart: +inf as 1, -inf as 2^7, NaN as 2^14 (exact in
-// both types), 0 elsewhere.  A tile has at most 64 keys, so the sums of ones over the keys a row sees
-// separate into their counts.
-template <bool F16>
-__device__ __forceinline__ s16x8 finite_part(s16x8 v) {
+// Infinities and NaNs among the values that a lane's row has seen: bit i of word i / 32 for its i-th
+// output, in the order of its accumulators (an output per four consecutive d each).
+template <int WORDS>
+struct Special {
+    uint32_t pos[WORDS], neg[WORDS];
+    __device__ __forceinline__ bool any() const {
+        uint32_t x = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = not_finite<F16>((uint16_t)v[e]) ? (short)0 : v[e];
-    return v;
-}
-template <bool F16>
-__device__ __forceinline__ s16x8 special_part(s16x8 v) {
-    constexpr uint16_t INF = F16 ? 0x7C00 : 0x7F80;
-    const short one = (short)from_f32<F16>(1.0f), p7 = (short)from_f32<F16>(128.0f), p14 = (short)from_f32<F16>(16384.0f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint16_t b = (uint16_t)v[e];
-        v[e] = !not_finite<F16>(b) ? (short)0 : b == INF ? one : b == (INF | 0x8000) ? p7 : p14;
+        for (int i = 0; i < WORDS; ++i) x |= pos[i] | neg[i];
+        return __any(x != 0);
     }
-    return v;
-}
-__device__ __forceinline__ float special_value(float count) {
-    const int n = (int)count;
-    if (n == 0) return 0.0f;
-    const bool pos = n & 127, neg = (n >> 7) & 127, nan = n >> 14;
-    return nan || (pos && neg) ? __builtin_nanf("") : pos ? INFINITY : -INFINITY;
-}
+    __device__ __forceinline__ float apply(int i, float o) const {
+        const bool p = (pos[i / 32] >> (i % 32)) & 1, n = (neg[i / 32] >> (i % 32)) & 1;
+        return !p && !n ? o : o + (p && n ? __builtin_nanf("") : p ? INFINITY : -INFINITY);
+    }
+    // The four outputs from number 4 j on, for which the key's values are v.
+    template <bool F16>
+    __device__ __forceinline__ void add(int j, uint2 v) {
+        uint32_t p = 0, n = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint16_t b = (uint16_t)((e < 2 ? v.x : v.y) >> (16 * (e & 1)));
+            const bool bad = not_finite<F16>(b), nan = bad && (b & (F16 ? 0x3FF : 0x7F));
+            p |= (uint32_t)(bad && (nan || !(b & 0x8000))) << e;
+            n |= (uint32_t)(bad && (nan || (b & 0x8000))) << e;
+        }
+        p <<= (4 * j) % 32;
+        n <<= (4 * j) % 32;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i)
+            if (i == 4 * j / 32) pos[i] |= p, neg[i] |= n;
+    }
+};
 
 // What the kernels need beside the arguments, worked out on the host.
 struct Plan {
@@ -109,6 +123,7 @@ struct Plan {
     int shift;
     int splits;       // parts that a row tile's keys are divided into, over workgroups
     int rows_lo, rows_hi;  // this launch takes the requests with rows_lo < rows <= rows_hi
+    int per_request;       // few rows: row tiles in the grid per request
     int64_t tiles;         // row tiles in the grid, per key/value head
     int zero_rest;         // this launch writes the tokens that belong to no request
 };
@@ -117,7 +132,7 @@ __device__ __forceinline__ int page_of(const Plan& p, int key) {
     return (int)(((uint64_t)(uint32_t)key * p.magic) >> p.shift);
 }
 
-// Row tile `tile` of `bm` rows -> its request and its number in it: request r's tiles start at
+// Many rows: row tile `tile` of `bm` rows -> its request and its number in it: request r's tiles start at
 // floor(cu[r] G / bm) + r, which leaves room for ceil(n_r G / bm).  Returns false where there is none.
 __device__ __forceinline__ bool find_tile(const AttentionArgs& a, int64_t tile, int G, int bm, int& r, int& first) {
     int lo = 0, hi = a.R - 1;  // the last request whose tiles start at or before `tile`
@@ -192,8 +207,7 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
     const int split = blockIdx.y;
     if (pl.zero_rest && blockIdx.x < (unsigned)a.Hkv && split == 0) zero_rest<F16>(a, kvh);
     if (a.R == 0) return;
-    int r, first;
-    if (!find_tile(a, tile, G, BM, r, first)) return;
+    const int r = (int)(tile / pl.per_request), first = (int)(tile % pl.per_request) * BM;
     const Rows w = rows_of(a, r, first, BM, G);
     const int rows = w.n * G;
     if (first >= rows || rows <= pl.rows_lo || rows > pl.rows_hi) return;
@@ -257,6 +271,7 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x4{0, 0, 0, 0};
     float m = -INFINITY, l = 0.0f;
+    Special<(4 * DT + 31) / 32> seen = {};
 
     int t = t0 + wave;
     fetch_ids(t);
@@ -274,8 +289,11 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 s[h] = mfma16<F16>(__builtin_bit_cast(s16x8, kr[h][ks]), q[ks], s[h]);
+                if (mixed && any_not_finite<F16>(vr[h][ks])) {
+                    bad = true;
+                    vr[h][ks] = finite_part<F16>(vr[h][ks]);
+                }
                 *reinterpret_cast<uint4*>(vl + (16 * h + col) * VS + 32 * ks + 8 * quad) = vr[h][ks];
-                if (mixed) bad |= any_not_finite<F16>(vr[h][ks]);
             }
         }
         const bool special = mixed && __any(bad);
@@ -318,32 +336,40 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
         const s16x8 pb = pack8<F16>(p);
         // O^T += V^T P^T: keys in the order 16 h + 4 quad + e
         const uint16_t* va = vl + (4 * quad + (col >> 2)) * VS + 4 * (col & 3);
-        if (!special) {
 #pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + 16 * d));
-                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + 16 * VS + 16 * d));
-                o[d] = mfma16<F16>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), pb, o[d]);
-            }
-        } else {
-            float ones[8];
+        for (int d = 0; d < DT; ++d) {
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + 16 * d));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + 16 * VS + 16 * d));
+            o[d] = mfma16<F16>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), pb, o[d]);
+        }
+        if (special) {
+            uint32_t mine = 0;  // which of this lane's keys its row sees
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ones[e] = p[e] == 0.0f ? 0.0f : 1.0f;
-            const s16x8 seen = pack8<F16>(ones);
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + 16 * d));
-                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + 16 * VS + 16 * d));
-                const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                o[d] = mfma16<F16>(finite_part<F16>(v), pb, o[d]);
-                const f32x4 n = mfma16<F16>(special_part<F16>(v), seen, f32x4{0, 0, 0, 0});
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[d][e] += special_value(n[e]);
+            for (int e = 0; e < 8; ++e) mine |= (uint32_t)!(p[e] == 0.0f) << e;
+#pragma unroll 1
+            for (int k = 0; k < BN; ++k) {
+                const int key = t * BN + k;
+                const uint32_t of = __shfl(mine, col + 16 * ((k & 15) >> 2));
+                if (key < w.key_begin || key >= w.key_end) continue;
+                const int id = table[page_of(pl, key)];
+                if (id < 0 || id >= a.n_pages) continue;
+                const uint16_t* v = a.vc + id * a.c_page + kvh * a.c_head + (int64_t)(key - page_of(pl, key) * a.page) * a.c_row;
+                if ((of >> (4 * (k >> 4) + (k & 3))) & 1)
+#pragma unroll 1
+                    for (int d = 0; d < DT; ++d)
+                        if (16 * d + 4 * quad < a.D) seen.template add<F16>(d, *reinterpret_cast<const uint2*>(v + 16 * d + 4 * quad));
             }
         }
     }
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
+
+    if (seen.any()) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][e] = seen.apply(4 * d + e, o[d][e]);
+    }
 
     // join the four waves
     float* ol = reinterpret_cast<float*>(lds + wave * WAVE_BYTES);
@@ -489,6 +515,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
     float m = -INFINITY, l = 0.0f;
+    Special<(16 * DT + 31) / 32> seen = {};
 
     if (tid < 2) bad_tile[tid] = 0;
     if (tid < 2 * KT) missing_lds[tid / KT][tid % KT] = 0;
@@ -504,9 +531,12 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) {
                 const int j = (tid + 256 * i) / PER_ROW, d = (tid + 256 * i) % PER_ROW * 8;
+                if (mixed && any_not_finite<F16>(vr[i])) {
+                    bad = true;
+                    vr[i] = finite_part<F16>(vr[i]);
+                }
                 *reinterpret_cast<uint4*>(kl + j * KST + d) = kr[i];
                 *reinterpret_cast<uint4*>(vl + j * VS + d) = vr[i];
-                if (mixed) bad |= any_not_finite<F16>(vr[i]);
                 if (d == 0 && !ok[i] && t * BN + j >= w.key_begin && t * BN + j < w.key_end)
                     atomicOr(&missing_lds[par][j / 32], 1u << (j % 32));
             }
@@ -573,33 +603,38 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
 #pragma unroll
             for (int e = 0; e < 8; ++e) p[e] = s[ss / 2][8 * (ss % 2) + e];
             const s16x8 pb = pack8<F16>(p);
-            if (!special) {
 #pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + (16 * ss) * VS + 32 * d));
-                    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + (16 * ss + 8) * VS + 32 * d));
-                    o[d] = mfma32<F16>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), pb, o[d]);
-                }
-            } else {
-                float ones[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ones[e] = p[e] == 0.0f ? 0.0f : 1.0f;
-                const s16x8 seen = pack8<F16>(ones);
-#pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + (16 * ss) * VS + 32 * d));
-                    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + (16 * ss + 8) * VS + 32 * d));
-                    const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                    o[d] = mfma32<F16>(finite_part<F16>(v), pb, o[d]);
-                    f32x16 n;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) n[e] = 0.0f;
-                    n = mfma32<F16>(special_part<F16>(v), seen, n);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[d][e] += special_value(n[e]);
-                }
+            for (int d = 0; d < DT; ++d) {
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + (16 * ss) * VS + 32 * d));
+                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + (16 * ss + 8) * VS + 32 * d));
+                o[d] = mfma32<F16>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), pb, o[d]);
             }
         }
+        if (special) {
+            uint32_t mine = 0;  // which of this lane's keys its row sees
+#pragma unroll
+            for (int e = 0; e < 16 * KT; ++e) mine |= (uint32_t)!(s[e / 16][e % 16] == 0.0f) << e;
+            const uint32_t theirs = __shfl_xor(mine, 32);
+#pragma unroll 1
+            for (int k = 0; k < BN; ++k) {
+                const int key = t * BN + k;
+                if (key < w.key_begin || key >= w.key_end) continue;
+                const int id = table[page_of(pl, key)];
+                if (id < 0 || id >= a.n_pages) continue;
+                const uint16_t* v = a.vc + id * a.c_page + kvh * a.c_head + (int64_t)(key - page_of(pl, key) * a.page) * a.c_row;
+                const uint32_t of = ((k >> 2) & 1) == half ? mine : theirs;
+                if ((of >> (16 * (k >> 5) + 4 * ((k >> 3) & 3) + (k & 3))) & 1)
+#pragma unroll 1
+                    for (int j = 0; j < 4 * DT; ++j)  // accumulators 4 j .. of the lane: d = 8 j + 4 half ..
+                        if (8 * j + 4 * half < a.D) seen.template add<F16>(j, *reinterpret_cast<const uint2*>(v + 8 * j + 4 * half));
+            }
+        }
+    }
+    if (seen.any()) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[d][e] = seen.apply(16 * d + e, o[d][e]);
     }
     l += __shfl_xor(l, 32);
     if (pl.splits > 1) {
@@ -650,7 +685,12 @@ __global__ __launch_bounds__(256) void join_kernel(AttentionArgs a, Plan pl) {
     const int kvh = (int)(wg / (BM / 4) % a.Hkv);
     const int64_t tile = wg / (BM / 4) / a.Hkv;
     int r, first;
-    if (!find_tile(a, tile, G, BM, r, first)) return;
+    if (BM == 16) {
+        r = (int)(tile / pl.per_request);
+        first = (int)(tile % pl.per_request) * BM;
+    } else if (!find_tile(a, tile, G, BM, r, first)) {
+        return;
+    }
     const Rows w = rows_of(a, r, first, BM, G);
     const int rows = w.n * G, row = first + c;
     if (row >= rows || rows <= pl.rows_lo || rows > pl.rows_hi) return;
@@ -687,6 +727,7 @@ constexpr int FEW = 64;  // requests of at most so many rows go to few_rows_kern
 
 struct Parts {
     int64_t few_tiles, many_tiles;
+    int few_per_request;
     int few_splits, many_splits;  // 0: not launched
 };
 
@@ -701,11 +742,12 @@ int splits_for(int64_t groups, int64_t want, int max_kv, int least_keys) {
 Parts divide(int R, int T, int max_q, int max_kv, int H, int Hkv) {
     const int64_t G = H / Hkv, rows = max_q * G;
     Parts p{};
-    p.few_tiles = T * G / 16 + R + 1;
+    p.few_per_request = (int)((rows < FEW ? rows + 15 : FEW) / 16);
+    if (p.few_per_request < 1) p.few_per_request = 1;
+    p.few_tiles = (int64_t)p.few_per_request * (R > 0 ? R : 1);
     p.many_tiles = T * G / 128 + R + 1;
-    if (rows <= FEW || (int64_t)R * max_q != T) {
-        const int64_t per = (rows < FEW ? rows + 15 : FEW) / 16;
-        p.few_splits = splits_for(R * per * Hkv, 768, max_kv, 128);
+    if (rows <= FEW || (int64_t)R * max_q != T) {  // some requests may have few rows
+        p.few_splits = splits_for(p.few_tiles * Hkv, 768, max_kv, 128);
     }
     if (rows > FEW) {
         const int64_t most = R * ((rows + 127) / 128);
@@ -722,6 +764,7 @@ hipError_t launch_dim(const AttentionArgs& a, Plan pl, const Parts& p, hipStream
         pl.rows_lo = 0;
         pl.rows_hi = p.many_splits ? FEW : INT32_MAX;
         pl.tiles = p.few_tiles;
+        pl.per_request = p.few_per_request;
         hipLaunchKernelGGL((few_rows_kernel<F16, DP>), dim3((unsigned)(p.few_tiles * a.Hkv), p.few_splits), dim3(256), 0,
                            st, a, pl);
         if (p.few_splits > 1)
