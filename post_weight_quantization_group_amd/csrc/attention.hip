@@ -345,7 +345,11 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
         if (special) {
             uint32_t mine = 0;  // which of this lane's keys its row sees
 #pragma unroll
-            for (int e = 0; e < 8; ++e) mine |= (uint32_t)!(p[e] == 0.0f) << e;
+            for (int e = 0; e < 8; ++e) {
+                float x = p[e];
+                asm volatile("" : "+v"(x));  // here, not ahead of the branch
+                mine |= (uint32_t)!(x == 0.0f) << e;
+            }
 #pragma unroll 1
             for (int k = 0; k < BN; ++k) {
                 const int key = t * BN + k;
@@ -426,18 +430,26 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
     }
 }
 
+// Place of the 16-byte piece `piece` in row `row` of a tile [keys][DP] in LDS.  Three accesses have to
+// miss each other's banks (64 of 4 bytes): 16 rows at one piece (K's operand), 4 neighbouring rows at 4
+// pieces (V's transposing read), and the same 4 x 4 as the staging writes it.
+template <int DP>
+__device__ __forceinline__ int place(int row, int piece) {
+    if constexpr (DP % 128 == 0) return piece ^ (4 * (row & 3) + ((row >> 2) & 3));
+    if constexpr (DP % 128 == 64) return piece ^ (4 * ((row >> 1) & 1) + ((row >> 2) & 3));
+    return piece ^ ((row >> 2) & 3);
+}
+
 // ---------------------------------------------------------------------------------------------
 // Many rows (prompts): a workgroup takes 128 rows, 32 per wave, and stages tiles of BN keys and
 // values in LDS for all four waves; the next tile is on its way into registers meanwhile.
 template <bool F16, int DP, int BN>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(AttentionArgs a, Plan pl) {
     constexpr int BM = 128, KS = DP / 16, DT = DP / 32, KT = BN / 32;
-    constexpr int KST = DP + 8;  // rows 4 banks apart
-    constexpr int VS = DP + ((DP / 2) % 64 == 16 || (DP / 2) % 64 == 48 ? 0 : 32);
-    constexpr int PIECES = BN * DP / 8 / 256;  // 16-byte pieces of a tile per thread
-    constexpr int PER_ROW = DP / 8;
-    __shared__ __align__(16) uint16_t kl[BN * KST];
-    __shared__ __align__(16) uint16_t vl[BN * VS];
+    constexpr int TPR = 256 / BN;              // threads per key
+    constexpr int PIECES = DP / 8 / TPR;       // 16-byte pieces of K and of V per thread
+    __shared__ __align__(16) uint16_t kl[BN * DP];
+    __shared__ __align__(16) uint16_t vl[BN * DP];
     __shared__ int bad_tile[2];
     __shared__ uint32_t missing_lds[2][KT];  // keys in range whose page is not in the pool
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, half = lane >> 5;
@@ -484,28 +496,28 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
     const int t0 = t_begin + split * per, t1 = min(t_end, t0 + per);
     const int32_t* table = a.table + r * a.table_stride;
 
-    int page_id[PIECES];
+    // Thread `tid` carries the pieces tid % TPR + TPR i of one key of each tile.  Loads are never
+    // skipped (what is not there is read from the pool's first row and zeroed on its way into LDS).
+    const int my_key = tid / TPR, my_piece = tid % TPR;
+    int page_id = -1;
     auto fetch_ids = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-            const int key = t * BN + (tid + 256 * i) / PER_ROW;
-            page_id[i] = -1;
-            if (t < t1 && key >= w.key_begin && key < w.key_end) page_id[i] = table[page_of(pl, key)];
-        }
+        const int key = t * BN + my_key;
+        page_id = -1;
+        if (t < t1 && key >= w.key_begin && key < w.key_end) page_id = table[page_of(pl, key)];
     };
     uint4 kr[PIECES], vr[PIECES];
-    bool ok[PIECES];
+    bool ok = false;
     auto fetch_kv = [&](int t) {
+        if (t >= t1) return;
+        const int key = t * BN + my_key;
+        ok = page_id >= 0 && page_id < a.n_pages;
+        int64_t at = page_id * a.c_page + (int64_t)(key - page_of(pl, key) * a.page) * a.c_row + kvh * a.c_head + 8 * my_piece;
+        if (!ok) at = 0;
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-            const int j = (tid + 256 * i) / PER_ROW, d = (tid + 256 * i) % PER_ROW * 8, key = t * BN + j;
-            ok[i] = page_id[i] >= 0 && page_id[i] < a.n_pages;
-            kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-            if (ok[i] && d < a.D) {
-                const int64_t at = page_id[i] * a.c_page + kvh * a.c_head + (int64_t)(key - page_of(pl, key) * a.page) * a.c_row + d;
-                kr[i] = *reinterpret_cast<const uint4*>(a.kc + at);
-                vr[i] = *reinterpret_cast<const uint4*>(a.vc + at);
-            }
+            const bool in = 8 * (my_piece + TPR * i) < a.D;
+            kr[i] = *reinterpret_cast<const uint4*>(a.kc + (in ? at + 8 * TPR * i : 0));
+            vr[i] = *reinterpret_cast<const uint4*>(a.vc + (in ? at + 8 * TPR * i : 0));
         }
     };
 
@@ -527,20 +539,29 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
         const bool mixed = t * BN < same_lo || (t + 1) * BN > same_hi;
         __syncthreads();  // the previous tile has been read
         {
-            bool bad = false;
+            if (DP > a.D || !__all(ok)) {
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i)
+                    if (!ok || 8 * (my_piece + TPR * i) >= a.D) kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+                if (!ok && my_piece == 0 && t * BN + my_key >= w.key_begin && t * BN + my_key < w.key_end)
+                    atomicOr(&missing_lds[par][my_key / 32], 1u << (my_key % 32));
+            }
+            if (mixed) {
+                bool bad = false;
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i)
+                    if (any_not_finite<F16>(vr[i])) {
+                        bad = true;
+                        vr[i] = finite_part<F16>(vr[i]);
+                    }
+                if (bad) bad_tile[par] = 1;
+            }
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) {
-                const int j = (tid + 256 * i) / PER_ROW, d = (tid + 256 * i) % PER_ROW * 8;
-                if (mixed && any_not_finite<F16>(vr[i])) {
-                    bad = true;
-                    vr[i] = finite_part<F16>(vr[i]);
-                }
-                *reinterpret_cast<uint4*>(kl + j * KST + d) = kr[i];
-                *reinterpret_cast<uint4*>(vl + j * VS + d) = vr[i];
-                if (d == 0 && !ok[i] && t * BN + j >= w.key_begin && t * BN + j < w.key_end)
-                    atomicOr(&missing_lds[par][j / 32], 1u << (j % 32));
+                const int at = my_key * DP + 8 * place<DP>(my_key, my_piece + TPR * i);
+                *reinterpret_cast<uint4*>(kl + at) = kr[i];
+                *reinterpret_cast<uint4*>(vl + at) = vr[i];
             }
-            if (mixed && bad) bad_tile[par] = 1;
         }
         __syncthreads();
         fetch_kv(t + 1);
@@ -558,10 +579,10 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
         for (int kt = 0; kt < KT; ++kt) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[kt][e] = 0.0f;
-            const uint16_t* ka = kl + (32 * kt + col) * KST + 8 * half;
+            const uint16_t* ka = kl + (32 * kt + col) * DP;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
-                s[kt] = mfma32<F16>(*reinterpret_cast<const s16x8*>(ka + 16 * ks), q[ks], s[kt]);
+                s[kt] = mfma32<F16>(*reinterpret_cast<const s16x8*>(ka + 8 * place<DP>(col, 2 * ks + half)), q[ks], s[kt]);
         }
         float top = -INFINITY;
 #pragma unroll
@@ -596,7 +617,8 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
                 l += s[kt][e];
             }
         }
-        const uint16_t* va = vl + (4 * half + ((lane & 15) >> 2)) * VS + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+        // lane's key in a run of four and its half of a 16-byte piece
+        const int vkey = 4 * half + ((lane & 15) >> 2), vpiece = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1), vd = 4 * (lane & 1);
 #pragma unroll
         for (int ss = 0; ss < BN / 16; ++ss) {
             float p[8];
@@ -605,15 +627,21 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
             const s16x8 pb = pack8<F16>(p);
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
-                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + (16 * ss) * VS + 32 * d));
-                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(va + (16 * ss + 8) * VS + 32 * d));
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (lds_s16x4)(vl + (16 * ss + vkey) * DP + 8 * place<DP>(vkey, 4 * d + vpiece) + vd));
+                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (lds_s16x4)(vl + (16 * ss + 8 + vkey) * DP + 8 * place<DP>(8 + vkey, 4 * d + vpiece) + vd));
                 o[d] = mfma32<F16>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), pb, o[d]);
             }
         }
         if (special) {
             uint32_t mine = 0;  // which of this lane's keys its row sees
 #pragma unroll
-            for (int e = 0; e < 16 * KT; ++e) mine |= (uint32_t)!(s[e / 16][e % 16] == 0.0f) << e;
+            for (int e = 0; e < 16 * KT; ++e) {
+                float p = s[e / 16][e % 16];
+                asm volatile("" : "+v"(p));  // here, not ahead of the branch
+                mine |= (uint32_t)!(p == 0.0f) << e;
+            }
             const uint32_t theirs = __shfl_xor(mine, 32);
 #pragma unroll 1
             for (int k = 0; k < BN; ++k) {
@@ -806,7 +834,9 @@ int64_t attention_ws(int32_t R, int32_t T, int32_t max_q, int32_t max_kv, int32_
     return few > many ? few : many;
 }
 
-hipError_t launch_attention(const AttentionArgs& a, hipStream_t st) {
+hipError_t launch_attention(const AttentionArgs& args, hipStream_t st) {
+    AttentionArgs a = args;
+    if (a.n_pages == 0) a.max_pages = 0;  // no key is read
     Plan pl{};
     pl.c = fmaxf(fabsf(a.scale) * 1.44269504f, 1e-37f);
     pl.flip = a.scale < 0.0f ? 0x80008000u : 0u;
