@@ -440,19 +440,22 @@ __device__ __forceinline__ int place(int row, int piece) {
     return piece ^ ((row >> 2) & 3);
 }
 
+__device__ const uint4 zeros[1] = {};  // what a lane reads for a key or a dimension that is not there
+
 // ---------------------------------------------------------------------------------------------
-// Many rows (prompts): a workgroup takes 128 rows, 32 per wave, and stages tiles of BN keys and
-// values in LDS for all four waves; the next tile is on its way into registers meanwhile.
+// Many rows (prompts): a workgroup takes 128 rows, 32 per wave; tiles of BN keys and values go from
+// memory straight into LDS for all four waves, the next tile's on their way while this one is worked
+// on, one barrier a tile.  The waves take turns in looking up where a tile's rows lie, two tiles ahead.
 template <bool F16, int DP, int BN>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(AttentionArgs a, Plan pl) {
     constexpr int BM = 128, KS = DP / 16, DT = DP / 32, KT = BN / 32;
-    constexpr int TPR = 256 / BN;              // threads per key
-    constexpr int PIECES = DP / 8 / TPR;       // 16-byte pieces of K and of V per thread
-    __shared__ __align__(16) uint16_t kl[BN * DP];
-    __shared__ __align__(16) uint16_t vl[BN * DP];
-    __shared__ int bad_tile[2];
-    __shared__ uint32_t missing_lds[2][KT];  // keys in range whose page is not in the pool
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 31, half = lane >> 5;
+    constexpr int PIECES = BN * DP / 8 / 256;  // 16-byte pieces of K and of V per thread
+    __shared__ __align__(16) uint16_t ktile[2][BN * DP];
+    __shared__ __align__(16) uint16_t vtile[2][BN * DP];
+    __shared__ int64_t row_at[4][BN];  // of tile t, in [t % 4]: offset of each key's row, -1: none
+    __shared__ uint64_t missing_at[4];  // keys in range whose page is not in the pool
+    __shared__ int bad_at[4];           // V holds what is not finite
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 31, half = lane >> 5;
     const int G = a.H / a.Hkv;
     const int kvh = blockIdx.x % a.Hkv;
     const int64_t tile = pl.tiles - 1 - blockIdx.x / a.Hkv;  // the longest rows first
@@ -496,28 +499,33 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
     const int t0 = t_begin + split * per, t1 = min(t_end, t0 + per);
     const int32_t* table = a.table + r * a.table_stride;
 
-    // Thread `tid` carries the pieces tid % TPR + TPR i of one key of each tile.  Loads are never
-    // skipped (what is not there is read from the pool's first row and zeroed on its way into LDS).
-    const int my_key = tid / TPR, my_piece = tid % TPR;
-    int page_id = -1;
-    auto fetch_ids = [&](int t) {
-        const int key = t * BN + my_key;
-        page_id = -1;
-        if (t < t1 && key >= w.key_begin && key < w.key_end) page_id = table[page_of(pl, key)];
+    // Where the rows of tile t lie: one wave, a lane per key; find() starts the table's load, note() ends it.
+    auto find = [&](int t) {
+        const int key = t * BN + lane;
+        return lane < BN && t < t1 && key >= w.key_begin && key < w.key_end ? table[page_of(pl, key)] : INT32_MIN;
     };
-    uint4 kr[PIECES], vr[PIECES];
-    bool ok = false;
-    auto fetch_kv = [&](int t) {
-        if (t >= t1) return;
-        const int key = t * BN + my_key;
-        ok = page_id >= 0 && page_id < a.n_pages;
-        int64_t at = page_id * a.c_page + (int64_t)(key - page_of(pl, key) * a.page) * a.c_row + kvh * a.c_head + 8 * my_piece;
-        if (!ok) at = 0;
+    auto note = [&](int t, int id) {
+        const int key = t * BN + lane;
+        const bool ok = id >= 0 && id < a.n_pages;
+        if (lane < BN)
+            row_at[t & 3][lane] = ok ? id * a.c_page + (int64_t)(key - page_of(pl, key) * a.page) * a.c_row : -1;
+        const uint64_t missing = __ballot(!ok && id != INT32_MIN);
+        if (lane == 0) {
+            missing_at[t & 3] = missing;
+            bad_at[t & 3] = 0;
+        }
+    };
+    const uint16_t* kbase = a.kc + kvh * a.c_head;
+    const uint16_t* vbase = a.vc + kvh * a.c_head;
+    auto fetch = [&](int t) {
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-            const bool in = 8 * (my_piece + TPR * i) < a.D;
-            kr[i] = *reinterpret_cast<const uint4*>(a.kc + (in ? at + 8 * TPR * i : 0));
-            vr[i] = *reinterpret_cast<const uint4*>(a.vc + (in ? at + 8 * TPR * i : 0));
+            const int run = (wave * PIECES + i) * 64, at = run + lane;
+            const int row = at / (DP / 8), d = 8 * place<DP>(row, at % (DP / 8));
+            const int64_t from = row_at[t & 3][row];
+            const bool none = from < 0 || d >= a.D;
+            load_to_lds(none ? (const uint16_t*)zeros : kbase + from + d, &ktile[t & 1][run * 8]);
+            load_to_lds(none ? (const uint16_t*)zeros : vbase + from + d, &vtile[t & 1][run * 8]);
         }
     };
 
@@ -529,61 +537,47 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
     float m = -INFINITY, l = 0.0f;
     Special<(16 * DT + 31) / 32> seen = {};
 
-    if (tid < 2) bad_tile[tid] = 0;
-    if (tid < 2 * KT) missing_lds[tid / KT][tid % KT] = 0;
-    fetch_ids(t0);
-    fetch_kv(t0);
-    fetch_ids(t0 + 1);
+    if (wave < 2) note(t0 + wave, find(t0 + wave));
+    __syncthreads();
+    if (t0 < t1) fetch(t0);
     for (int t = t0; t < t1; ++t) {
-        const int par = t & 1;
-        const bool mixed = t * BN < same_lo || (t + 1) * BN > same_hi;
-        __syncthreads();  // the previous tile has been read
-        {
-            if (DP > a.D || !__all(ok)) {
-#pragma unroll
-                for (int i = 0; i < PIECES; ++i)
-                    if (!ok || 8 * (my_piece + TPR * i) >= a.D) kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-                if (!ok && my_piece == 0 && t * BN + my_key >= w.key_begin && t * BN + my_key < w.key_end)
-                    atomicOr(&missing_lds[par][my_key / 32], 1u << (my_key % 32));
-            }
-            if (mixed) {
-                bool bad = false;
-#pragma unroll
-                for (int i = 0; i < PIECES; ++i)
-                    if (any_not_finite<F16>(vr[i])) {
-                        bad = true;
-                        vr[i] = finite_part<F16>(vr[i]);
-                    }
-                if (bad) bad_tile[par] = 1;
-            }
-#pragma unroll
+        loaded_to_lds();
+        __syncthreads();  // this tile is in LDS, the other buffer has been read, the next tile's rows are known
+        if (t + 1 < t1) fetch(t + 1);
+        int id = INT32_MIN;
+        if (wave == (t & 3)) id = find(t + 2);
+        const uint16_t* kl = ktile[t & 1];
+        uint16_t* vl = vtile[t & 1];
+        bool special = false;
+        if (t * BN < same_lo || (t + 1) * BN > same_hi) {  // the rows' masks differ here
+#pragma unroll 1
             for (int i = 0; i < PIECES; ++i) {
-                const int at = my_key * DP + 8 * place<DP>(my_key, my_piece + TPR * i);
-                *reinterpret_cast<uint4*>(kl + at) = kr[i];
-                *reinterpret_cast<uint4*>(vl + at) = vr[i];
+                uint16_t* at = vl + ((wave * PIECES + i) * 64 + lane) * 8;
+                const uint4 v = *reinterpret_cast<const uint4*>(at);
+                if (any_not_finite<F16>(v)) {
+                    bad_at[t & 3] = 1;
+                    *reinterpret_cast<uint4*>(at) = finite_part<F16>(v);
+                }
             }
+            __syncthreads();
+            special = __builtin_amdgcn_readfirstlane(bad_at[t & 3]);
         }
-        __syncthreads();
-        fetch_kv(t + 1);
-        fetch_ids(t + 2);
-        const bool special = mixed && bad_tile[par];
+        if (t * BN < wave_hi && (t + 1) * BN > wave_lo) {  // some row of this wave sees the tile
         uint32_t missing[KT];
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) missing[kt] = missing_lds[par][kt];
-        if (tid == 0) bad_tile[par ^ 1] = 0;
-        if (tid < KT) missing_lds[par ^ 1][tid] = 0;
-        if (t * BN >= wave_hi || (t + 1) * BN <= wave_lo) continue;  // no row of this wave sees the tile
-
+        for (int kt = 0; kt < KT; ++kt) missing[kt] = __builtin_amdgcn_readfirstlane((uint32_t)(missing_at[t & 3] >> (32 * kt)));
         f32x16 s[KT];
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
+        for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[kt][e] = 0.0f;
-            const uint16_t* ka = kl + (32 * kt + col) * DP;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-                s[kt] = mfma32<F16>(*reinterpret_cast<const s16x8*>(ka + 8 * place<DP>(col, 2 * ks + half)), q[ks], s[kt]);
-        }
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                const uint16_t* ka = kl + (32 * kt + col) * DP + 8 * place<DP>(col, 2 * ks + half);
+                s[kt] = mfma32<F16>(*reinterpret_cast<const s16x8*>(ka), q[ks], s[kt]);
+            }
         float top = -INFINITY;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
@@ -657,6 +651,8 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
                         if (8 * j + 4 * half < a.D) seen.template add<F16>(j, *reinterpret_cast<const uint2*>(v + 8 * j + 4 * half));
             }
         }
+        }
+        if (wave == (t & 3)) note(t + 2, id);
     }
     if (seen.any()) {
 #pragma unroll

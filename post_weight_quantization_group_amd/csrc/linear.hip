@@ -288,9 +288,7 @@ __global__ __launch_bounds__(256, 2) void many_rows_linear(LinearArgs a, int row
     auto fetch_x = [&](int g, int buf) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(xp[i] + (int64_t)g * 128),
-                                             (__attribute__((address_space(3))) void*)(&xs[buf][(32 * wave + 4 * i) * 128]),
-                                             16, 0, 0);
+            load_to_lds(xp[i] + (int64_t)g * 128, &xs[buf][(32 * wave + 4 * i) * 128]);
     };
     uint32_t wn[8][2];
     uint16_t sn[2];
@@ -333,7 +331,7 @@ __global__ __launch_bounds__(256, 2) void many_rows_linear(LinearArgs a, int row
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) w[ks][t] = zero ? 0x88888888u : wn[ks][t];
         }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        loaded_to_lds();
         __syncthreads();  // this group's x is in LDS, and the other buffer has been read
         if (g + 1 < groups) {
             fetch_x(g + 1, (g + 1) & 1);

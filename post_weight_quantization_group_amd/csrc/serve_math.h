@@ -43,4 +43,14 @@ __device__ __forceinline__ float activate(int act, float z) {
     }
 }
 
+// 16 bytes per lane from memory straight into LDS: lane l's to lds + 16 l (lds the same in all lanes).
+// Written out, because the compiler's own form of it waits for every such load before the next read
+// of LDS, also where that reads another buffer.  The caller waits (loaded_to_lds) before the barrier
+// behind which the data is read.
+__device__ __forceinline__ void load_to_lds(const void* from, const void* lds) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "memory", "m0");
+}
+__device__ __forceinline__ void loaded_to_lds() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 }  // namespace cqk
