@@ -345,11 +345,7 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
         if (special) {
             uint32_t mine = 0;  // which of this lane's keys its row sees
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float x = p[e];
-                asm volatile("" : "+v"(x));  // here, not ahead of the branch
-                mine |= (uint32_t)!(x == 0.0f) << e;
-            }
+            for (int e = 7; e >= 0; --e) mine = 2 * mine + !(p[e] == 0.0f);
 #pragma unroll 1
             for (int k = 0; k < BN; ++k) {
                 const int key = t * BN + k;
@@ -434,11 +430,27 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
 // miss each other's banks (64 of 4 bytes): 16 rows at one piece (K's operand), 4 neighbouring rows at 4
 // pieces (V's transposing read), and the same 4 x 4 as the staging writes it.
 template <int DP>
-__device__ __forceinline__ int place(int row, int piece) {
-    if constexpr (DP % 128 == 0) return piece ^ (4 * (row & 3) + ((row >> 2) & 3));
-    if constexpr (DP % 128 == 64) return piece ^ (4 * ((row >> 1) & 1) + ((row >> 2) & 3));
-    return piece ^ ((row >> 2) & 3);
+__device__ __forceinline__ int turn(int row) {
+    if constexpr (DP % 128 == 0) return 4 * (row & 3) + ((row >> 2) & 3);
+    if constexpr (DP % 128 == 64) return 4 * ((row >> 1) & 1) + ((row >> 2) & 3);
+    return (row >> 2) & 3;
 }
+template <int DP>
+__device__ __forceinline__ int place(int row, int piece) {
+    return piece ^ turn<DP>(row);
+}
+// Address in LDS of piece `piece` (a constant) moved by a lane's own share of it: `lane_at` holds the
+// tile, the row and 16 (own ^ turn), own and piece having no bits in common; the turn stays within
+// BLOCK bytes, to a multiple of which tile and rows are aligned.
+template <int DP>
+__device__ __forceinline__ uint32_t piece_at(uint32_t lane_at, int piece) {
+    constexpr int BLOCK = DP % 128 == 0 ? 256 : DP % 128 == 64 ? 128 : 64;
+    return (lane_at ^ (uint32_t)(16 * piece & (BLOCK - 1))) + (uint32_t)(16 * piece & ~(BLOCK - 1));
+}
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+typedef const __attribute__((address_space(3))) s16x8* lds_s16x8;
 
 __device__ const uint4 zeros[1] = {};  // what a lane reads for a key or a dimension that is not there
 
@@ -450,8 +462,8 @@ template <bool F16, int DP, int BN>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(AttentionArgs a, Plan pl) {
     constexpr int BM = 128, KS = DP / 16, DT = DP / 32, KT = BN / 32;
     constexpr int PIECES = BN * DP / 8 / 256;  // 16-byte pieces of K and of V per thread
-    __shared__ __align__(16) uint16_t ktile[2][BN * DP];
-    __shared__ __align__(16) uint16_t vtile[2][BN * DP];
+    __shared__ __align__(256) uint16_t ktile[2][BN * DP];
+    __shared__ __align__(256) uint16_t vtile[2][BN * DP];
     __shared__ int64_t row_at[4][BN];  // of tile t, in [t % 4]: offset of each key's row, -1: none
     __shared__ uint64_t missing_at[4];  // keys in range whose page is not in the pool
     __shared__ int bad_at[4];           // V holds what is not finite
@@ -537,6 +549,11 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
     float m = -INFINITY, l = 0.0f;
     Special<(16 * DT + 31) / 32> seen = {};
 
+    // the lane's row of K and 16-byte piece of it; its key in a run of four of V, and its half of a piece
+    const uint32_t k_lane = lds_offset(ktile) + 2 * DP * col + 16 * (half ^ turn<DP>(col));
+    const int vkey = 4 * half + ((lane & 15) >> 2), vpiece = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    const uint32_t v_lane = lds_offset(vtile) + 2 * DP * vkey + 16 * (vpiece ^ turn<DP>(vkey)) + 8 * (lane & 1);
+
     if (wave < 2) note(t0 + wave, find(t0 + wave));
     __syncthreads();
     if (t0 < t1) fetch(t0);
@@ -546,13 +563,11 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
         if (t + 1 < t1) fetch(t + 1);
         int id = INT32_MIN;
         if (wave == (t & 3)) id = find(t + 2);
-        const uint16_t* kl = ktile[t & 1];
-        uint16_t* vl = vtile[t & 1];
         bool special = false;
         if (t * BN < same_lo || (t + 1) * BN > same_hi) {  // the rows' masks differ here
 #pragma unroll 1
             for (int i = 0; i < PIECES; ++i) {
-                uint16_t* at = vl + ((wave * PIECES + i) * 64 + lane) * 8;
+                uint16_t* at = &vtile[t & 1][((wave * PIECES + i) * 64 + lane) * 8];
                 const uint4 v = *reinterpret_cast<const uint4*>(at);
                 if (any_not_finite<F16>(v)) {
                     bad_at[t & 3] = 1;
@@ -571,21 +586,25 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[kt][e] = 0.0f;
+        const uint32_t ka = k_lane + (t & 1) * (2 * BN * DP), va = v_lane + (t & 1) * (2 * BN * DP);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
-                const uint16_t* ka = kl + (32 * kt + col) * DP + 8 * place<DP>(col, 2 * ks + half);
-                s[kt] = mfma32<F16>(*reinterpret_cast<const s16x8*>(ka), q[ks], s[kt]);
+                const uint32_t at = piece_at<DP>(ka, 2 * ks) + 64 * DP * kt;
+                s[kt] = mfma32<F16>(*(lds_s16x8)at, q[ks], s[kt]);
             }
         float top = -INFINITY;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
             if (t * BN < wsame_lo || (t + 1) * BN > wsame_hi || missing[kt]) {
+                // key 8 (e / 4) + e % 4 after the lane's first one
+                const int at = t * BN + 32 * kt + 4 * half, lo = see_lo - at, hi = see_hi - at;
+                const uint32_t gone = missing[kt] >> (4 * half);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const int k = 8 * (e >> 2) + 4 * half + (e & 3), key = t * BN + 32 * kt + k;
-                    if (key < see_lo || key >= see_hi || ((missing[kt] >> k) & 1)) s[kt][e] = -INFINITY;
+                    const int k = 8 * (e >> 2) + (e & 3);
+                    if (k < lo || k >= hi || (gone & (1u << k))) s[kt][e] = -INFINITY;
                 }
             }
 #pragma unroll
@@ -611,8 +630,6 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
                 l += s[kt][e];
             }
         }
-        // lane's key in a run of four and its half of a 16-byte piece
-        const int vkey = 4 * half + ((lane & 15) >> 2), vpiece = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1), vd = 4 * (lane & 1);
 #pragma unroll
         for (int ss = 0; ss < BN / 16; ++ss) {
             float p[8];
@@ -621,21 +638,17 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
             const s16x8 pb = pack8<F16>(p);
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
-                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (lds_s16x4)(vl + (16 * ss + vkey) * DP + 8 * place<DP>(vkey, 4 * d + vpiece) + vd));
+                // keys 16 ss + vkey, and 8 further on, whose turn differs in one bit
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(piece_at<DP>(va, 4 * d) + 32 * DP * ss));
                 const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (lds_s16x4)(vl + (16 * ss + 8 + vkey) * DP + 8 * place<DP>(8 + vkey, 4 * d + vpiece) + vd));
+                    (lds_s16x4)(piece_at<DP>(va, (4 * d) ^ 2) + 32 * DP * ss + 16 * DP));
                 o[d] = mfma32<F16>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), pb, o[d]);
             }
         }
         if (special) {
             uint32_t mine = 0;  // which of this lane's keys its row sees
 #pragma unroll
-            for (int e = 0; e < 16 * KT; ++e) {
-                float p = s[e / 16][e % 16];
-                asm volatile("" : "+v"(p));  // here, not ahead of the branch
-                mine |= (uint32_t)!(p == 0.0f) << e;
-            }
+            for (int e = 16 * KT - 1; e >= 0; --e) mine = 2 * mine + !(s[e / 16][e % 16] == 0.0f);
             const uint32_t theirs = __shfl_xor(mine, 32);
 #pragma unroll 1
             for (int k = 0; k < BN; ++k) {
