@@ -34,6 +34,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
+constexpr int MANY = 256;  // rows of a workgroup of many_rows_kernel
+
 constexpr float LN2 = 0.69314718f;
 
 template <bool F16>
@@ -90,11 +92,19 @@ struct Special {
         uint32_t x = 0;
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) x |= pos[i] | neg[i];
-        return __any(x != 0);
+        return x != 0;
     }
-    __device__ __forceinline__ float apply(int i, float o) const {
-        const bool p = (pos[i / 32] >> (i % 32)) & 1, n = (neg[i / 32] >> (i % 32)) & 1;
-        return !p && !n ? o : o + (p && n ? __builtin_nanf("") : p ? INFINITY : -INFINITY);
+    // Calls add(i, infinity or NaN) for every output i that has seen one.
+    template <typename F>
+    __device__ __forceinline__ void apply(F add) const {
+#pragma unroll 1
+        for (int i = 0; i < 32 * WORDS; ++i) {
+            uint32_t p = 0, n = 0;
+#pragma unroll
+            for (int k = 0; k < WORDS; ++k)
+                if (k == i / 32) p = pos[k] >> (i % 32) & 1, n = neg[k] >> (i % 32) & 1;
+            if (p | n) add(i, p & n ? __builtin_nanf("") : p ? INFINITY : -INFINITY);
+        }
     }
     // The four outputs from number 4 j on, for which the key's values are v.
     template <bool F16>
@@ -135,11 +145,13 @@ __device__ __forceinline__ int page_of(const Plan& p, int key) {
 // Many rows: row tile `tile` of `bm` rows -> its request and its number in it: request r's tiles start at
 // floor(cu[r] G / bm) + r, which leaves room for ceil(n_r G / bm).  Returns false where there is none.
 __device__ __forceinline__ bool find_tile(const AttentionArgs& a, int64_t tile, int G, int bm, int& r, int& first) {
-    int lo = 0, hi = a.R - 1;  // the last request whose tiles start at or before `tile`
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)a.cu[mid] * G / bm + mid <= tile) lo = mid;
-        else hi = mid - 1;
+    int lo = 0;  // the last request whose tiles start at or before `tile`, by 64 probes at a time
+    for (int n = a.R; n > 1;) {
+        const int step = (n + 63) / 64, lane = threadIdx.x & 63, at = lo + lane * step;
+        const bool before = lane * step < n && (int64_t)a.cu[at] * G / bm + at <= tile;
+        const int k = __builtin_amdgcn_readfirstlane(__popcll(__ballot(before)));  // (the first is, the others in order)
+        lo += (k > 0 ? k - 1 : 0) * step;
+        n = min(step, a.R - lo);
     }
     r = lo;
     first = (int)(tile - ((int64_t)a.cu[lo] * G / bm + lo)) * bm;
@@ -186,6 +198,12 @@ __device__ void zero_rest(const AttentionArgs& a, int kvh) {
     }
 }
 
+// The larger of a lane's value and that of lane l XOR 32.
+__device__ __forceinline__ float max_of_halves(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 // ---------------------------------------------------------------------------------------------
 // Few rows (generation): a workgroup takes 16 rows and one part of the keys; its four waves take tiles
 // of 32 keys in turn, each with its own running maximum, and join at the end.  Bound by reading K and V:
@@ -221,13 +239,14 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
     const int same_hi = a.causal ? min(w.kv, w.pos0 + first / G + 1) : w.kv;  // every live row sees keys in
     const int same_lo = a.window ? max(0, w.pos0 + min(rows - 1, first + BM - 1) / G - a.window + 1) : 0;  // [same_lo, same_hi)
 
+    int64_t q_at = (int64_t)(w.t0 + tok) * a.q_tok + (int64_t)(kvh * G + row - tok * G) * a.q_head + 8 * quad;
+    asm volatile("" : "+v"(q_at));  // worked out once, and not in front of every load
     s16x8 q[KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        const int d = 32 * ks + 8 * quad;
-        if (live && d < a.D) {
-            v = *reinterpret_cast<const uint4*>(a.q + (int64_t)(w.t0 + tok) * a.q_tok + (int64_t)(kvh * G + row % G) * a.q_head + d);
+        if (live && 32 * ks + 8 * quad < a.D) {
+            v = *reinterpret_cast<const uint4*>(a.q + q_at + 32 * ks);
             v.x ^= pl.flip; v.y ^= pl.flip; v.z ^= pl.flip; v.w ^= pl.flip;
         }
         q[ks] = __builtin_bit_cast(s16x8, v);
@@ -364,13 +383,6 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
 
-    if (seen.any()) {
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[d][e] = seen.apply(4 * d + e, o[d][e]);
-    }
-
     // join the four waves
     float* ol = reinterpret_cast<float*>(lds + wave * WAVE_BYTES);
     __syncthreads();
@@ -382,6 +394,7 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
     for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int e = 0; e < 4; ++e) ol[col * OS + 16 * d + 4 * quad + e] = o[d][e];
+    if (seen.any()) seen.apply([&](int i, float x) { ol[col * OS + 4 * (i & ~3) + 4 * quad + (i & 3)] += x; });
     __syncthreads();
     const int live_rows = min(BM, rows - first);
     const int64_t part = (tile * a.Hkv + kvh) * pl.splits + split;
@@ -455,18 +468,21 @@ typedef const __attribute__((address_space(3))) s16x8* lds_s16x8;
 __device__ const uint4 zeros[1] = {};  // what a lane reads for a key or a dimension that is not there
 
 // ---------------------------------------------------------------------------------------------
-// Many rows (prompts): a workgroup takes 128 rows, 32 per wave; tiles of BN keys and values go from
-// memory straight into LDS for all four waves, the next tile's on their way while this one is worked
-// on, one barrier a tile.  The waves take turns in looking up where a tile's rows lie, two tiles ahead.
+// Many rows (prompts): a workgroup takes 256 rows, 32 per wave (two waves per SIMD); tiles of BN keys and values go from
+// memory straight into LDS for all eight waves, three tiles ahead, one barrier a tile.  Where the
+// rows of the next 512 keys lie is looked up at a time.
 template <bool F16, int DP, int BN>
-__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(AttentionArgs a, Plan pl) {
-    constexpr int BM = 128, KS = DP / 16, DT = DP / 32, KT = BN / 32;
-    constexpr int PIECES = BN * DP / 8 / 256;  // 16-byte pieces of K and of V per thread
-    __shared__ __align__(256) uint16_t ktile[2][BN * DP];
-    __shared__ __align__(256) uint16_t vtile[2][BN * DP];
-    __shared__ int64_t row_at[4][BN];  // of tile t, in [t % 4]: offset of each key's row, -1: none
-    __shared__ uint64_t missing_at[4];  // keys in range whose page is not in the pool
-    __shared__ int bad_at[4];           // V holds what is not finite
+__global__ __launch_bounds__(2 * MANY, 2) void many_rows_kernel(AttentionArgs a, Plan pl) {
+    constexpr int BM = MANY, KS = DP / 16, DT = DP / 32, KT = BN / 32;
+    constexpr int RUNS = BN * DP / 8 / 64, WAVES = MANY / 32;  // loads of 64 16-byte pieces a tile of K or V takes
+    constexpr int PIECES = (RUNS + WAVES - 1) / WAVES;         // of them, per wave
+    constexpr int STAGES = 4, BLOCK = 2 * MANY;  // tiles in LDS; keys looked up at a time, one per thread
+    __shared__ __align__(256) uint16_t ktile[STAGES][BN * DP];
+    __shared__ __align__(256) uint16_t vtile[STAGES][BN * DP];
+    __shared__ int64_t row_at[2][BLOCK];             // of block b, in [b % 2]: offset of each key's row, -1: none
+    __shared__ uint64_t missing_at[2][BLOCK / 64];  // keys in range whose page is not in the pool
+    __shared__ int bad_at[4];                       // V of tile t, in [t % 4], holds what is not finite
+    __shared__ Special<(16 * DT + 31) / 32> seen_at[2 * MANY];  // (in LDS: it is hardly ever used)
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 31, half = lane >> 5;
     const int G = a.H / a.Hkv;
     const int kvh = blockIdx.x % a.Hkv;
@@ -494,13 +510,15 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
     const int wsame_hi = a.causal ? min(w.kv, w.pos0 + wfirst / G + 1) : w.kv;
     const int wsame_lo = a.window ? max(0, w.pos0 + wlast / G - a.window + 1) : 0;
 
+    const int head = kvh * G + row - tok * G;
+    int64_t q_at = (int64_t)(w.t0 + tok) * a.q_tok + (int64_t)head * a.q_head + 8 * half;
+    asm volatile("" : "+v"(q_at));  // worked out once, and not in front of every load
     s16x8 q[KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        const int d = 16 * ks + 8 * half;
-        if (live && d < a.D) {
-            v = *reinterpret_cast<const uint4*>(a.q + (int64_t)(w.t0 + tok) * a.q_tok + (int64_t)(kvh * G + row % G) * a.q_head + d);
+        if (live && 16 * ks + 8 * half < a.D) {
+            v = *reinterpret_cast<const uint4*>(a.q + q_at + 16 * ks);
             v.x ^= pl.flip; v.y ^= pl.flip; v.z ^= pl.flip; v.w ^= pl.flip;
         }
         q[ks] = __builtin_bit_cast(s16x8, v);
@@ -511,33 +529,33 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
     const int t0 = t_begin + split * per, t1 = min(t_end, t0 + per);
     const int32_t* table = a.table + r * a.table_stride;
 
-    // Where the rows of tile t lie: one wave, a lane per key; find() starts the table's load, note() ends it.
-    auto find = [&](int t) {
-        const int key = t * BN + lane;
-        return lane < BN && t < t1 && key >= w.key_begin && key < w.key_end ? table[page_of(pl, key)] : INT32_MIN;
+    // Where the rows of a block of keys lie, a thread per key: find() starts the table's load, note() ends it.
+    auto find = [&](int b) {
+        const int key = b * BLOCK + tid;
+        return key >= t0 * BN && key < t1 * BN && key >= w.key_begin && key < w.key_end ? table[page_of(pl, key)] : INT32_MIN;
     };
-    auto note = [&](int t, int id) {
-        const int key = t * BN + lane;
+    auto note = [&](int b, int id) {
+        const int key = b * BLOCK + tid;
         const bool ok = id >= 0 && id < a.n_pages;
-        if (lane < BN)
-            row_at[t & 3][lane] = ok ? id * a.c_page + (int64_t)(key - page_of(pl, key) * a.page) * a.c_row : -1;
+        row_at[b & 1][tid] = ok ? id * a.c_page + (int64_t)(key - page_of(pl, key) * a.page) * a.c_row : -1;
         const uint64_t missing = __ballot(!ok && id != INT32_MIN);
-        if (lane == 0) {
-            missing_at[t & 3] = missing;
-            bad_at[t & 3] = 0;
-        }
+        if (lane == 0) missing_at[b & 1][wave] = missing;
     };
     const uint16_t* kbase = a.kc + kvh * a.c_head;
     const uint16_t* vbase = a.vc + kvh * a.c_head;
     auto fetch = [&](int t) {
+        int me = lane;
+        if constexpr (DP > 128) asm volatile("" : "+v"(me));  // worked out anew each time: there are no registers to keep it
+        const int64_t* rows_at = &row_at[t * BN / BLOCK & 1][t * BN % BLOCK];
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-            const int run = (wave * PIECES + i) * 64, at = run + lane;
+            const int run = wave + WAVES * i, at = 64 * run + me;
+            if (RUNS % WAVES && run >= RUNS) break;
             const int row = at / (DP / 8), d = 8 * place<DP>(row, at % (DP / 8));
-            const int64_t from = row_at[t & 3][row];
+            const int64_t from = rows_at[row];
             const bool none = from < 0 || d >= a.D;
-            load_to_lds(none ? (const uint16_t*)zeros : kbase + from + d, &ktile[t & 1][run * 8]);
-            load_to_lds(none ? (const uint16_t*)zeros : vbase + from + d, &vtile[t & 1][run * 8]);
+            load_to_lds(none ? (const uint16_t*)zeros : kbase + from + d, &ktile[t % STAGES][run * 512]);
+            load_to_lds(none ? (const uint16_t*)zeros : vbase + from + d, &vtile[t % STAGES][run * 512]);
         }
     };
 
@@ -547,27 +565,37 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
     float m = -INFINITY, l = 0.0f;
-    Special<(16 * DT + 31) / 32> seen = {};
+    bool seen_yet = false;  // of the wave: its lanes' Special are in use
 
     // the lane's row of K and 16-byte piece of it; its key in a run of four of V, and its half of a piece
     const uint32_t k_lane = lds_offset(ktile) + 2 * DP * col + 16 * (half ^ turn<DP>(col));
     const int vkey = 4 * half + ((lane & 15) >> 2), vpiece = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
     const uint32_t v_lane = lds_offset(vtile) + 2 * DP * vkey + 16 * (vpiece ^ turn<DP>(vkey)) + 8 * (lane & 1);
 
-    if (wave < 2) note(t0 + wave, find(t0 + wave));
-    __syncthreads();
-    if (t0 < t1) fetch(t0);
+    if (t0 < t1) {
+        const int b = t0 * BN / BLOCK;
+        const int id0 = find(b), id1 = find(b + 1);
+        note(b, id0);
+        note(b + 1, id1);
+        if (tid < 4) bad_at[tid] = 0;
+        __syncthreads();
+        for (int t = t0; t < min(t0 + STAGES - 1, t1); ++t) fetch(t);
+    }
     for (int t = t0; t < t1; ++t) {
-        loaded_to_lds();
-        __syncthreads();  // this tile is in LDS, the other buffer has been read, the next tile's rows are known
-        if (t + 1 < t1) fetch(t + 1);
+        // the two tiles after this one may still be on their way
+        if (t + STAGES - 2 < t1) loaded_to_lds<(STAGES - 2) * 2 * (RUNS / WAVES)>();
+        else loaded_to_lds<0>();
+        __syncthreads();  // this tile is in LDS, the previous one has been read
         int id = INT32_MIN;
-        if (wave == (t & 3)) id = find(t + 2);
+        const bool turn_over = t * BN % BLOCK == 0;  // the block before this one is done with
+        if (turn_over) id = find(t * BN / BLOCK + 1);
+        if (t + STAGES - 1 < t1) fetch(t + STAGES - 1);
+        if (tid == 0) bad_at[(t + 2) & 3] = 0;
         bool special = false;
         if (t * BN < same_lo || (t + 1) * BN > same_hi) {  // the rows' masks differ here
 #pragma unroll 1
-            for (int i = 0; i < PIECES; ++i) {
-                uint16_t* at = &vtile[t & 1][((wave * PIECES + i) * 64 + lane) * 8];
+            for (int i = 64 * wave + lane; i < 64 * RUNS; i += 64 * WAVES) {
+                uint16_t* at = &vtile[t % STAGES][8 * i];
                 const uint4 v = *reinterpret_cast<const uint4*>(at);
                 if (any_not_finite<F16>(v)) {
                     bad_at[t & 3] = 1;
@@ -580,13 +608,14 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
         if (t * BN < wave_hi && (t + 1) * BN > wave_lo) {  // some row of this wave sees the tile
         uint32_t missing[KT];
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) missing[kt] = __builtin_amdgcn_readfirstlane((uint32_t)(missing_at[t & 3] >> (32 * kt)));
+        for (int kt = 0; kt < KT; ++kt) missing[kt] = __builtin_amdgcn_readfirstlane(
+                (uint32_t)(missing_at[t * BN / BLOCK & 1][t * BN % BLOCK / 64] >> (t * BN % 64 + 32 * kt)));
         f32x16 s[KT];
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[kt][e] = 0.0f;
-        const uint32_t ka = k_lane + (t & 1) * (2 * BN * DP), va = v_lane + (t & 1) * (2 * BN * DP);
+        const uint32_t ka = k_lane + t % STAGES * (2 * BN * DP), va = v_lane + t % STAGES * (2 * BN * DP);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -594,6 +623,14 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
                 const uint32_t at = piece_at<DP>(ka, 2 * ks) + 64 * DP * kt;
                 s[kt] = mfma32<F16>(*(lds_s16x8)at, q[ks], s[kt]);
             }
+        // four operands ahead of their products (the compiler reads each just before it)
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+        for (int x = 0; x < KS * KT / 2 - 2; ++x) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x8, 4, 0);
         float top = -INFINITY;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
@@ -610,8 +647,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
 #pragma unroll
             for (int e = 0; e < 16; ++e) top = fmaxf(top, s[kt][e]);
         }
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float m_new = fmaxf(m, top);
+        const float m_new = fmaxf(m, max_of_halves(top));
         const float mc = m_new == -INFINITY ? 0.0f : m_new * pl.c;
         if (__any(m_new > m)) {
             const float keep = __builtin_amdgcn_exp2f(__builtin_fmaf(m, pl.c, -mc));
@@ -650,28 +686,26 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
 #pragma unroll
             for (int e = 16 * KT - 1; e >= 0; --e) mine = 2 * mine + !(s[e / 16][e % 16] == 0.0f);
             const uint32_t theirs = __shfl_xor(mine, 32);
+            Special<(16 * DT + 31) / 32> seen = {};
+            if (seen_yet) seen = seen_at[tid];
+            seen_yet = true;
 #pragma unroll 1
             for (int k = 0; k < BN; ++k) {
                 const int key = t * BN + k;
                 if (key < w.key_begin || key >= w.key_end) continue;
-                const int id = table[page_of(pl, key)];
-                if (id < 0 || id >= a.n_pages) continue;
-                const uint16_t* v = a.vc + id * a.c_page + kvh * a.c_head + (int64_t)(key - page_of(pl, key) * a.page) * a.c_row;
+                const int page = table[page_of(pl, key)];
+                if (page < 0 || page >= a.n_pages) continue;
+                const uint16_t* v = a.vc + page * a.c_page + kvh * a.c_head + (int64_t)(key - page_of(pl, key) * a.page) * a.c_row;
                 const uint32_t of = ((k >> 2) & 1) == half ? mine : theirs;
                 if ((of >> (16 * (k >> 5) + 4 * ((k >> 3) & 3) + (k & 3))) & 1)
 #pragma unroll 1
                     for (int j = 0; j < 4 * DT; ++j)  // accumulators 4 j .. of the lane: d = 8 j + 4 half ..
                         if (8 * j + 4 * half < a.D) seen.template add<F16>(j, *reinterpret_cast<const uint2*>(v + 8 * j + 4 * half));
             }
+            seen_at[tid] = seen;
         }
         }
-        if (wave == (t & 3)) note(t + 2, id);
-    }
-    if (seen.any()) {
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[d][e] = seen.apply(16 * d + e, o[d][e]);
+        if (turn_over) note(t * BN / BLOCK + 1, id);
     }
     l += __shfl_xor(l, 32);
     if (pl.splits > 1) {
@@ -688,39 +722,47 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void many_rows_kernel(Atten
                 wp[BM * DP + 2 * c] = m * pl.c;
                 wp[BM * DP + 2 * c + 1] = l;
             }
+            if (seen_yet) seen_at[tid].apply([&](int i, float x) { wp[c * DP + 2 * (i & ~3) + 4 * half + (i & 3)] += x; });
         }
         return;
     }
     if (live) {
         const bool none = l == 0.0f;
-        const int head = kvh * G + row % G;
-        uint16_t* out = a.out + (int64_t)(w.t0 + tok) * a.o_tok + (int64_t)head * a.o_head;
-        const float inv = none ? 0.0f : 1.0f / l;
+        const float inv = none ? 0.0f : 1.0f / l;  // (o is 0 there)
+        int64_t o_at = (int64_t)(w.t0 + tok) * a.o_tok + (int64_t)head * a.o_head + 4 * half;
+        asm volatile("" : "+v"(o_at));
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                const int dd = 32 * d + 2 * e + 4 * half;
-                if (dd < a.D) {
-                    uint16_t b[4];
+            for (int e = 0; e < 16; e += 4)
+                if (32 * d + 2 * e + 4 * half < a.D) {
+                    uint32_t b[4];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) b[x] = from_f32<F16>(none ? 0.0f : o[d][e + x] * inv);
-                    *reinterpret_cast<uint2*>(out + dd) = make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
+                    for (int x = 0; x < 4; ++x) b[x] = from_f32<F16>(o[d][e + x] * inv);
+                    *reinterpret_cast<uint2*>(a.out + o_at + 32 * d + 2 * e) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
                 }
-            }
+        if (seen_yet)
+            seen_at[tid].apply([&](int i, float x) {
+                if (2 * (i & ~3) + 4 * half >= a.D) return;
+                uint16_t* at = a.out + o_at + 2 * (i & ~3) + (i & 3);
+                *at = from_f32<F16>(to_f32<F16>(*at) + x);
+            });
         if (a.lse && half == 0) a.lse[(int64_t)(w.t0 + tok) * a.H + head] = none ? -INFINITY : (m * pl.c + __log2f(l)) * LN2;
     }
 }
 
-// Joins the parts of a row tile: a wave per row.
+// Joins the parts of a row tile: four rows a workgroup, a wave a row, four neighbouring d a lane; bound by reading the
+// parts' sums.
+constexpr int JOIN_ROWS = 4;
 template <bool F16, int DP, int BM>
 __global__ __launch_bounds__(256) void join_kernel(AttentionArgs a, Plan pl) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int G = a.H / a.Hkv;
     const int64_t wg = blockIdx.x;
-    const int c = (int)(wg % (BM / 4)) * 4 + wave;
-    const int kvh = (int)(wg / (BM / 4) % a.Hkv);
-    const int64_t tile = wg / (BM / 4) / a.Hkv;
+    const int c = (int)(wg % (BM / JOIN_ROWS)) * JOIN_ROWS + wave;
+    const int kvh = (int)(wg / (BM / JOIN_ROWS) % a.Hkv);
+    const int64_t tile = wg / (BM / JOIN_ROWS) / a.Hkv;
+    if (a.R == 0) return;
     int r, first;
     if (BM == 16) {
         r = (int)(tile / pl.per_request);
@@ -735,29 +777,32 @@ __global__ __launch_bounds__(256) void join_kernel(AttentionArgs a, Plan pl) {
     float M = -INFINITY;
     for (int s = 0; s < pl.splits; ++s) M = fmaxf(M, wp[s * (BM * (DP + 2)) + BM * DP + 2 * c]);
     const float Mc = M == -INFINITY ? 0.0f : M;
-    float L = 0.0f, acc[DP / 64 + 1];
-#pragma unroll
-    for (int i = 0; i <= DP / 64; ++i) acc[i] = 0.0f;
+    float L = 0.0f;
+    f32x4 acc = {0, 0, 0, 0};
     for (int s = 0; s < pl.splits; ++s) {
         const float* part = wp + s * (BM * (DP + 2));
-        const float ms = part[BM * DP + 2 * c], ls = part[BM * DP + 2 * c + 1];
-        if (ms == -INFINITY && !(ls != ls)) continue;
-        const float f = __builtin_amdgcn_exp2f(ms - Mc);
-        L = __builtin_fmaf(f, ls, L);
+        const float2 ml = *reinterpret_cast<const float2*>(part + BM * DP + 2 * c);
+        if (ml.x == -INFINITY && !(ml.y != ml.y)) continue;  // this part saw no key of the row
+        const float f = __builtin_amdgcn_exp2f(ml.x - Mc);
+        L = __builtin_fmaf(f, ml.y, L);
+        if (4 * lane < DP) {
+            const f32x4 v = *reinterpret_cast<const f32x4*>(part + c * DP + 4 * lane);
 #pragma unroll
-        for (int i = 0; i <= (DP - 1) / 64; ++i)
-            if (lane + 64 * i < DP) acc[i] = __builtin_fmaf(f, part[c * DP + lane + 64 * i], acc[i]);
+            for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(f, v[e], acc[e]);
+        }
     }
     const bool none = L == 0.0f;
     const int64_t tk = w.t0 + row / G;
     const int head = kvh * G + row % G;
+    if (4 * lane < a.D) {
+        uint16_t b[4];
 #pragma unroll
-    for (int i = 0; i <= (DP - 1) / 64; ++i)
-        if (lane + 64 * i < a.D)
-            a.out[tk * a.o_tok + (int64_t)head * a.o_head + lane + 64 * i] = from_f32<F16>(none ? 0.0f : acc[i] / L);
+        for (int e = 0; e < 4; ++e) b[e] = from_f32<F16>(none ? 0.0f : acc[e] / L);
+        *reinterpret_cast<uint2*>(a.out + tk * a.o_tok + (int64_t)head * a.o_head + 4 * lane) =
+            make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
+    }
     if (a.lse && lane == 0) a.lse[tk * a.H + head] = none ? -INFINITY : (M + __log2f(L)) * LN2;
 }
-
 
 // ---------------------------------------------------------------------------------------------
 constexpr int FEW = 64;  // requests of at most so many rows go to few_rows_kernel
@@ -782,13 +827,13 @@ Parts divide(int R, int T, int max_q, int max_kv, int H, int Hkv) {
     p.few_per_request = (int)((rows < FEW ? rows + 15 : FEW) / 16);
     if (p.few_per_request < 1) p.few_per_request = 1;
     p.few_tiles = (int64_t)p.few_per_request * (R > 0 ? R : 1);
-    p.many_tiles = T * G / 128 + R + 1;
+    p.many_tiles = T * G / MANY + R + 1;
     if (rows <= FEW || (int64_t)R * max_q != T) {  // some requests may have few rows
         p.few_splits = splits_for(p.few_tiles * Hkv, 768, max_kv, 128);
     }
     if (rows > FEW) {
-        const int64_t most = R * ((rows + 127) / 128);
-        p.many_splits = splits_for((most < p.many_tiles ? most : p.many_tiles) * Hkv, 512, max_kv, 512);
+        const int64_t most = R * ((rows + MANY - 1) / MANY), tiles = most < p.many_tiles ? most : p.many_tiles;
+        p.many_splits = splits_for(tiles * Hkv, 256, max_kv, 256);  // a workgroup per CU, no more
     }
     return p;
 }
@@ -805,7 +850,7 @@ hipError_t launch_dim(const AttentionArgs& a, Plan pl, const Parts& p, hipStream
         hipLaunchKernelGGL((few_rows_kernel<F16, DP>), dim3((unsigned)(p.few_tiles * a.Hkv), p.few_splits), dim3(256), 0,
                            st, a, pl);
         if (p.few_splits > 1)
-            hipLaunchKernelGGL((join_kernel<F16, DP, 16>), dim3((unsigned)(p.few_tiles * a.Hkv * 4)), dim3(256), 0, st, a, pl);
+            hipLaunchKernelGGL((join_kernel<F16, DP, 16>), dim3((unsigned)(p.few_tiles * a.Hkv * (16 / JOIN_ROWS))), dim3(256), 0, st, a, pl);
         pl.zero_rest = 0;
     }
     if (p.many_splits) {
@@ -814,9 +859,9 @@ hipError_t launch_dim(const AttentionArgs& a, Plan pl, const Parts& p, hipStream
         pl.rows_hi = INT32_MAX;
         pl.tiles = p.many_tiles;
         hipLaunchKernelGGL((many_rows_kernel<F16, DP, (DP <= 128 ? 64 : 32)>),
-                           dim3((unsigned)(p.many_tiles * a.Hkv), p.many_splits), dim3(256), 0, st, a, pl);
+                           dim3((unsigned)(p.many_tiles * a.Hkv), p.many_splits), dim3(2 * MANY), 0, st, a, pl);
         if (p.many_splits > 1)
-            hipLaunchKernelGGL((join_kernel<F16, DP, 128>), dim3((unsigned)(p.many_tiles * a.Hkv * 32)), dim3(256), 0, st, a,
+            hipLaunchKernelGGL((join_kernel<F16, DP, MANY>), dim3((unsigned)(p.many_tiles * a.Hkv * (MANY / JOIN_ROWS))), dim3(256), 0, st, a,
                                pl);
     }
     return hipGetLastError();
@@ -839,7 +884,7 @@ int64_t attention_ws(int32_t R, int32_t T, int32_t max_q, int32_t max_kv, int32_
     const Parts p = divide(R, T, max_q, max_kv, H, Hkv);
     const int64_t row = padded_dim(D) + 2;
     const int64_t few = p.few_splits > 1 ? p.few_tiles * Hkv * p.few_splits * 16 * row : 0;
-    const int64_t many = p.many_splits > 1 ? p.many_tiles * Hkv * p.many_splits * 128 * row : 0;
+    const int64_t many = p.many_splits > 1 ? p.many_tiles * Hkv * p.many_splits * MANY * row : 0;
     return few > many ? few : many;
 }
 

@@ -51,6 +51,10 @@ __device__ __forceinline__ void load_to_lds(const void* from, const void* lds) {
     const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "memory", "m0");
 }
-__device__ __forceinline__ void loaded_to_lds() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Waits until at most LATER of the wave's loads are outstanding (they arrive in order).
+template <int LATER = 0>
+__device__ __forceinline__ void loaded_to_lds() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER) : "memory");
+}
 
 }  // namespace cqk
