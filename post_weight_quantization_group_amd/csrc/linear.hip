@@ -39,22 +39,24 @@ __device__ __forceinline__ f32x16 mfma32(uint4 a, uint4 b, f32x16 c) {
 // The eight codes of a word as 16 (u - 8) in the 16-bit type: u XOR 8 is u - 8 as a signed 4-bit
 // field, which in the upper half of a byte reads as 16 times its value, converted by one
 // instruction per code (a byte's conversion with sign extension); exact in both types, and the 1/16
-// goes into the group's scale.  15 instructions a word against 21 with the fields shifted down.
+// goes into the group's scale.  15 instructions a word against 21 with the fields shifted down.  A mask of
+// 0 in place of FIELDS makes the codes 0.
 constexpr float CODE_UNIT = 1.0f / 16.0f;
+constexpr uint32_t FIELDS = 0xF0F0F0F0u;
+__device__ __forceinline__ uint32_t even_codes(uint32_t word, uint32_t mask) { return ((word << 4) ^ 0x80808080u) & mask; }
+__device__ __forceinline__ uint32_t odd_codes(uint32_t word, uint32_t mask) { return (word ^ 0x88888888u) & mask; }
+// Codes 2 j and 2 j + 1.
+template <bool F16>
+__device__ __forceinline__ uint32_t two_codes(uint32_t even, uint32_t odd, int j) {
+    const float lo = (float)(int8_t)(even >> (8 * j)), hi = (float)(int8_t)(odd >> (8 * j));
+    if constexpr (F16) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(lo, hi));
+    return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+}
 template <bool F16>
 __device__ __forceinline__ uint4 codes(uint32_t word) {
-    const uint32_t v = word ^ 0x88888888u;
-    const uint32_t even = (v << 4) & 0xF0F0F0F0u, odd = v & 0xF0F0F0F0u;
-    uint32_t h[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float lo = (float)(int8_t)(even >> (8 * j)), hi = (float)(int8_t)(odd >> (8 * j));
-        if constexpr (F16)
-            h[j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(lo, hi));
-        else
-            h[j] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
-    }
-    return make_uint4(h[0], h[1], h[2], h[3]);
+    const uint32_t even = even_codes(word, FIELDS), odd = odd_codes(word, FIELDS);
+    return make_uint4(two_codes<F16>(even, odd, 0), two_codes<F16>(even, odd, 1), two_codes<F16>(even, odd, 2),
+                      two_codes<F16>(even, odd, 3));
 }
 
 __device__ __forceinline__ float scale_of(uint16_t bits) { return (float)__builtin_bit_cast(_Float16, bits); }
@@ -234,18 +236,25 @@ __global__ __launch_bounds__(64 * W) void few_rows_linear(LinearArgs a, int col_
 
 // ---------------------------------------------------------------------------------------------
 // Many rows: a workgroup takes 128 rows and 256 columns (gated: 128 of either half), each of its four
-// waves all rows and 64 columns, as 4 x 2 tiles of 32 x 32.  x goes through LDS once for all waves, two
-// groups' tiles in turn, from memory straight into LDS; each wave dequantizes its own columns' words.
+// waves all rows and 64 columns, as 4 x 2 tiles of 32 x 32.  x and the qweight words go from memory
+// straight into LDS, a group ahead: x, in two buffers, for all waves; the words for the wave that
+// dequantizes them, which has taken them into registers before the next ones are asked for.
 //
 // The accumulators hold z / s_g: at a group's start they are multiplied by s_{g-1} / s_g, and the
 // matrix cores add the group's products on top.  Sums per group beside them, scaled in by an fma,
 // would take another 128 registers and leave one wave per SIMD instead of two.  A scale of 0 leaves the
-// accumulators as they are and its codes as 0.
+// accumulators as they are and masks its codes to 0.
+//
+// A group's 64 products per wave (32 cycles each) come with 15 instructions per word (240) and 128
+// multiplications: 5.8 vector instructions a product, of which 6 run beside one for nothing where
+// they stand between the products; so the order is written out, slot by slot.
 constexpr int BIG_M = 128;
 
-template <bool F16, bool PAIR>
+// PAIR: the lane's columns are neighbours (not gated).  WIDE: words move 16 bytes a lane.
+template <bool F16, bool PAIR, bool WIDE>
 __global__ __launch_bounds__(256, 2) void many_rows_linear(LinearArgs a, int row_tiles, int col_tiles) {
     __shared__ __align__(16) uint16_t xs[2][BIG_M * 128];
+    __shared__ __align__(16) uint32_t words[4][16 * 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 31,
               half = lane >> 5;
     const int64_t cols = a.gated ? 2 * a.out : a.out;
@@ -262,18 +271,13 @@ __global__ __launch_bounds__(256, 2) void many_rows_linear(LinearArgs a, int row
     const int64_t high = row_tiles - band * 8 < 8 ? row_tiles - band * 8 : 8;
     const int64_t rt = band * 8 + in_band % high, ct = in_band / high;
     const int64_t m0 = rt * BIG_M, n0 = ct * per + wave * (per / 4);
-    // the lane's two columns: PAIR (not gated, an even number of columns): neighbours
-    int64_t c[2];
-    if (PAIR) {
-        c[0] = n0 + 2 * col < a.out ? n0 + 2 * col : a.out - 2;
-        c[1] = c[0] + 1;
-    } else if (a.gated) {
-        c[0] = n0 + col < a.out ? n0 + col : a.out - 1;
-        c[1] = c[0] + a.out;
-    } else {
-        c[0] = n0 + col < a.out ? n0 + col : a.out - 1;
-        c[1] = n0 + 32 + col < a.out ? n0 + 32 + col : a.out - 1;
-    }
+    // Column of slot k of the wave's 64: gated: 32 of the gate, then the same of the other half.  Past the
+    // edge: any column in range (WIDE: runs of four that start at a multiple of four, which end with it).
+    auto column = [&](int k) {
+        const int64_t o = n0 + (a.gated ? k & 31 : k), edge = WIDE ? a.out - 4 + (k & 3) : a.out - 1;
+        return (o < a.out ? o : edge) + (a.gated && k >= 32 ? a.out : 0);
+    };
+    const int64_t c[2] = {column(PAIR ? 2 * col : col), column(PAIR ? 2 * col + 1 : 32 + col)};
     const int groups = (int)(a.in / 128);
 
     // x tile of a group: 16-byte piece p of row r lies at place p XOR (r % 16) of its row, so that the 16
@@ -285,27 +289,28 @@ __global__ __launch_bounds__(256, 2) void many_rows_linear(LinearArgs a, int row
         const int64_t m = m0 + row < a.M ? m0 + row : a.M - 1;
         xp[i] = a.x + m * a.ldx + 8 * ((lane & 15) ^ (row & 15));
     }
-    auto fetch_x = [&](int g, int buf) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            load_to_lds(xp[i] + (int64_t)g * 128, &xs[buf][(32 * wave + 4 * i) * 128]);
+    auto ask_x = [&](int g, int i, int buf) { load_to_lds(xp[i] + (int64_t)g * 128, &xs[buf][(32 * wave + 4 * i) * 128]); };
+    // words: qweight row r of the group in row r of the wave's LDS, its 64 slots in order
+    constexpr int WORD_LOADS = WIDE ? 4 : 16;
+    const int32_t* wp = a.qw + (WIDE ? (lane >> 4) * cols + column(4 * (lane & 15)) : column(lane));
+    auto ask_words = [&](int g, int i) {
+        if constexpr (WIDE) load_to_lds(wp + ((int64_t)g * 16 + 4 * i) * cols, &words[wave][i * 256]);
+        else load_to_lds_4(wp + ((int64_t)g * 16 + i) * cols, &words[wave][i * 64]);
     };
-    uint32_t wn[8][2];
-    uint16_t sn[2];
-    auto fetch_w = [&](int g) {
+    // step ks of a group (k = 16 ks ..) takes qweight row 2 ks + half
+    uint32_t w[8][2];
+    auto take_words = [&] {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-            const int32_t* q = a.qw + ((int64_t)g * 16 + 2 * ks + half) * cols;
+            const uint32_t* row = &words[wave][(2 * ks + half) * 64];
             if (PAIR) {
-                const uint2 v = *reinterpret_cast<const uint2*>(q + c[0]);
-                wn[ks][0] = v.x; wn[ks][1] = v.y;
+                const uint2 v = *reinterpret_cast<const uint2*>(row + 2 * col);
+                w[ks][0] = v.x; w[ks][1] = v.y;
             } else {
-                wn[ks][0] = (uint32_t)q[c[0]];
-                wn[ks][1] = (uint32_t)q[c[1]];
+                w[ks][0] = row[col];
+                w[ks][1] = row[32 + col];
             }
         }
-#pragma unroll
-        for (int t = 0; t < 2; ++t) sn[t] = a.scales[(int64_t)g * cols + c[t]];
     };
 
     f32x16 acc[4][2];
@@ -315,45 +320,92 @@ __global__ __launch_bounds__(256, 2) void many_rows_linear(LinearArgs a, int row
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][t][e] = 0.0f;
-    float s[2] = {1.0f, 1.0f};
-    fetch_x(0, 0);
-    fetch_w(0);
-    for (int g = 0; g < groups; ++g) {
-        const uint16_t* xt = xs[g & 1];
-        uint32_t w[8][2];
-        float ratio[2];
+
+    // Scales of the group in hand: the ratio the accumulators take on, and the mask of its codes.
+    float s[2] = {1.0f, 1.0f}, ratio[2];
+    uint32_t mask[2];
+    uint16_t sn[2];
+    auto take_scales = [&] {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const float sg = scale_of(sn[t]);
+            uint32_t bits = sn[t];
+            asm volatile("" : "+v"(bits));  // the wait for it belongs here, not behind its load
+            const float sg = scale_of((uint16_t)bits);
             const bool zero = sg == 0.0f;
             ratio[t] = zero ? 1.0f : s[t] / sg;
             s[t] = zero ? s[t] : sg;
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks) w[ks][t] = zero ? 0x88888888u : wn[ks][t];
+            mask[t] = zero ? 0u : FIELDS;
         }
-        loaded_to_lds();
-        __syncthreads();  // this group's x is in LDS, and the other buffer has been read
-        if (g + 1 < groups) {
-            fetch_x(g + 1, (g + 1) & 1);
-            fetch_w(g + 1);
+    };
+    auto scale_tile = [&](int j) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[j / 2][j % 2][e] *= ratio[j % 2];
+    };
+
+#pragma unroll 1
+    for (int i = 0; i < WORD_LOADS; ++i) ask_words(0, i);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ask_x(0, i, 0);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) sn[t] = a.scales[c[t]];
+    loaded_to_lds();
+    take_words();
+    take_scales();
+    uint32_t b[2][4], bn[2][4];  // operands of this step and of the next
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        b[j / 4][j % 4] = two_codes<F16>(even_codes(w[0][j / 4], mask[j / 4]), odd_codes(w[0][j / 4], mask[j / 4]), j % 4);
+    for (int g = 0; g < groups; ++g) {
+        const uint16_t* xt = xs[g & 1];
+        const int next = g + 1 < groups ? g + 1 : g;  // (the last group asks for its own once more, into the idle buffer)
+        __syncthreads();                              // this group's x is in LDS, and the other buffer has been read
+#pragma unroll
+        for (int t = 0; t < 2; ++t) sn[t] = a.scales[(int64_t)next * cols + c[t]];
+        if constexpr (!WIDE) {
+#pragma unroll 1
+            for (int i = 0; i < WORD_LOADS; ++i) ask_words(next, i);
         }
+        uint4 x[4];
+        auto read_x = [&](int i, int ks) {
+            const int row = 32 * i + col;
+            x[i] = *reinterpret_cast<const uint4*>(xt + row * 128 + 8 * ((2 * ks + half) ^ (row & 15)));
+        };
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) acc[i][t][e] *= ratio[t];
+        for (int i = 0; i < 4; ++i) read_x(i, 0);
+        scale_tile(0);
+        uint32_t even, odd, last[2];
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-            const uint4 b0 = codes<F16>(w[ks][0]), b1 = codes<F16>(w[ks][1]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 32 * i + col;
-                const uint4 x = *reinterpret_cast<const uint4*>(xt + row * 128 + 8 * ((2 * ks + half) ^ (row & 15)));
-                acc[i][0] = mfma32<F16>(x, b0, acc[i][0]);
-                acc[i][1] = mfma32<F16>(x, b1, acc[i][1]);
+            if (ks == 6) {
+                last[0] = w[7][0];
+                last[1] = w[7][1];
+                loaded_to_lds<8>();  // (x was asked for after the words)
+                take_words();
             }
+            if (ks == 7) take_scales();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int i = j / 2, t = j % 2, slot = 8 * ks + j;
+                acc[i][t] = mfma32<F16>(x[i], make_uint4(b[t][0], b[t][1], b[t][2], b[t][3]), acc[i][t]);
+                // an operand is read as soon as its register's last product is issued, 6 slots before its own
+                if (t == 1 && ks < 7) read_x(i, ks + 1);
+                if (ks == 0 && j < 7) scale_tile(j + 1);
+                if (j % 4 == 0) {
+                    const uint32_t word = ks == 6 ? last[j / 4] : w[(ks + 1) % 8][j / 4];
+                    even = even_codes(word, mask[j / 4]);
+                    odd = odd_codes(word, mask[j / 4]);
+                }
+                bn[j / 4][j % 4] = two_codes<F16>(even, odd, j % 4);
+                // The next group's loads, one in a slot: asked for in a row, they hold the wave up (1 KB keeps
+                // the memory pipe for 16 cycles or more).
+                if (WIDE && slot < WORD_LOADS) ask_words(next, slot);
+                else if (slot >= 4 && slot < 28 && slot % 3 == 1) ask_x(next, (slot - 4) / 3, (g + 1) & 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) b[j / 4][j % 4] = bn[j / 4][j % 4];
         }
+        loaded_to_lds();
     }
     // The epilogue, 32 rows at a time through LDS: every thread then has four neighbouring outputs of a
     // row, and residual and y move in whole lines.
@@ -404,10 +456,13 @@ hipError_t launch_type(const LinearArgs& a, hipStream_t st) {
     if (rt * ct >= 256) {
         if (rt * ct > INT32_MAX) return hipErrorInvalidValue;
         const dim3 grid((unsigned)(rt * ct));
-        if (!a.gated && a.out % 2 == 0 && ((uintptr_t)a.qw & 7) == 0)
-            hipLaunchKernelGGL((many_rows_linear<F16, true>), grid, dim3(256), 0, st, a, (int)rt, (int)ct);
+        const bool wide = a.out % 4 == 0 && aligned16;
+        if (wide && !a.gated)
+            hipLaunchKernelGGL((many_rows_linear<F16, true, true>), grid, dim3(256), 0, st, a, (int)rt, (int)ct);
+        else if (wide)
+            hipLaunchKernelGGL((many_rows_linear<F16, false, true>), grid, dim3(256), 0, st, a, (int)rt, (int)ct);
         else
-            hipLaunchKernelGGL((many_rows_linear<F16, false>), grid, dim3(256), 0, st, a, (int)rt, (int)ct);
+            hipLaunchKernelGGL((many_rows_linear<F16, false, false>), grid, dim3(256), 0, st, a, (int)rt, (int)ct);
         return hipGetLastError();
     }
     const bool vec = a.gated ? a.out % 2 == 0 && ((uintptr_t)a.qw & 7) == 0 : a.out % 4 == 0 && aligned16;

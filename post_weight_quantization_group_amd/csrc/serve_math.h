@@ -51,6 +51,11 @@ __device__ __forceinline__ void load_to_lds(const void* from, const void* lds) {
     const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "memory", "m0");
 }
+// The same with 4 bytes per lane.
+__device__ __forceinline__ void load_to_lds_4(const void* from, const void* lds) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(from) : "memory", "m0");
+}
 // Waits until at most LATER of the wave's loads are outstanding (they arrive in order).
 template <int LATER = 0>
 __device__ __forceinline__ void loaded_to_lds() {
