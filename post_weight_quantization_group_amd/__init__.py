@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -178,6 +179,16 @@ def _rows(t):
     if not t.is_cuda:
         raise ValueError("arrays passed to the library must live on the GPU")
     return t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, device: int):
+    """_stream for the helpers on a hot path: the current stream of `device` without building an object."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    return _stream(stream)
 
 
 def _stream(stream):
@@ -557,16 +568,48 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _one_device(first, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, the first array on {first.device}")
+def _on(device: int, *named):
+    """Device pointers of (name, tensor or None) pairs, all of which must be on `device`."""
+    ptrs = []
+    for name, t in named:
+        if t is None:
+            ptrs.append(None)
+        elif t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}; all arrays must live on one GPU")
+        else:
+            ptrs.append(t.data_ptr())
+    return ptrs
+
+
+def _gpu(t) -> int:
+    d = t.get_device()
+    if d < 0:
+        raise ValueError("arrays passed to the library must live on the GPU")
+    return d
+
+
+def _contiguous(**arrays):
+    for name, t in arrays.items():
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
 
 
 def _int32(**arrays):
     for name, t in arrays.items():
         if t.dtype != torch.int32:
             raise ValueError(f"{name} must be int32")
+
+
+def _ld(t):
+    """Leading dimension of a row-major matrix; that of a single row is its length."""
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("the rows of x, residual, out and block_table must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _step(t, dim):
+    """Stride of a dimension; that of a single entry is never used, and 0."""
+    return t.stride(dim) if t.shape[dim] > 1 else 0
 
 
 def w4a16_linear(x, qweight, scales, bias=None, residual=None, activation="none", gated=False, out_dtype=None,
@@ -579,7 +622,8 @@ def w4a16_linear(x, qweight, scales, bias=None, residual=None, activation="none"
     [M, out] have x's type.  activation: "none", "relu", "silu", "gelu" or "gelu_tanh".  The result
     has x's type, or float32 with out_dtype=torch.float32, or goes into ``out`` (which may be the
     residual itself)."""
-    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float16):
+    dt = x.dtype
+    if x.dim() != 2 or (dt != torch.bfloat16 and dt != torch.float16):
         raise ValueError("x must be bfloat16 or float16 [M, in]")
     M, inp = x.shape
     if qweight.dim() != 2 or qweight.dtype != torch.int32 or qweight.shape[0] * 8 != inp or inp % GROUP:
@@ -590,36 +634,30 @@ def w4a16_linear(x, qweight, scales, bias=None, residual=None, activation="none"
     if gated and cols % 2:
         raise ValueError("gated needs an even number of columns")
     n = cols // 2 if gated else cols
-    if bias is not None and (bias.shape != (cols,) or bias.dtype != x.dtype):
+    if bias is not None and (bias.shape != (cols,) or bias.dtype != dt):
         raise ValueError("bias must be [cols], of x's type")
-    if residual is not None and (residual.shape != (M, n) or residual.dtype != x.dtype):
+    if residual is not None and (residual.shape != (M, n) or residual.dtype != dt):
         raise ValueError("residual must be [M, out], of x's type")
-    if activation not in _ACTIVATIONS:
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
-    _one_device(x, qweight=qweight, scales=scales, bias=bias, residual=residual, out=out)
+    _contiguous(qweight=qweight, scales=scales)
+    if bias is not None:
+        _contiguous(bias=bias)
+    device = _gpu(x)
     if out is None:
-        out = _empty((M, n), out_dtype or x.dtype, x, stream)
+        out = _empty((M, n), out_dtype or dt, x, stream)
     elif out.shape != (M, n) or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must be [M, out], of the type asked for")
-    if out.dtype not in (x.dtype, torch.float32):
+    if out.dtype != dt and out.dtype != torch.float32:
         raise ValueError("the result has x's type or float32")
-    for name, t in (("x", x), ("residual", residual), ("out", out)):
-        if t is not None and t.stride(1) != 1 and t.shape[1] > 1:
-            raise ValueError(f"the rows of {name} must be contiguous")
-    cq_w4a16_linear(x, _ld(x), _TYPES[x.dtype], qweight, scales, bias, residual,
-                    0 if residual is None else _ld(residual), _ACTIVATIONS[activation], int(gated), M, n, inp,
-                    out, _ld(out), _TYPES[out.dtype], stream)
+    px, pq, ps, pb, pr, py = _on(device, ("x", x), ("qweight", qweight), ("scales", scales), ("bias", bias),
+                                 ("residual", residual), ("out", out))
+    _check((_lib or load()).cq_w4a16_linear(px, _ld(x), _TYPES[dt], pq, ps, pb, pr,
+                                            0 if residual is None else _ld(residual), act, int(gated), M, n, inp, py,
+                                            _ld(out), _TYPES[out.dtype], _stream_on(stream, device)),
+           "cq_w4a16_linear")
     return out
-
-
-def _ld(t):
-    """Leading dimension of a row-major matrix; that of a single row is its length."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _step(t, dim):
-    """Stride of a dimension; that of a single entry is never used, and 0."""
-    return t.stride(dim) if t.shape[dim] > 1 else 0
 
 
 def kv_block_map(ctx_len, new_len, free_pages, n_free, block_table, page_size, max_tokens, stream=None):
@@ -634,43 +672,58 @@ def kv_block_map(ctx_len, new_len, free_pages, n_free, block_table, page_size, m
     _int32(ctx_len=ctx_len, new_len=new_len, free_pages=free_pages, n_free=n_free, block_table=block_table)
     if new_len.numel() != R or n_free.numel() != 1 or block_table.dim() != 2 or block_table.shape[0] != R:
         raise ValueError("ctx_len and new_len must be [R], n_free [1], block_table [R, max_pages]")
-    if block_table.stride(1) != 1 and block_table.shape[1] > 1:
-        raise ValueError("the rows of block_table must be contiguous")
-    _one_device(ctx_len, new_len=new_len, free_pages=free_pages, n_free=n_free, block_table=block_table)
+    _contiguous(ctx_len=ctx_len, new_len=new_len, free_pages=free_pages)
+    device, most = _gpu(ctx_len), block_table.shape[1]
     sizes = (R + 1, R, max_tokens, max_tokens, R, 1)
-    cu, kv, slots, pos, status, left = _empty(sum(sizes), torch.int32, ctx_len, stream).split(sizes)
-    cq_kv_block_map(ctx_len, new_len, R, page_size, free_pages, n_free, free_pages.numel(), block_table,
-                    _ld(block_table), block_table.shape[1], max_tokens, cu, kv, slots,
-                    pos, status, left, stream)
+    buf = _empty(2 * R + R + 2 + 2 * max_tokens, torch.int32, ctx_len, stream)
+    cu, kv, slots, pos, status, left = buf.split_with_sizes(sizes)
+    pc, pn, pf, pfree, pt, at = _on(device, ("ctx_len", ctx_len), ("new_len", new_len), ("free_pages", free_pages),
+                                    ("n_free", n_free), ("block_table", block_table), ("the result", buf))
+    kv_at = at + 4 * (R + 1)
+    slots_at = kv_at + 4 * R
+    pos_at = slots_at + 4 * max_tokens
+    status_at = pos_at + 4 * max_tokens
+    _check((_lib or load()).cq_kv_block_map(pc, pn, R, page_size, pf, pfree, free_pages.numel(), pt, _ld(block_table),
+                                            most, max_tokens, at, kv_at, slots_at, pos_at, status_at,
+                                            status_at + 4 * R, _stream_on(stream, device)), "cq_kv_block_map")
     return {"cu_q": cu, "kv_len": kv, "slots": slots, "positions": pos, "status": status, "n_left": left}
 
 
 def _cache_shape(k_cache, v_cache):
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or \
-            any(k_cache.shape[i] > 1 and v_cache.stride(i) != k_cache.stride(i) for i in range(4)):
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or v_cache.shape != shape or \
+            (v_cache.stride() != strides and any(shape[i] > 1 and v_cache.stride(i) != strides[i] for i in range(4))):
         raise ValueError("k_cache and v_cache must be [pages, kv_heads, page_size, head_dim], strided alike")
-    if k_cache.dtype not in (torch.bfloat16, torch.float16) or v_cache.dtype != k_cache.dtype:
+    dt = k_cache.dtype
+    if (dt != torch.bfloat16 and dt != torch.float16) or v_cache.dtype != dt:
         raise ValueError("k_cache and v_cache must be bfloat16 or float16")
-    if k_cache.stride(3) != 1:
+    if strides[3] != 1:
         raise ValueError("head_dim must be contiguous")
+    return shape, [st if n > 1 else 0 for st, n in zip(strides, shape)]
 
 
 def kv_cache_write(k, v, k_cache, v_cache, slots, stream=None):
     """Writes k, v [T, kv_heads, head_dim] (strided views allowed) into the caches
     [pages, kv_heads, page_size, head_dim] at slots int32 [T] (page * page_size + offset; a
     negative slot is skipped)."""
-    _cache_shape(k_cache, v_cache)
+    (pages, heads, page, D), (c_page, c_head, c_row, _) = _cache_shape(k_cache, v_cache)
     T = slots.numel()
     _int32(slots=slots)
-    want = (T, k_cache.shape[1], k_cache.shape[3])
-    if k.shape != want or v.shape != want or k.dtype != k_cache.dtype or v.dtype != k_cache.dtype:
+    want, dt = (T, heads, D), k_cache.dtype
+    if k.shape != want or v.shape != want or k.dtype != dt or v.dtype != dt:
         raise ValueError("k and v must be [T, kv_heads, head_dim] of the caches' type, slots int32 [T]")
     if k.stride(2) != 1 or v.stride(2) != 1:
         raise ValueError("head_dim must be contiguous")
-    _one_device(k_cache, v_cache=v_cache, k=k, v=v, slots=slots)
-    cq_kv_cache_write(k, _step(k, 0), _step(k, 1), v, _step(v, 0), _step(v, 1), k_cache, v_cache, _step(k_cache, 0),
-                      _step(k_cache, 1), _step(k_cache, 2), k_cache.shape[0], k_cache.shape[2], want[1], want[2],
-                      slots, T, stream)
+    _contiguous(slots=slots)
+    device = _gpu(k_cache)
+    pk, pv, pkc, pvc, ps = _on(device, ("k", k), ("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("slots", slots))
+    _check((_lib or load()).cq_kv_cache_write(pk, _step(k, 0), _step(k, 1), pv, _step(v, 0), _step(v, 1), pkc, pvc,
+                                              c_page, c_head, c_row, pages, page, heads, D, ps, T,
+                                              _stream_on(stream, device)), "cq_kv_cache_write")
+
+
+_ATTENTION_ARGS = struct.Struct("@8P8q13if")  # PagedAttentionArgs, field by field
+assert _ATTENTION_ARGS.size == ctypes.sizeof(PagedAttentionArgs)
 
 
 def paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_kv, scale=None, causal=True, window=0,
@@ -682,34 +735,38 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_k
     included); max_q and max_kv are the host's bounds of the requests' new and cached tokens.
     scale defaults to 1/sqrt(head_dim).  Returns out [T, heads, head_dim] of q's type; ``lse``, if
     given, is a contiguous float32 [T, heads] to fill."""
-    _cache_shape(k_cache, v_cache)
-    if q.dim() != 3 or q.dtype != k_cache.dtype or q.shape[2] != k_cache.shape[3] or q.stride(2) != 1:
+    (pages, Hkv, page, D), (c_page, c_head, c_row, _) = _cache_shape(k_cache, v_cache)
+    dt = q.dtype
+    if q.dim() != 3 or dt != k_cache.dtype or q.shape[2] != D or q.stride(2) != 1:
         raise ValueError("q must be [T, heads, head_dim] of the caches' type, head_dim contiguous")
     _int32(block_table=block_table, cu_q=cu_q, kv_len=kv_len)
-    T, H, D = q.shape
+    T, H, _ = q.shape
     R = kv_len.numel()
     if cu_q.numel() != R + 1 or block_table.dim() != 2 or block_table.shape[0] != R:
         raise ValueError("cu_q must be [R + 1], kv_len [R], block_table [R, max_pages]")
-    if block_table.stride(1) != 1 and block_table.shape[1] > 1:
-        raise ValueError("the rows of block_table must be contiguous")
-    if lse is not None and (lse.shape != (T, H) or lse.dtype != torch.float32):
-        raise ValueError("lse must be float32 [T, heads]")
-    _one_device(q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, cu_q=cu_q, kv_len=kv_len, out=out,
-                lse=lse)
+    _contiguous(cu_q=cu_q, kv_len=kv_len)
+    if lse is not None:
+        if lse.shape != (T, H) or lse.dtype != torch.float32:
+            raise ValueError("lse must be float32 [T, heads]")
+        _contiguous(lse=lse)
+    device = _gpu(q)
     if out is None:
-        out = _empty((T, H, D), q.dtype, q, stream)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.stride(2) != 1:
+        out = _empty((T, H, D), dt, q, stream)
+    elif out.shape != q.shape or out.dtype != dt or out.stride(2) != 1:
         raise ValueError("out must be [T, heads, head_dim] of q's type, head_dim contiguous")
-    Hkv = k_cache.shape[1]
-    need = cq_paged_attention_workspace_size(T, R, max_q, max_kv, H, Hkv, D)
+    lib = _lib or load()
+    need = lib.cq_paged_attention_workspace_size(T, R, max_q, max_kv, H, Hkv, D)
     if need and workspace is None:
         workspace = _empty(need, torch.uint8, q, stream)
-    cq_paged_attention(PagedAttentionArgs(
-        _rows(q), _rows(k_cache), _rows(v_cache), _rows(block_table), _p(cu_q), _p(kv_len), _rows(out), _p(lse),
-        _step(q, 0), _step(q, 1), _step(out, 0), _step(out, 1), _step(k_cache, 0), _step(k_cache, 1),
-        _step(k_cache, 2), _ld(block_table), _TYPES[q.dtype], T, R, max_q, max_kv, H,
-        Hkv, D, k_cache.shape[2], k_cache.shape[0], block_table.shape[1], int(causal), window,
-        D ** -0.5 if scale is None else scale), workspace, stream)
+    pq, pk, pv, pt, pcu, pkv, po, pl, pw = _on(
+        device, ("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("block_table", block_table), ("cu_q", cu_q),
+        ("kv_len", kv_len), ("out", out), ("lse", lse), ("workspace", workspace))
+    args = PagedAttentionArgs.from_buffer_copy(_ATTENTION_ARGS.pack(
+        pq, pk, pv, pt, pcu, pkv, po, pl or 0, _step(q, 0), _step(q, 1), _step(out, 0), _step(out, 1), c_page, c_head,
+        c_row, _ld(block_table), _TYPES[dt], T, R, max_q, max_kv, H, Hkv, D, page, pages, block_table.shape[1],
+        int(causal), window, D ** -0.5 if scale is None else scale))
+    _check(lib.cq_paged_attention(args, pw, 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                  _stream_on(stream, device)), "cq_paged_attention")
     return out
 
 

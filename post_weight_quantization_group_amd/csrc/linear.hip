@@ -453,7 +453,9 @@ hipError_t launch_type(const LinearArgs& a, hipStream_t st) {
     const int per = a.gated ? 128 : 256;
     const int64_t rt = (a.M + BIG_M - 1) / BIG_M, ct = (a.out + per - 1) / per;
     const bool aligned16 = ((uintptr_t)a.qw & 15) == 0;
-    if (rt * ct >= 256) {
+    // At 4096 inputs: 64 tiles (512 x 4096) 69 us here and 48 by the other kernel, 128 tiles 70 and 95: this one's time
+    // does not fall with fewer tiles than CUs, the other's does.
+    if (rt * ct >= 88) {
         if (rt * ct > INT32_MAX) return hipErrorInvalidValue;
         const dim3 grid((unsigned)(rt * ct));
         const bool wide = a.out % 4 == 0 && aligned16;
