@@ -7,6 +7,22 @@ namespace {
 
 constexpr int MAP_THREADS = 1024;
 
+// Sums that stay at their largest value instead of wrapping: all that is asked of them is whether they
+// exceed a limit below 2^31.
+__device__ __forceinline__ uint32_t add_sat(uint32_t x, uint32_t y) { return __builtin_elementwise_add_sat(x, y); }
+// Inclusive sums over the lanes of a wave: within rows of 16 lanes by shifts, then row ends onto the rows behind.
+__device__ __forceinline__ uint32_t scan_of_wave(uint32_t x) {
+    x = add_sat(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false));  // row_shr:1
+    x = add_sat(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false));
+    x = add_sat(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false));
+    x = add_sat(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false));
+    x = add_sat(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false));  // lane 15 (47) to the second (fourth) row
+    return add_sat(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false));  // lane 31 to the upper rows
+}
+__device__ __forceinline__ uint32_t pages_for(int32_t tokens, int32_t page) {
+    return (uint32_t)tokens / (uint32_t)page + ((uint32_t)tokens % (uint32_t)page != 0);
+}
+
 // Block tables and slot maps.  Request r holds ctx_r tokens and receives add_r more:
 //   need_r = ceil((ctx_r + add_r) / page) - ceil(ctx_r / page) pages, 0 for an invalid request;
 //   P_r, C_r = inclusive prefix sums of need and add over the valid requests;
@@ -22,68 +38,60 @@ __global__ __launch_bounds__(MAP_THREADS) void block_map_kernel(BlockMapArgs a) 
     extern __shared__ int32_t lds[];
     int32_t* cum = lds;               // [R] served tokens through r (C_r, frozen from the first misfit on)
     int32_t* first = lds + a.R;       // [R] pages taken before r; -1 - that for a request not served
-    __shared__ int64_t wave_pages[MAP_THREADS / 64], wave_tokens[MAP_THREADS / 64];
+    __shared__ uint32_t wave_pages[MAP_THREADS / 64], wave_tokens[MAP_THREADS / 64];
     __shared__ int32_t served_pages, served_tokens;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int32_t n_free = a.n_free[0];
     n_free = n_free < 0 ? 0 : n_free > a.free_cap ? a.free_cap : n_free;
     if (tid == 0) served_pages = served_tokens = 0;
-    int64_t base_pages = 0, base_tokens = 0;
+    uint32_t base_pages = 0, base_tokens = 0;
     for (int r0 = 0; r0 < a.R; r0 += MAP_THREADS) {
         const int r = r0 + tid;
-        int64_t need = 0, add = 0;
+        uint32_t need = 0, add = 0;
         int32_t ctx = 0;
         bool valid = false;
         if (r < a.R) {
             ctx = a.ctx[r];
-            const int64_t n = a.add[r];
-            valid = ctx >= 0 && n >= 0 && ctx + n <= (int64_t)a.max_pages * a.page;
+            const int32_t n = a.add[r];
+            valid = ctx >= 0 && n >= 0 && (int64_t)ctx + n <= (int64_t)a.max_pages * a.page;
             if (valid) {
                 add = n;
-                need = (ctx + n + a.page - 1) / a.page - ((int64_t)ctx + a.page - 1) / a.page;
+                need = pages_for(ctx + n, a.page) - pages_for(ctx, a.page);
             }
         }
-        int64_t p = need, c = add;
-#pragma unroll
-        for (int s = 1; s < 64; s <<= 1) {
-            const int64_t pp = __shfl_up(p, s), cc = __shfl_up(c, s);
-            if (lane >= s) {
-                p += pp;
-                c += cc;
-            }
-        }
-        __syncthreads();  // the wave sums of the previous 1,024 requests have been read
+        uint32_t p = scan_of_wave(need), c = scan_of_wave(add);
+        if (r0 > 0) __syncthreads();  // the wave sums of the previous 1,024 requests have been read
         if (lane == 63) {
             wave_pages[wave] = p;
             wave_tokens[wave] = c;
         }
         __syncthreads();
-        int64_t all_p = 0, all_c = 0;
-        for (int w = 0; w < MAP_THREADS / 64; ++w) {
+        const int waves = min(MAP_THREADS, a.R - r0 + 63) / 64;  // that hold requests
+        uint32_t all_p = base_pages, all_c = base_tokens;
+        for (int w = 0; w < waves; ++w) {
             if (w == wave) {
-                p += all_p;
-                c += all_c;
+                p = add_sat(p, all_p);
+                c = add_sat(c, all_c);
             }
-            all_p += wave_pages[w];
-            all_c += wave_tokens[w];
+            all_p = add_sat(all_p, wave_pages[w]);
+            all_c = add_sat(all_c, wave_tokens[w]);
         }
-        p += base_pages;
-        c += base_tokens;
-        base_pages += all_p;
-        base_tokens += all_c;
+        base_pages = all_p;
+        base_tokens = all_c;
+        const bool fits = r < a.R && p <= (uint32_t)n_free && c <= (uint32_t)a.max_tokens;
         if (r < a.R) {
-            const bool fits = p <= n_free && c <= a.max_tokens;
             const bool served = valid && fits;
             cum[r] = fits ? (int32_t)c : INT32_MAX;
             first[r] = served ? (int32_t)(p - need) : -1;
-            if (fits) {
-                atomicMax(&served_pages, (int32_t)p);
-                atomicMax(&served_tokens, (int32_t)c);
-            }
             if (blockIdx.x == 0) {
                 a.status[r] = !valid ? 2 : fits ? 0 : 1;
                 a.kv_len[r] = served ? (int32_t)(ctx + add) : ctx < 0 ? 0 : ctx;
             }
+        }
+        // the requests that fit are the first ones: the last of them holds the served sums
+        if (lane == (int)__popcll(__ballot(fits)) - 1) {
+            atomicMax(&served_pages, (int32_t)p);
+            atomicMax(&served_tokens, (int32_t)c);
         }
     }
     __syncthreads();
@@ -116,7 +124,7 @@ __global__ __launch_bounds__(MAP_THREADS) void block_map_kernel(BlockMapArgs a) 
             }
             const int32_t ctx = a.ctx[lo];
             pos = ctx + (int32_t)(t - (lo > 0 ? cum[lo - 1] : 0));
-            const int32_t b = pos / a.page, b0 = (ctx + a.page - 1) / a.page;
+            const int32_t b = pos / a.page, b0 = pages_for(ctx, a.page);
             const int32_t pg = b < b0 ? a.table[lo * a.table_stride + b]
                                       : a.free_pages[n_free - 1 - first[lo] - (b - b0)];
             const int64_t s = (int64_t)pg * a.page + pos % a.page;
