@@ -75,6 +75,15 @@ __device__ __forceinline__ bool any_not_finite(uint4 v) {
     for (int i = 0; i < 4; ++i) bad |= (w[i] & E) == E || (w[i] & (E << 16)) == (E << 16);
     return bad;
 }
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+// The larger of each half's values so far and those of eight more, signs aside: infinities and NaNs are the largest.
+template <bool F16>
+__device__ __forceinline__ u16x2 largest_exponents(u16x2 most, uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
+    return most;
+}
 template <bool F16>
 __device__ __forceinline__ uint4 finite_part(uint4 v) {
     s16x8 b = __builtin_bit_cast(s16x8, v);
@@ -131,6 +140,7 @@ struct Plan {
     uint32_t flip;    // sign bits of a pair of 16-bit values where scale < 0: applied to q
     uint32_t magic;   // n / page = (n * magic) >> shift for 0 <= n < 2^31
     int shift;
+    int G;            // query heads per key/value head
     int splits;       // parts that a row tile's keys are divided into, over workgroups
     int rows_lo, rows_hi;  // this launch takes the requests with rows_lo < rows <= rows_hi
     int per_request;       // few rows: row tiles in the grid per request
@@ -190,7 +200,7 @@ __device__ void zero_rest(const AttentionArgs& a, int kvh) {
     for (int t = 0; t < a.T; ++t) {
         if (t == begin) t = max(t, end);
         if (t >= a.T) return;
-        for (int i = threadIdx.x; i < G * (a.D / 8); i += 256) {
+        for (int i = threadIdx.x; i < G * (a.D / 8); i += blockDim.x) {
             const int h = kvh * G + i / (a.D / 8), d = i % (a.D / 8) * 8;
             *reinterpret_cast<uint4*>(a.out + t * a.o_tok + (int64_t)h * a.o_head + d) = make_uint4(0, 0, 0, 0);
             if (a.lse && d == 0) a.lse[(int64_t)t * a.H + h] = -INFINITY;
@@ -219,13 +229,10 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
     __shared__ __align__(16) uint8_t lds[4 * WAVE_BYTES];
     __shared__ float wave_m[4][BM], wave_l[4][BM];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, quad = lane >> 4;
-    const int G = a.H / a.Hkv;
-    const int kvh = blockIdx.x % a.Hkv;
-    const int64_t tile = blockIdx.x / a.Hkv;
-    const int split = blockIdx.y;
-    if (pl.zero_rest && blockIdx.x < (unsigned)a.Hkv && split == 0) zero_rest<F16>(a, kvh);
+    const int G = pl.G, kvh = blockIdx.x, tile = blockIdx.y, split = blockIdx.z;
+    if (pl.zero_rest && tile == 0 && split == 0) zero_rest<F16>(a, kvh);
     if (a.R == 0) return;
-    const int r = (int)(tile / pl.per_request), first = (int)(tile % pl.per_request) * BM;
+    const int r = (uint32_t)tile / (uint32_t)pl.per_request, first = (tile - r * pl.per_request) * BM;
     const Rows w = rows_of(a, r, first, BM, G);
     const int rows = w.n * G;
     if (first >= rows || rows <= pl.rows_lo || rows > pl.rows_hi) return;
@@ -276,12 +283,20 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
             ok_next[h] = page_id[h] >= 0 && page_id[h] < a.n_pages;
             const int64_t at = page_id[h] * a.c_page + kvh * a.c_head + (int64_t)(key - page_of(pl, key) * a.page) * a.c_row + 8 * quad;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                kr[h][ks] = vr[h][ks] = make_uint4(0, 0, 0, 0);
-                if (ok_next[h] && 32 * ks + 8 * quad < a.D) {
-                    kr[h][ks] = *reinterpret_cast<const uint4*>(a.kc + at + 32 * ks);
-                    vr[h][ks] = *reinterpret_cast<const uint4*>(a.vc + at + 32 * ks);
-                }
+            for (int ks = 0; ks < KS; ++ks) kr[h][ks] = vr[h][ks] = make_uint4(0, 0, 0, 0);
+            if (!ok_next[h]) continue;
+            if (a.D == DP) {
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) kr[h][ks] = *reinterpret_cast<const uint4*>(a.kc + at + 32 * ks);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) vr[h][ks] = *reinterpret_cast<const uint4*>(a.vc + at + 32 * ks);
+            } else {
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+                    if (32 * ks + 8 * quad < a.D) {
+                        kr[h][ks] = *reinterpret_cast<const uint4*>(a.kc + at + 32 * ks);
+                        vr[h][ks] = *reinterpret_cast<const uint4*>(a.vc + at + 32 * ks);
+                    }
             }
         }
     };
@@ -298,7 +313,6 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
     fetch_ids(t + 4);
     for (; t < t1; t += 4) {
         f32x4 s[2];
-        bool bad = false;
         const bool mixed = t * BN < same_lo || (t + 1) * BN > same_hi;
         uint64_t there[2];
 #pragma unroll
@@ -308,14 +322,24 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
                 s[h] = mfma16<F16>(__builtin_bit_cast(s16x8, kr[h][ks]), q[ks], s[h]);
-                if (mixed && any_not_finite<F16>(vr[h][ks])) {
-                    bad = true;
-                    vr[h][ks] = finite_part<F16>(vr[h][ks]);
-                }
                 *reinterpret_cast<uint4*>(vl + (16 * h + col) * VS + 32 * ks + 8 * quad) = vr[h][ks];
             }
         }
-        const bool special = mixed && __any(bad);
+        bool special = false;
+        if (mixed) {
+            u16x2 most = {0, 0};
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) most = largest_exponents<F16>(most, vr[h][ks]);
+            special = __any(not_finite<F16>(most.x) || not_finite<F16>(most.y));
+            if (special)
+#pragma unroll 1
+                for (int i = quad; i < 2 * DP / 8; i += 4) {  // the pieces this lane has stored
+                    uint4* at = reinterpret_cast<uint4*>(vl + (16 * (i / (DP / 8)) + col) * VS + 8 * (i % (DP / 8)));
+                    *at = finite_part<F16>(*at);
+                }
+        }
         fetch_kv(t + 4);
         fetch_ids(t + 8);
         // masks, running maximum
@@ -408,8 +432,7 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
         f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(wave_m[x][c], pl.c, -Mc));
-            if (wave_m[x][c] == -INFINITY && !(wave_l[x][c] != wave_l[x][c])) continue;  // this wave saw no key of the row
+            const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(wave_m[x][c], pl.c, -Mc));  // 0: it saw no key of the row
             L = __builtin_fmaf(f, wave_l[x][c], L);
             const f32x4 v = *reinterpret_cast<const f32x4*>(lds + x * WAVE_BYTES + (c * OS + d) * 4);
 #pragma unroll
@@ -751,57 +774,100 @@ __global__ __launch_bounds__(2 * MANY, 2) void many_rows_kernel(AttentionArgs a,
     }
 }
 
-// Joins the parts of a row tile: four rows a workgroup, a wave a row, four neighbouring d a lane; bound by reading the
-// parts' sums.
-constexpr int JOIN_ROWS = 4;
-template <bool F16, int DP, int BM>
+// Joins the parts of a row tile: THREADS threads a row, each with four neighbouring d of every SUBS-th part, eight parts
+// on their way at a time.  What it takes is the chain of loads, not their bytes: with a wave a row and one part after
+// the other it took 62 of 84 us for a token against 16,000 keys in 125 parts.
+template <bool F16, int DP, int BM, int THREADS>
 __global__ __launch_bounds__(256) void join_kernel(AttentionArgs a, Plan pl) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int G = a.H / a.Hkv;
+    constexpr int SHARE = 256 / THREADS, PER = DP / 4, SUBS = THREADS / PER, PART = BM * (DP + 2), AHEAD = 8;
+    __shared__ float factor[SHARE][256], most[4], total[4];
+    __shared__ __align__(16) f32x4 sums[256];
+    const int tid = threadIdx.x, wave = tid >> 6, own = tid % THREADS, mine = tid / THREADS;
+    const int G = pl.G;
     const int64_t wg = blockIdx.x;
-    const int c = (int)(wg % (BM / JOIN_ROWS)) * JOIN_ROWS + wave;
-    const int kvh = (int)(wg / (BM / JOIN_ROWS) % a.Hkv);
-    const int64_t tile = wg / (BM / JOIN_ROWS) / a.Hkv;
+    const int c0 = (int)(wg % (BM / SHARE)) * SHARE, kvh = (int)(wg / (BM / SHARE) % a.Hkv);
+    const int64_t tile = wg / (BM / SHARE) / a.Hkv;
     if (a.R == 0) return;
     int r, first;
     if (BM == 16) {
-        r = (int)(tile / pl.per_request);
-        first = (int)(tile % pl.per_request) * BM;
+        r = (uint32_t)tile / (uint32_t)pl.per_request;
+        first = (int)(tile - (int64_t)r * pl.per_request) * BM;
     } else if (!find_tile(a, tile, G, BM, r, first)) {
         return;
     }
     const Rows w = rows_of(a, r, first, BM, G);
-    const int rows = w.n * G, row = first + c;
-    if (row >= rows || rows <= pl.rows_lo || rows > pl.rows_hi) return;
-    const float* wp = a.ws + (tile * a.Hkv + kvh) * pl.splits * (BM * (DP + 2));
+    const int rows = w.n * G, c = c0 + mine, row = first + c;
+    if (first + c0 >= rows || rows <= pl.rows_lo || rows > pl.rows_hi) return;  // none of the workgroup's rows
+    const float* wp = a.ws + (tile * a.Hkv + kvh) * pl.splits * PART;
+    // the parts' maxima and sums, up to 256 / THREADS parts a thread
+    float2 ml[SHARE];
     float M = -INFINITY;
-    for (int s = 0; s < pl.splits; ++s) M = fmaxf(M, wp[s * (BM * (DP + 2)) + BM * DP + 2 * c]);
+#pragma unroll
+    for (int i = 0; i < SHARE; ++i) {
+        const int s = own + i * THREADS;
+        ml[i] = make_float2(-INFINITY, 0.0f);
+        if (s < pl.splits) ml[i] = *reinterpret_cast<const float2*>(wp + (int64_t)s * PART + BM * DP + 2 * c);
+        M = fmaxf(M, ml[i].x);
+    }
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) M = fmaxf(M, __shfl_xor(M, x));
+    if (THREADS > 64) {
+        if ((tid & 63) == 0) most[wave] = M;
+        __syncthreads();
+        M = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+    }
     const float Mc = M == -INFINITY ? 0.0f : M;
     float L = 0.0f;
-    f32x4 acc = {0, 0, 0, 0};
-    for (int s = 0; s < pl.splits; ++s) {
-        const float* part = wp + s * (BM * (DP + 2));
-        const float2 ml = *reinterpret_cast<const float2*>(part + BM * DP + 2 * c);
-        if (ml.x == -INFINITY && !(ml.y != ml.y)) continue;  // this part saw no key of the row
-        const float f = __builtin_amdgcn_exp2f(ml.x - Mc);
-        L = __builtin_fmaf(f, ml.y, L);
-        if (4 * lane < DP) {
-            const f32x4 v = *reinterpret_cast<const f32x4*>(part + c * DP + 4 * lane);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(f, v[e], acc[e]);
-        }
+    for (int i = 0; i < SHARE; ++i) {
+        const float f = __builtin_amdgcn_exp2f(ml[i].x - Mc);  // 0 for a part that saw no key of the row
+        factor[mine][own + i * THREADS] = f;
+        L = __builtin_fmaf(f, ml[i].y, L);
     }
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) L += __shfl_xor(L, x);
+    if (THREADS > 64 && (tid & 63) == 0) total[wave] = L;
+    __syncthreads();
+    if (THREADS > 64) L = (total[0] + total[1]) + (total[2] + total[3]);
+    const int d = own % PER * 4, sub = own / PER;
+    f32x4 acc = {0, 0, 0, 0};
+    if (sub < SUBS)
+        for (int s0 = sub; s0 < pl.splits; s0 += SUBS * AHEAD) {
+            f32x4 v[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int s = s0 + i * SUBS;
+                v[i] = *reinterpret_cast<const f32x4*>(wp + (int64_t)(s < pl.splits ? s : 0) * PART + c * DP + d);
+            }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int s = s0 + i * SUBS;
+                if (s < pl.splits) {
+                    const float f = factor[mine][s];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(f, v[i][e], acc[e]);
+                }
+            }
+        }
+    if (SUBS > 1) {
+        sums[tid] = acc;
+        __syncthreads();
+        if (sub == 0)
+#pragma unroll
+            for (int i = 1; i < SUBS; ++i) acc += sums[tid + i * PER];
+    }
+    if (sub != 0 || row >= rows) return;
     const bool none = L == 0.0f;
     const int64_t tk = w.t0 + row / G;
     const int head = kvh * G + row % G;
-    if (4 * lane < a.D) {
+    if (d < a.D) {
         uint16_t b[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) b[e] = from_f32<F16>(none ? 0.0f : acc[e] / L);
-        *reinterpret_cast<uint2*>(a.out + tk * a.o_tok + (int64_t)head * a.o_head + 4 * lane) =
+        *reinterpret_cast<uint2*>(a.out + tk * a.o_tok + (int64_t)head * a.o_head + d) =
             make_uint2(b[0] | (uint32_t)b[1] << 16, b[2] | (uint32_t)b[3] << 16);
     }
-    if (a.lse && lane == 0) a.lse[tk * a.H + head] = none ? -INFINITY : (M + __log2f(L)) * LN2;
+    if (a.lse && d == 0) a.lse[tk * a.H + head] = none ? -INFINITY : (M + __log2f(L)) * LN2;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -821,7 +887,7 @@ int splits_for(int64_t groups, int64_t want, int max_kv, int least_keys) {
     return s < 1 ? 1 : s > 256 ? 256 : (int)s;
 }
 
-Parts divide(int R, int T, int max_q, int max_kv, int H, int Hkv) {
+Parts divide(int R, int T, int max_q, int max_kv, int H, int Hkv, int D) {
     const int64_t G = H / Hkv, rows = max_q * G;
     Parts p{};
     p.few_per_request = (int)((rows < FEW ? rows + 15 : FEW) / 16);
@@ -829,7 +895,10 @@ Parts divide(int R, int T, int max_q, int max_kv, int H, int Hkv) {
     p.few_tiles = (int64_t)p.few_per_request * (R > 0 ? R : 1);
     p.many_tiles = T * G / MANY + R + 1;
     if (rows <= FEW || (int64_t)R * max_q != T) {  // some requests may have few rows
-        p.few_splits = splits_for(p.few_tiles * Hkv, 768, max_kv, 128);
+        // A workgroup per CU, two up to 64 dimensions; D = 128 (64), us: 32 requests of 4,000 keys 31.0 (21.9) at 256
+        // workgroups, 31.4 (19.3) at 512, 33.1 (19.6) at 768; 100 of 9,000: 166 (125), 193 (97), 192 (108).  64 keys at
+        // least: one request of 1,000 keys 10.3 us, at 128 11.7, at 256 14.1.
+        p.few_splits = splits_for(p.few_tiles * Hkv, D <= 64 ? 512 : 256, max_kv, 64);
     }
     if (rows > FEW) {
         const int64_t most = R * ((rows + MANY - 1) / MANY), tiles = most < p.many_tiles ? most : p.many_tiles;
@@ -847,10 +916,10 @@ hipError_t launch_dim(const AttentionArgs& a, Plan pl, const Parts& p, hipStream
         pl.rows_hi = p.many_splits ? FEW : INT32_MAX;
         pl.tiles = p.few_tiles;
         pl.per_request = p.few_per_request;
-        hipLaunchKernelGGL((few_rows_kernel<F16, DP>), dim3((unsigned)(p.few_tiles * a.Hkv), p.few_splits), dim3(256), 0,
+        hipLaunchKernelGGL((few_rows_kernel<F16, DP>), dim3(a.Hkv, (unsigned)p.few_tiles, p.few_splits), dim3(256), 0,
                            st, a, pl);
         if (p.few_splits > 1)
-            hipLaunchKernelGGL((join_kernel<F16, DP, 16>), dim3((unsigned)(p.few_tiles * a.Hkv * (16 / JOIN_ROWS))), dim3(256), 0, st, a, pl);
+            hipLaunchKernelGGL((join_kernel<F16, DP, 16, 256>), dim3((unsigned)(p.few_tiles * a.Hkv * 16)), dim3(256), 0, st, a, pl);
         pl.zero_rest = 0;
     }
     if (p.many_splits) {
@@ -861,8 +930,8 @@ hipError_t launch_dim(const AttentionArgs& a, Plan pl, const Parts& p, hipStream
         hipLaunchKernelGGL((many_rows_kernel<F16, DP, (DP <= 128 ? 64 : 32)>),
                            dim3((unsigned)(p.many_tiles * a.Hkv), p.many_splits), dim3(2 * MANY), 0, st, a, pl);
         if (p.many_splits > 1)
-            hipLaunchKernelGGL((join_kernel<F16, DP, MANY>), dim3((unsigned)(p.many_tiles * a.Hkv * (MANY / JOIN_ROWS))), dim3(256), 0, st, a,
-                               pl);
+            hipLaunchKernelGGL((join_kernel<F16, DP, MANY, 64>), dim3((unsigned)(p.many_tiles * a.Hkv * (MANY / 4))), dim3(256),
+                               0, st, a, pl);
     }
     return hipGetLastError();
 }
@@ -881,7 +950,7 @@ hipError_t launch_type(const AttentionArgs& a, const Plan& pl, const Parts& p, h
 }  // namespace
 
 int64_t attention_ws(int32_t R, int32_t T, int32_t max_q, int32_t max_kv, int32_t H, int32_t Hkv, int32_t D) {
-    const Parts p = divide(R, T, max_q, max_kv, H, Hkv);
+    const Parts p = divide(R, T, max_q, max_kv, H, Hkv, D);
     const int64_t row = padded_dim(D) + 2;
     const int64_t few = p.few_splits > 1 ? p.few_tiles * Hkv * p.few_splits * 16 * row : 0;
     const int64_t many = p.many_splits > 1 ? p.many_tiles * Hkv * p.many_splits * MANY * row : 0;
@@ -898,7 +967,8 @@ hipError_t launch_attention(const AttentionArgs& args, hipStream_t st) {
     while (((int64_t)1 << bits) < a.page) ++bits;
     pl.magic = (uint32_t)((((uint64_t)1 << (31 + bits)) + a.page - 1) / a.page);
     pl.shift = 31 + bits;
-    const Parts p = divide(a.R, a.T, a.max_q, a.max_kv, a.H, a.Hkv);
+    pl.G = a.H / a.Hkv;
+    const Parts p = divide(a.R, a.T, a.max_q, a.max_kv, a.H, a.Hkv, a.D);
     return a.f16 ? launch_type<true>(a, pl, p, st) : launch_type<false>(a, pl, p, st);
 }
 
