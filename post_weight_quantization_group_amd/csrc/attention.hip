@@ -36,6 +36,9 @@ typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
 constexpr int MANY = 256;  // rows of a workgroup of many_rows_kernel
 
+// How far (in powers of two of the weights) the maximum that the weights are taken against may stay behind the true one:
+// the sums' and the weights' relative roundings are the same up to 2^8, and most steps then leave the outputs alone.
+constexpr float LAG = 8.0f;
 constexpr float LN2 = 0.69314718f;
 
 template <bool F16>
@@ -658,22 +661,19 @@ __global__ __launch_bounds__(2 * MANY, 2) void many_rows_kernel(AttentionArgs a,
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
             if (t * BN < wsame_lo || (t + 1) * BN > wsame_hi || missing[kt]) {
-                // key 8 (e / 4) + e % 4 after the lane's first one
-                const int at = t * BN + 32 * kt + 4 * half, lo = see_lo - at, hi = see_hi - at;
-                const uint32_t gone = missing[kt] >> (4 * half);
+                // bit k: the row sees key k of these 32; the lane's are 8 (e / 4) + e % 4 after its first one
+                const int at = t * BN + 32 * kt, lo = min(max(see_lo - at, 0), 32), hi = min(max(see_hi - at, 0), 32);
+                const uint32_t sees = ((uint32_t)(((uint64_t)1 << hi) - 1) & ~(uint32_t)(((uint64_t)1 << lo) - 1) & ~missing[kt]) >> (4 * half);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int k = 8 * (e >> 2) + (e & 3);
-                    if (k < lo || k >= hi || (gone & (1u << k))) s[kt][e] = -INFINITY;
-                }
+                for (int e = 0; e < 16; ++e)
+                    if (!((sees >> (8 * (e >> 2) + (e & 3))) & 1)) s[kt][e] = -INFINITY;
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e) top = fmaxf(top, s[kt][e]);
         }
         const float m_new = fmaxf(m, max_of_halves(top));
-        const float mc = m_new == -INFINITY ? 0.0f : m_new * pl.c;
-        if (__any(m_new > m)) {
-            const float keep = __builtin_amdgcn_exp2f(__builtin_fmaf(m, pl.c, -mc));
+        if (__any((m_new - m) * pl.c > LAG)) {
+            const float keep = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - m_new) * pl.c);  // (before the first key: 0)
             l *= keep;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
@@ -681,14 +681,17 @@ __global__ __launch_bounds__(2 * MANY, 2) void many_rows_kernel(AttentionArgs a,
                 for (int e = 0; e < 16; ++e) o[d][e] *= keep;
             m = m_new;
         }
+        const float mc = m == -INFINITY ? 0.0f : m * pl.c;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 s[kt][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][e], pl.c, -mc));
-                l += s[kt][e];
+                sum[e & 3] += s[kt][e];
             }
         }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
 #pragma unroll
         for (int ss = 0; ss < BN / 16; ++ss) {
             float p[8];
