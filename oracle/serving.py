@@ -100,7 +100,8 @@ def block_map(ctx_len, new_len, free_pages, n_free, block_table, page_size, max_
         for i in range(new):
             p = ctx + i
             page = table[r, p // page_size]
-            slots[tokens + i] = page * page_size + p % page_size if page >= 0 else -1
+            slot = page * page_size + p % page_size
+            slots[tokens + i] = slot if page >= 0 and slot < 1 << 31 else -1
             positions[tokens + i] = p
         tokens += new
         status.append(0)

@@ -85,6 +85,14 @@ def test_one_long_prompt():
     _check([100, 7], [70001, 1], 16, 5000, rng.permutation(4400), max_tokens=70010)
 
 
+@pytest.mark.parametrize("R", [5, 70, 1100])
+def test_sums_past_32_bits(R):
+    """Lengths whose sums pass 2^32, behind requests that fit."""
+    new = [1 << 20, 0] + [1 << 30] * (R - 3) + [1]
+    _check([0] * R, new, 1 << 20, 2047, np.arange(1000), max_tokens=(1 << 20) + 5)
+    _check([(1 << 30) - 1] * R, [1] * R, 1 << 20, 2047, np.arange(50), max_tokens=60)
+
+
 def test_no_requests():
     got = cq.kv_block_map(i32([]), i32([]), i32([1, 2]), i32([2]), torch.zeros((0, 3), dtype=torch.int32, device="cuda"),
                           16, 5)

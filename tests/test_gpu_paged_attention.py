@@ -6,7 +6,7 @@ import torch
 
 import post_weight_quantization_group_amd as cq
 from parity import say
-from serving import Paged, TORCH, close, i32
+from serving import Paged, TORCH, close, i32, t16
 
 pytestmark = pytest.mark.gpu
 
@@ -170,6 +170,49 @@ def test_infinite_and_nan_values_that_are_seen():
     assert torch.isfinite(out[:10, :, 0]).all() and (out[10:20, :, 0] == np.inf).all() and torch.isnan(out[20:, :, 0]).all()
     assert torch.isfinite(out[:30, :, 1]).all() and torch.isnan(out[30:, :, 1]).all()
     assert (out[5:, :, 2] == -np.inf).all() and torch.isfinite(out[:, :, 3:]).all()
+
+
+@pytest.mark.parametrize("R", [66, 150])
+def test_many_requests_of_every_kind(R):
+    """More requests than one search step covers: none, one, few and many new tokens in turn."""
+    rng = np.random.default_rng(R)
+    lens = []
+    for r in range(R):
+        n = [1, 90, 0, 20, 130, 65][r % 6]
+        lens.append((n, n + int(rng.integers(0, 40))))
+    _say("requests", R)
+    Paged(lens, 2, 1, 64, 16, "bf16", seed=R).check(cq)
+    Paged(lens, 2, 2, 128, 16, "f16", seed=R).check(cq, window=37)
+
+
+@pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("lens,window", [([(1, 9000), (2, 70)], 0), ([(1, 6000)], 3000), ([(70, 3000)], 0),
+                                         ([(90, 2600), (1, 5)], 700)])
+def test_parts_of_the_keys(lens, window, D):
+    """Few rows against many keys: divided over workgroups and joined, with pages that are not there and a NaN
+    behind the last key and in front of the window."""
+    _say("parts", lens, window, D)
+    p = Paged(lens, 4, 2, D, 16, "bf16" if D % 128 else "f16", seed=D)
+    p.table_np[0, 3], p.table_np[0, 90], p.table_np[0, 91] = -1, p.kc.shape[0], -7
+    p.table = i32(p.table_np)
+    p.check(cq, window=window)
+
+
+@pytest.mark.parametrize("step", [0.004, 0.03, 0.3, -0.03])
+@pytest.mark.parametrize("lens", [[(1, 700)], [(100, 700)]])
+@pytest.mark.parametrize("D", [64, 256])
+def test_scores_that_climb(D, lens, step):
+    """The maximum moves with every key, by steps below and above what the outputs are rescaled for."""
+    _say("climb", D, lens, step)
+    p = Paged(lens, 2, 1, D, 16, "f16", seed=D)
+    p.q, p.q_np = t16(np.ones(p.q.shape), "f16")
+    pos = np.arange(lens[0][1])
+    rows = (step * pos * D ** -0.5).astype(np.float16).astype(np.float64)
+    page, at = p.table_np[0, pos // 16], pos % 16
+    for i, x in enumerate(rows):
+        p.kc_np[page[i], 0, at[i]] = x
+    p.kc.copy_(torch.from_numpy(p.kc_np).half())
+    p.check(cq)
 
 
 @pytest.mark.parametrize("lens", [[(1, 90), (1, 50)], [(70, 90), (2, 50)]])

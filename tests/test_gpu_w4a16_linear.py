@@ -70,6 +70,12 @@ def test_many_tiles(M, out, inp, kw):
     _check(M, out, inp, **kw)
 
 
+@pytest.mark.parametrize("M", [1280, 1281, 1408, 1409])
+@pytest.mark.parametrize("out,gated", [(2048, False), (1001, True), (1030, True), (2047, False)])
+def test_either_side_of_the_border_between_the_kernels(M, out, gated):
+    _check(M, out, 128, x="f16" if M % 2 else "bf16", gated=gated, act="silu", bias=True, res=True)
+
+
 @pytest.mark.parametrize("M,out", [(1, 64), (30, 33), (300, 65), (4100, 2060), (2049, 4097)])
 @pytest.mark.parametrize("gated", [False, True])
 def test_scales_of_zero_and_of_every_size(M, out, gated):
