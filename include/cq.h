@@ -359,8 +359,9 @@ int32_t cq_w4a16_matmul(const uint16_t *x, const int32_t *qweight, const uint16_
  *        z[m][c] = sum_g s[g][c] sum_{k in g} x[m][k] (u[k][c] - 8) + bias[c],
  *        y[m][o] = act(z[m][o]) + residual[m][o]                        (gated = 0)
  *        y[m][o] = act(z[m][o]) z[m][out + o] + residual[m][o]          (gated = 1)
- * each group's sum in fp32 on the matrix cores (exact products), its scale one fp32 fma, the
- * epilogue in fp32 and one rounding into y's type.
+ * the products exact and summed in fp32 on the matrix cores, the groups' scales applied in fp32, the
+ * epilogue in fp32 and one rounding into y's type.  (Sums may be held divided by a group's scale:
+ * below 2^100 in magnitude, nothing overflows that fp32 can hold.)
  *   x         x_type (CQ_BF16 or CQ_F16) [M] rows of `in`, ldx apart; 16-byte aligned, ldx a
  *             multiple of 8.
  *   qweight   int32 [in/8][cols], scales uint16 [in/128][cols] binary16 bits, as packed by
@@ -433,7 +434,8 @@ int32_t cq_kv_cache_write(const void *k, int64_t k_token_stride, int64_t k_head_
  * over the keys seen; a token that sees none, or belongs to no request, gets out = 0, lse = -inf.
  * What a masked key or value holds (an unwritten slot, an infinity, a NaN) has no effect on the row
  * that does not see it.  Scores, softmax statistics and sums are fp32; the weights are rounded to the
- * 16-bit type for their product with V on the matrix cores.
+ * 16-bit type for their product with V on the matrix cores (against a maximum that may lag by 2^8:
+ * the sums of weights times V stay finite while 2^8 times their sum of magnitudes does).
  *   type              CQ_BF16 or CQ_F16: q, k_cache, v_cache and out.
  *   q, out            [n_tokens][heads][head_dim], strides as given, head_dim contiguous.
  *   k_cache, v_cache  as for cq_kv_cache_write.

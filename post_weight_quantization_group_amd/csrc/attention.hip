@@ -34,6 +34,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
+// Rows of a request up to which few_rows_kernel takes it, one workgroup a part.  32 requests against 2,000 keys (32 heads
+// over 8, D = 128): 32 rows 70 us there and 54 in many_rows_kernel, 64 rows 120 and 56; 4 against 8,000: 41 and 36.
+constexpr int FEW = 16;
 constexpr int MANY = 256;  // rows of a workgroup of many_rows_kernel
 
 // How far (in powers of two of the weights) the maximum that the weights are taken against may stay behind the true one:
@@ -146,7 +149,6 @@ struct Plan {
     int G;            // query heads per key/value head
     int splits;       // parts that a row tile's keys are divided into, over workgroups
     int rows_lo, rows_hi;  // this launch takes the requests with rows_lo < rows <= rows_hi
-    int per_request;       // few rows: row tiles in the grid per request
     int64_t tiles;         // row tiles in the grid, per key/value head
     int zero_rest;         // this launch writes the tokens that belong to no request
 };
@@ -218,36 +220,37 @@ __device__ __forceinline__ float max_of_halves(float x) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// Few rows (generation): a workgroup takes 16 rows and one part of the keys; its four waves take tiles
-// of 32 keys in turn, each with its own running maximum, and join at the end.  Bound by reading K and V:
-// both go from memory to registers in pieces of 16 bytes a lane, the next tile's while this one is
-// worked on; V passes through the wave's own LDS to be transposed, so the waves never wait for each
-// other.
+// Few rows (generation): a workgroup takes a request's rows (at most 16) and one part of the keys; its four waves take
+// tiles of 32 keys in turn, each with its own running maximum, and join at the end.  Bound by reading K and V: both go
+// from memory to registers in pieces of 16 bytes a lane, the next tile's while this one is worked on; V passes through
+// the wave's own LDS to be transposed, so the waves never wait for each other.  64 requests of up to 8,192 keys (32
+// heads over 8, D = 128): 323 us, 5.3 TB/s (a copy of 2 GiB reaches 4.9).  One request of some 400 keys: 7.2 us, of
+// which three loads that wait for each other (lengths, table, keys) take the most, and 4.0 for the join.  Eight waves a
+// workgroup gained nothing (7.0 / 6.8 us for 100 keys, D = 256 12.4 / 9.5).
 template <bool F16, int DP>
 __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl) {
-    constexpr int BM = 16, BN = 32, KS = DP / 32, DT = DP / 16;
+    constexpr int BM = FEW, BN = 32, KS = DP / 32, DT = DP / 16;
     constexpr int VS = DP + ((DP / 2) % 64 == 16 || (DP / 2) % 64 == 48 ? 0 : 32);  // rows 16 banks apart (mod 64)
     constexpr int OS = DP + 4;
     constexpr int WAVE_BYTES = BN * VS * 2 > BM * OS * 4 ? BN * VS * 2 : BM * OS * 4;
     __shared__ __align__(16) uint8_t lds[4 * WAVE_BYTES];
     __shared__ float wave_m[4][BM], wave_l[4][BM];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, quad = lane >> 4;
-    const int G = pl.G, kvh = blockIdx.x, tile = blockIdx.y, split = blockIdx.z;
-    if (pl.zero_rest && tile == 0 && split == 0) zero_rest<F16>(a, kvh);
+    const int G = pl.G, kvh = blockIdx.x, r = blockIdx.y, split = blockIdx.z;
+    if (pl.zero_rest && r == 0 && split == 0) zero_rest<F16>(a, kvh);
     if (a.R == 0) return;
-    const int r = (uint32_t)tile / (uint32_t)pl.per_request, first = (tile - r * pl.per_request) * BM;
-    const Rows w = rows_of(a, r, first, BM, G);
+    const Rows w = rows_of(a, r, 0, BM, G);
     const int rows = w.n * G;
-    if (first >= rows || rows <= pl.rows_lo || rows > pl.rows_hi) return;
+    if (rows <= pl.rows_lo || rows > pl.rows_hi) return;
 
     uint16_t* vl = reinterpret_cast<uint16_t*>(lds + wave * WAVE_BYTES);
-    const int row = first + col, tok = row / G, pos = w.pos0 + tok;
+    const int row = col, tok = row / G, pos = w.pos0 + tok;
     const bool live = row < rows;
     // the keys this lane's row sees: [see_lo, see_hi)
     const int see_hi = !live ? 0 : a.causal ? min(w.kv, pos + 1) : w.kv;
     const int see_lo = a.window ? max(0, pos - a.window + 1) : 0;
-    const int same_hi = a.causal ? min(w.kv, w.pos0 + first / G + 1) : w.kv;  // every live row sees keys in
-    const int same_lo = a.window ? max(0, w.pos0 + min(rows - 1, first + BM - 1) / G - a.window + 1) : 0;  // [same_lo, same_hi)
+    const int same_hi = a.causal ? min(w.kv, w.pos0 + 1) : w.kv;  // every live row sees keys in
+    const int same_lo = a.window ? max(0, w.pos0 + (rows - 1) / G - a.window + 1) : 0;  // [same_lo, same_hi)
 
     int64_t q_at = (int64_t)(w.t0 + tok) * a.q_tok + (int64_t)(kvh * G + row - tok * G) * a.q_head + 8 * quad;
     asm volatile("" : "+v"(q_at));  // worked out once, and not in front of every load
@@ -423,8 +426,8 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
         for (int e = 0; e < 4; ++e) ol[col * OS + 16 * d + 4 * quad + e] = o[d][e];
     if (seen.any()) seen.apply([&](int i, float x) { ol[col * OS + 4 * (i & ~3) + 4 * quad + (i & 3)] += x; });
     __syncthreads();
-    const int live_rows = min(BM, rows - first);
-    const int64_t part = (tile * a.Hkv + kvh) * pl.splits + split;
+    const int live_rows = rows;
+    const int64_t part = ((int64_t)r * a.Hkv + kvh) * pl.splits + split;
     for (int i = tid; i < live_rows * (DP / 4); i += 256) {
         const int c = i / (DP / 4), d = i % (DP / 4) * 4;
         float M = -INFINITY;
@@ -449,7 +452,7 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
                 wp[BM * DP + 2 * c + 1] = L;
             }
         } else {
-            const int rw = first + c;
+            const int rw = c;
             const int64_t tk = w.t0 + rw / G;
             const int head = kvh * G + rw % G;
             const bool none = L == 0.0f;
@@ -495,8 +498,16 @@ __device__ const uint4 zeros[1] = {};  // what a lane reads for a key or a dimen
 
 // ---------------------------------------------------------------------------------------------
 // Many rows (prompts): a workgroup takes 256 rows, 32 per wave (two waves per SIMD); tiles of BN keys and values go from
-// memory straight into LDS for all eight waves, three tiles ahead, one barrier a tile.  Where the
-// rows of the next 512 keys lie is looked up at a time.
+// memory straight into LDS for all eight waves, three tiles ahead, one barrier a tile.  Where the rows of the next 512
+// keys lie is looked up at a time, a key per thread.  64 keys a tile up to 128 dimensions, 32 above, where four tiles of
+// 64 would not fit into LDS (32 at D = 128: 1290 us in place of 784 at the time).
+//
+// Bound by the vector instructions of the softmax beside the matrix instructions: per 256 x 64 scores a SIMD has 64
+// products of 32 cycles and some 460 vector instructions of 4 to 8, which overlap only in part.  2 requests of up to
+// 2,048 tokens against 16,384 keys (32 heads over 8, D = 128): 680 us, 880 TFLOP/s; 32 requests of 256 tokens (8 heads over
+// 2, D = 256): 47 us.  LDS is busy 19 % of the time, without conflicts.  Measured and not kept: 64 rows a wave with one
+// wave per SIMD and the next scores between the exponentials (792 us); 128 rows a workgroup (766); two groups of waves
+// in turns (712 to 740).
 template <bool F16, int DP, int BN>
 __global__ __launch_bounds__(2 * MANY, 2) void many_rows_kernel(AttentionArgs a, Plan pl) {
     constexpr int BM = MANY, KS = DP / 16, DT = DP / 32, KT = BN / 32;
@@ -778,8 +789,9 @@ __global__ __launch_bounds__(2 * MANY, 2) void many_rows_kernel(AttentionArgs a,
 }
 
 // Joins the parts of a row tile: THREADS threads a row, each with four neighbouring d of every SUBS-th part, eight parts
-// on their way at a time.  What it takes is the chain of loads, not their bytes: with a wave a row and one part after
-// the other it took 62 of 84 us for a token against 16,000 keys in 125 parts.
+// on their way at a time.  What it takes is the chain of loads, not their bytes: a token against 16,000 keys in 125 parts
+// (8 heads over 2, D = 128) took 84 us with a wave a row and one part after the other, and takes 12.  A workgroup a row
+// where the rows are few, a wave a row where a tile has 256 of them.
 template <bool F16, int DP, int BM, int THREADS>
 __global__ __launch_bounds__(256) void join_kernel(AttentionArgs a, Plan pl) {
     constexpr int SHARE = 256 / THREADS, PER = DP / 4, SUBS = THREADS / PER, PART = BM * (DP + 2), AHEAD = 8;
@@ -792,9 +804,9 @@ __global__ __launch_bounds__(256) void join_kernel(AttentionArgs a, Plan pl) {
     const int64_t tile = wg / (BM / SHARE) / a.Hkv;
     if (a.R == 0) return;
     int r, first;
-    if (BM == 16) {
-        r = (uint32_t)tile / (uint32_t)pl.per_request;
-        first = (int)(tile - (int64_t)r * pl.per_request) * BM;
+    if (BM == FEW) {
+        r = (int)tile;
+        first = 0;
     } else if (!find_tile(a, tile, G, BM, r, first)) {
         return;
     }
@@ -874,11 +886,9 @@ __global__ __launch_bounds__(256) void join_kernel(AttentionArgs a, Plan pl) {
 }
 
 // ---------------------------------------------------------------------------------------------
-constexpr int FEW = 64;  // requests of at most so many rows go to few_rows_kernel
 
 struct Parts {
     int64_t few_tiles, many_tiles;
-    int few_per_request;
     int few_splits, many_splits;  // 0: not launched
 };
 
@@ -893,9 +903,7 @@ int splits_for(int64_t groups, int64_t want, int max_kv, int least_keys) {
 Parts divide(int R, int T, int max_q, int max_kv, int H, int Hkv, int D) {
     const int64_t G = H / Hkv, rows = max_q * G;
     Parts p{};
-    p.few_per_request = (int)((rows < FEW ? rows + 15 : FEW) / 16);
-    if (p.few_per_request < 1) p.few_per_request = 1;
-    p.few_tiles = (int64_t)p.few_per_request * (R > 0 ? R : 1);
+    p.few_tiles = R > 0 ? R : 1;
     p.many_tiles = T * G / MANY + R + 1;
     if (rows <= FEW || (int64_t)R * max_q != T) {  // some requests may have few rows
         // A workgroup per CU, two up to 64 dimensions; D = 128 (64), us: 32 requests of 4,000 keys 31.0 (21.9) at 256
@@ -905,7 +913,9 @@ Parts divide(int R, int T, int max_q, int max_kv, int H, int Hkv, int D) {
     }
     if (rows > FEW) {
         const int64_t most = R * ((rows + MANY - 1) / MANY), tiles = most < p.many_tiles ? most : p.many_tiles;
-        p.many_splits = splits_for(tiles * Hkv, 256, max_kv, 256);  // a workgroup per CU, no more
+        // A workgroup per CU and no more (D = 128): 32 requests of 16 tokens against 2,000 keys 56 us, at 512 workgroups 88;
+        // 4 of 64 against 8,000 77 and 85.  Parts of 128 or 512 keys at least: the same within 1 %.
+        p.many_splits = splits_for(tiles * Hkv, 256, max_kv, 256);
     }
     return p;
 }
@@ -916,13 +926,13 @@ hipError_t launch_dim(const AttentionArgs& a, Plan pl, const Parts& p, hipStream
     if (p.few_splits) {
         pl.splits = p.few_splits;
         pl.rows_lo = 0;
-        pl.rows_hi = p.many_splits ? FEW : INT32_MAX;
+        pl.rows_hi = FEW;
         pl.tiles = p.few_tiles;
-        pl.per_request = p.few_per_request;
         hipLaunchKernelGGL((few_rows_kernel<F16, DP>), dim3(a.Hkv, (unsigned)p.few_tiles, p.few_splits), dim3(256), 0,
                            st, a, pl);
         if (p.few_splits > 1)
-            hipLaunchKernelGGL((join_kernel<F16, DP, 16, 256>), dim3((unsigned)(p.few_tiles * a.Hkv * 16)), dim3(256), 0, st, a, pl);
+            hipLaunchKernelGGL((join_kernel<F16, DP, FEW, 256>), dim3((unsigned)(p.few_tiles * a.Hkv * FEW)), dim3(256), 0,
+                               st, a, pl);
         pl.zero_rest = 0;
     }
     if (p.many_splits) {
@@ -930,6 +940,7 @@ hipError_t launch_dim(const AttentionArgs& a, Plan pl, const Parts& p, hipStream
         pl.rows_lo = p.few_splits ? FEW : 0;
         pl.rows_hi = INT32_MAX;
         pl.tiles = p.many_tiles;
+        if (p.many_tiles * a.Hkv > UINT32_MAX / (2 * MANY)) return hipErrorInvalidValue;  // threads of a launch
         hipLaunchKernelGGL((many_rows_kernel<F16, DP, (DP <= 128 ? 64 : 32)>),
                            dim3((unsigned)(p.many_tiles * a.Hkv), p.many_splits), dim3(2 * MANY), 0, st, a, pl);
         if (p.many_splits > 1)
@@ -955,7 +966,7 @@ hipError_t launch_type(const AttentionArgs& a, const Plan& pl, const Parts& p, h
 int64_t attention_ws(int32_t R, int32_t T, int32_t max_q, int32_t max_kv, int32_t H, int32_t Hkv, int32_t D) {
     const Parts p = divide(R, T, max_q, max_kv, H, Hkv, D);
     const int64_t row = padded_dim(D) + 2;
-    const int64_t few = p.few_splits > 1 ? p.few_tiles * Hkv * p.few_splits * 16 * row : 0;
+    const int64_t few = p.few_splits > 1 ? p.few_tiles * Hkv * p.few_splits * FEW * row : 0;
     const int64_t many = p.many_splits > 1 ? p.many_tiles * Hkv * p.many_splits * MANY * row : 0;
     return few > many ? few : many;
 }

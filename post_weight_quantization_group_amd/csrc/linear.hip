@@ -4,8 +4,8 @@
 //
 // The products run on the matrix cores, in x's own 16-bit type: the codes u - 8 are exact in both,
 // so are their products with x in fp32, and the sums are fp32.  A qweight word holds eight
-// consecutive k of one column, which is what one lane of the B operand takes: words go from memory to
-// registers and are dequantized there, never through LDS.
+// consecutive k of one column, which is what one lane of the B operand takes: words are dequantized in the
+// registers of the lane that multiplies them.
 //
 // Lane layouts (checked on gfx950).  16x16x32: lane l holds A[l % 16][8 (l / 16) + e], B[8 (l / 16) +
 // e][l % 16], D[4 (l / 16) + r][l % 16].  32x32x16: A[l % 32][8 (l / 32) + e], B likewise,
@@ -122,7 +122,9 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int64_t m, int64_t 
 // Few rows, or few tiles: a workgroup takes 16 MT rows and 4 x 16 columns (gated: 2 x 16 of the gate and
 // the same of the other half), its W waves every W-th group, and their sums join in LDS in the order
 // of the waves.  For one row the weights' words are all there is to read, and each lane reads 16
-// bytes of them at a time (VEC); x comes straight from memory, no wave needs another's.
+// bytes of them at a time (VEC); x comes straight from memory, no wave needs another's.  Bound by the latency of its
+// few rounds of loads: 1 row, 3584 -> 1024 8.0 us (16 waves in place of 8: 7.7); 16 rows, 1024 -> 2 x 3584 gated 5.3
+// (5.5); 203 rows, 4096 -> 809 14.5.
 template <bool F16, int MT, int W, bool VEC>
 __global__ __launch_bounds__(64 * W) void few_rows_linear(LinearArgs a, int col_tiles) {
     __shared__ __align__(16) float sums[W * MT * 16 * 64];
@@ -247,7 +249,9 @@ __global__ __launch_bounds__(64 * W) void few_rows_linear(LinearArgs a, int col_
 //
 // A group's 64 products per wave (32 cycles each) come with 15 instructions per word (240) and 128
 // multiplications: 5.8 vector instructions a product, of which 6 run beside one for nothing where
-// they stand between the products; so the order is written out, slot by slot.
+// they stand between the products; so the order is written out, slot by slot.  8192 rows, 4096 -> 4096 bf16: 268 to 276 us,
+// 1.0 PFLOP/s (the library's product of dense bf16 matrices of these sizes 211); without the loads it took 211, so what
+// bounds it is their issue between the products (all in a row: 290).
 constexpr int BIG_M = 128;
 
 // PAIR: the lane's columns are neighbours (not gated).  WIDE: words move 16 bytes a lane.
@@ -468,6 +472,8 @@ hipError_t launch_type(const LinearArgs& a, hipStream_t st) {
         return hipGetLastError();
     }
     const bool vec = a.gated ? a.out % 2 == 0 && ((uintptr_t)a.qw & 7) == 0 : a.out % 4 == 0 && aligned16;
+    // Rows a tile and waves: 203 rows (4096 -> 809) 14.5 us with 32 rows and 8 waves, 17.3 with 4; 512 rows (4096 -> 4096)
+    // 48 us with 64 rows and 4 waves, 53 with 32 and 8.
     if (a.M <= 16) return few<F16, 1, 8>(a, vec, st);
     if (a.M <= 256) return few<F16, 2, 8>(a, vec, st);
     return few<F16, 4, 4>(a, vec, st);
