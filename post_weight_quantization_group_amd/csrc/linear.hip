@@ -238,7 +238,7 @@ __global__ __launch_bounds__(64 * W) void few_rows_linear(LinearArgs a, int col_
 
 // ---------------------------------------------------------------------------------------------
 // Many rows: a workgroup takes 128 rows and 256 columns (gated: 128 of either half), each of its four
-// waves all rows and 64 columns, as 4 x 2 tiles of 32 x 32.  x and the qweight words go from memory
+// waves all rows and 64 columns, as 4 x T tiles of 32 x 32 (T = 1: half the columns).  x and the qweight words go from memory
 // straight into LDS, a group ahead: x, in two buffers, for all waves; the words for the wave that
 // dequantizes them, which has taken them into registers before the next ones are asked for.
 //
@@ -247,22 +247,23 @@ __global__ __launch_bounds__(64 * W) void few_rows_linear(LinearArgs a, int col_
 // would take another 128 registers and leave one wave per SIMD instead of two.  A scale of 0 leaves the
 // accumulators as they are and masks its codes to 0.
 //
-// A group's 64 products per wave (32 cycles each) come with 15 instructions per word (240) and 128
+// A group's 64 products per wave (32 cycles each, T = 2) come with 15 instructions per word (240) and 128
 // multiplications: 5.8 vector instructions a product, of which 6 run beside one for nothing where
 // they stand between the products; so the order is written out, slot by slot.  8192 rows, 4096 -> 4096 bf16: 268 to 276 us,
 // 1.0 PFLOP/s (the library's product of dense bf16 matrices of these sizes 211); without the loads it took 211, so what
 // bounds it is their issue between the products (all in a row: 290).
 constexpr int BIG_M = 128;
 
-// PAIR: the lane's columns are neighbours (not gated).  WIDE: words move 16 bytes a lane.
-template <bool F16, bool PAIR, bool WIDE>
+// T: column tiles of a wave.  PAIR: its two columns of a lane are neighbours (not gated).  WIDE: words move 16 bytes a lane.
+template <bool F16, int T, bool PAIR, bool WIDE>
 __global__ __launch_bounds__(256, 2) void many_rows_linear(LinearArgs a, int row_tiles, int col_tiles) {
     __shared__ __align__(16) uint16_t xs[2][BIG_M * 128];
-    __shared__ __align__(16) uint32_t words[4][16 * 64];
+    constexpr int COLS = 32 * T, EACH = COLS / 2;  // columns of a wave; gated: of either half
+    __shared__ __align__(16) uint32_t words[4][16 * COLS];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 31,
               half = lane >> 5;
     const int64_t cols = a.gated ? 2 * a.out : a.out;
-    const int per = a.gated ? 128 : 256;  // outputs per workgroup
+    const int per = a.gated ? 4 * EACH : 4 * COLS;  // outputs per workgroup
     // Workgroups go to the eight XCDs in turn: each XCD takes a run of tiles, in bands of 8 row tiles,
     // so that the tiles it works on at a time share rows of x and columns of W in its L2.
     int64_t id = blockIdx.x;
@@ -275,14 +276,17 @@ __global__ __launch_bounds__(256, 2) void many_rows_linear(LinearArgs a, int row
     const int64_t high = row_tiles - band * 8 < 8 ? row_tiles - band * 8 : 8;
     const int64_t rt = band * 8 + in_band % high, ct = in_band / high;
     const int64_t m0 = rt * BIG_M, n0 = ct * per + wave * (per / 4);
-    // Column of slot k of the wave's 64: gated: 32 of the gate, then the same of the other half.  Past the
+    // Column of slot k of the wave's: gated: half of them of the gate, then the same of the other half.  Past the
     // edge: any column in range (WIDE: runs of four that start at a multiple of four, which end with it).
     auto column = [&](int k) {
-        const int64_t o = n0 + (a.gated ? k & 31 : k), edge = WIDE ? a.out - 4 + (k & 3) : a.out - 1;
-        return (o < a.out ? o : edge) + (a.gated && k >= 32 ? a.out : 0);
+        const int64_t o = n0 + (a.gated ? k & (EACH - 1) : k), edge = WIDE ? a.out - 4 + (k & 3) : a.out - 1;
+        return (o < a.out ? o : edge) + (a.gated && k >= EACH ? a.out : 0);
     };
-    const int64_t c[2] = {column(PAIR ? 2 * col : col), column(PAIR ? 2 * col + 1 : 32 + col)};
+    int64_t c[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) c[t] = column(PAIR ? 2 * col + t : 32 * t + col);
     const int groups = (int)(a.in / 128);
+    constexpr int FIRST = 2 * T, APART = T == 1 ? 2 : 3;  // slots of the loads of x
 
     // x tile of a group: 16-byte piece p of row r lies at place p XOR (r % 16) of its row, so that the 16
     // rows a quarter of a wave reads at once lie in different banks.  A wave's load fills 1 KB: four rows.
@@ -294,44 +298,48 @@ __global__ __launch_bounds__(256, 2) void many_rows_linear(LinearArgs a, int row
         xp[i] = a.x + m * a.ldx + 8 * ((lane & 15) ^ (row & 15));
     }
     auto ask_x = [&](int g, int i, int buf) { load_to_lds(xp[i] + (int64_t)g * 128, &xs[buf][(32 * wave + 4 * i) * 128]); };
-    // words: qweight row r of the group in row r of the wave's LDS, its 64 slots in order
-    constexpr int WORD_LOADS = WIDE ? 4 : 16;
-    const int32_t* wp = a.qw + (WIDE ? (lane >> 4) * cols + column(4 * (lane & 15)) : column(lane));
+    // words: qweight row r of the group in row r of the wave's LDS, its slots in order
+    constexpr int A_LOAD = WIDE ? 256 : 64, WORD_LOADS = 16 * COLS / A_LOAD;  // words a load
+    constexpr int LINE = COLS / (WIDE ? 4 : 1), LINES = 64 / LINE;  // lanes a row, rows a load
+    const int32_t* wp = a.qw + lane / LINE * cols + column((WIDE ? 4 : 1) * (lane % LINE));
     auto ask_words = [&](int g, int i) {
-        if constexpr (WIDE) load_to_lds(wp + ((int64_t)g * 16 + 4 * i) * cols, &words[wave][i * 256]);
-        else load_to_lds_4(wp + ((int64_t)g * 16 + i) * cols, &words[wave][i * 64]);
+        const int32_t* from = wp + ((int64_t)g * 16 + LINES * i) * cols;
+        if constexpr (WIDE) load_to_lds(from, &words[wave][i * A_LOAD]);
+        else load_to_lds_4(from, &words[wave][i * A_LOAD]);
     };
     // step ks of a group (k = 16 ks ..) takes qweight row 2 ks + half
-    uint32_t w[8][2];
+    uint32_t w[8][T];
     auto take_words = [&] {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-            const uint32_t* row = &words[wave][(2 * ks + half) * 64];
-            if (PAIR) {
+            const uint32_t* row = &words[wave][(2 * ks + half) * COLS];
+            if constexpr (PAIR) {
                 const uint2 v = *reinterpret_cast<const uint2*>(row + 2 * col);
                 w[ks][0] = v.x; w[ks][1] = v.y;
             } else {
-                w[ks][0] = row[col];
-                w[ks][1] = row[32 + col];
+#pragma unroll
+                for (int t = 0; t < T; ++t) w[ks][t] = row[32 * t + col];
             }
         }
     };
 
-    f32x16 acc[4][2];
+    f32x16 acc[4][T];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < T; ++t)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][t][e] = 0.0f;
 
     // Scales of the group in hand: the ratio the accumulators take on, and the mask of its codes.
-    float s[2] = {1.0f, 1.0f}, ratio[2];
-    uint32_t mask[2];
-    uint16_t sn[2];
+    float s[T], ratio[T];
+    uint32_t mask[T];
+    uint16_t sn[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) s[t] = 1.0f;
     auto take_scales = [&] {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < T; ++t) {
             uint32_t bits = sn[t];
             asm volatile("" : "+v"(bits));  // the wait for it belongs here, not behind its load
             const float sg = scale_of((uint16_t)bits);
@@ -343,7 +351,7 @@ __global__ __launch_bounds__(256, 2) void many_rows_linear(LinearArgs a, int row
     };
     auto scale_tile = [&](int j) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[j / 2][j % 2][e] *= ratio[j % 2];
+        for (int e = 0; e < 16; ++e) acc[j / T][j % T][e] *= ratio[j % T];
     };
 
 #pragma unroll 1
@@ -351,20 +359,20 @@ __global__ __launch_bounds__(256, 2) void many_rows_linear(LinearArgs a, int row
 #pragma unroll
     for (int i = 0; i < 8; ++i) ask_x(0, i, 0);
 #pragma unroll
-    for (int t = 0; t < 2; ++t) sn[t] = a.scales[c[t]];
+    for (int t = 0; t < T; ++t) sn[t] = a.scales[c[t]];
     loaded_to_lds();
     take_words();
     take_scales();
-    uint32_t b[2][4], bn[2][4];  // operands of this step and of the next
+    uint32_t b[T][4], bn[T][4];  // operands of this step and of the next
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 4 * T; ++j)
         b[j / 4][j % 4] = two_codes<F16>(even_codes(w[0][j / 4], mask[j / 4]), odd_codes(w[0][j / 4], mask[j / 4]), j % 4);
     for (int g = 0; g < groups; ++g) {
         const uint16_t* xt = xs[g & 1];
         const int next = g + 1 < groups ? g + 1 : g;  // (the last group asks for its own once more, into the idle buffer)
         __syncthreads();                              // this group's x is in LDS, and the other buffer has been read
 #pragma unroll
-        for (int t = 0; t < 2; ++t) sn[t] = a.scales[(int64_t)next * cols + c[t]];
+        for (int t = 0; t < T; ++t) sn[t] = a.scales[(int64_t)next * cols + c[t]];
         if constexpr (!WIDE) {
 #pragma unroll 1
             for (int i = 0; i < WORD_LOADS; ++i) ask_words(next, i);
@@ -377,23 +385,23 @@ __global__ __launch_bounds__(256, 2) void many_rows_linear(LinearArgs a, int row
 #pragma unroll
         for (int i = 0; i < 4; ++i) read_x(i, 0);
         scale_tile(0);
-        uint32_t even, odd, last[2];
+        uint32_t even, odd, last[T];
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
             if (ks == 6) {
-                last[0] = w[7][0];
-                last[1] = w[7][1];
+#pragma unroll
+                for (int t = 0; t < T; ++t) last[t] = w[7][t];
                 loaded_to_lds<8>();  // (x was asked for after the words)
                 take_words();
             }
             if (ks == 7) take_scales();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int i = j / 2, t = j % 2, slot = 8 * ks + j;
+            for (int j = 0; j < 4 * T; ++j) {
+                const int i = j / T, t = j % T, slot = 4 * T * ks + j;
                 acc[i][t] = mfma32<F16>(x[i], make_uint4(b[t][0], b[t][1], b[t][2], b[t][3]), acc[i][t]);
                 // an operand is read as soon as its register's last product is issued, 6 slots before its own
-                if (t == 1 && ks < 7) read_x(i, ks + 1);
-                if (ks == 0 && j < 7) scale_tile(j + 1);
+                if (t == T - 1 && ks < 7) read_x(i, ks + 1);
+                if (ks == 0 && j < 4 * T - 1) scale_tile(j + 1);
                 if (j % 4 == 0) {
                     const uint32_t word = ks == 6 ? last[j / 4] : w[(ks + 1) % 8][j / 4];
                     even = even_codes(word, mask[j / 4]);
@@ -403,11 +411,11 @@ __global__ __launch_bounds__(256, 2) void many_rows_linear(LinearArgs a, int row
                 // The next group's loads, one in a slot: asked for in a row, they hold the wave up (1 KB keeps
                 // the memory pipe for 16 cycles or more).
                 if (WIDE && slot < WORD_LOADS) ask_words(next, slot);
-                else if (slot >= 4 && slot < 28 && slot % 3 == 1) ask_x(next, (slot - 4) / 3, (g + 1) & 1);
+                else if (slot >= FIRST && slot < FIRST + 8 * APART && (slot - FIRST) % APART == 0) ask_x(next, (slot - FIRST) / APART, (g + 1) & 1);
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) b[j / 4][j % 4] = bn[j / 4][j % 4];
+            for (int j = 0; j < 4 * T; ++j) b[j / 4][j % 4] = bn[j / 4][j % 4];
         }
         loaded_to_lds();
     }
@@ -416,26 +424,28 @@ __global__ __launch_bounds__(256, 2) void many_rows_linear(LinearArgs a, int row
     const bool wide = outputs_in_fours(a);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float* tile = reinterpret_cast<float*>(xs[i & 1]);  // [32][256]
+        float* tile = reinterpret_cast<float*>(xs[i & 1]);  // [32][4 COLS]
         if (i == 0) __syncthreads();                        // the last group's x has been read
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            float* to = tile + (8 * (e >> 2) + 4 * half + (e & 3)) * 256 + 64 * wave;
-            const float z0 = acc[i][0][e] * (s[0] * CODE_UNIT), z1 = acc[i][1][e] * (s[1] * CODE_UNIT);
-            if (PAIR) {
-                *reinterpret_cast<float2*>(to + 2 * col) = make_float2(z0, z1);
+            float* to = tile + (8 * (e >> 2) + 4 * half + (e & 3)) * (4 * COLS) + COLS * wave;
+            float z[T];
+#pragma unroll
+            for (int t = 0; t < T; ++t) z[t] = acc[i][t][e] * (s[t] * CODE_UNIT);
+            if constexpr (PAIR) {
+                *reinterpret_cast<float2*>(to + 2 * col) = make_float2(z[0], z[1]);
             } else {
-                to[col] = z0;
-                to[32 + col] = z1;
+#pragma unroll
+                for (int t = 0; t < T; ++t) to[32 * t + col] = z[t];
             }
         }
         __syncthreads();
         const int n = 4 * (tid % (per / 4)), lines = 1024 / per;
-        const int at = a.gated ? (n >> 5) * 64 + (n & 31) : n;
+        const int at = a.gated ? n / EACH * COLS + n % EACH : n;
         for (int row = tid / (per / 4); row < 32; row += lines) {
-            const f32x4 z = *reinterpret_cast<const f32x4*>(tile + row * 256 + at);
+            const f32x4 z = *reinterpret_cast<const f32x4*>(tile + row * (4 * COLS) + at);
             f32x4 up = {0, 0, 0, 0};
-            if (a.gated) up = *reinterpret_cast<const f32x4*>(tile + row * 256 + at + 32);
+            if (a.gated) up = *reinterpret_cast<const f32x4*>(tile + row * (4 * COLS) + at + EACH);
             finish4<F16>(a, m0 + 32 * i + row, ct * per + n, z, up, wide);
         }
     }
@@ -452,28 +462,34 @@ hipError_t few(const LinearArgs& a, bool vec, hipStream_t st) {
     return hipGetLastError();
 }
 
+template <bool F16, int T>
+hipError_t many(const LinearArgs& a, int64_t rt, int64_t ct, hipStream_t st) {
+    if (rt * ct > INT32_MAX) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(rt * ct));
+    const bool wide = a.out % 4 == 0 && ((uintptr_t)a.qw & 15) == 0;
+    if (T == 2 && wide && !a.gated)
+        hipLaunchKernelGGL((many_rows_linear<F16, T, T == 2, true>), grid, dim3(256), 0, st, a, (int)rt, (int)ct);
+    else if (wide)
+        hipLaunchKernelGGL((many_rows_linear<F16, T, false, true>), grid, dim3(256), 0, st, a, (int)rt, (int)ct);
+    else
+        hipLaunchKernelGGL((many_rows_linear<F16, T, false, false>), grid, dim3(256), 0, st, a, (int)rt, (int)ct);
+    return hipGetLastError();
+}
+
 template <bool F16>
 hipError_t launch_type(const LinearArgs& a, hipStream_t st) {
-    const int per = a.gated ? 128 : 256;
-    const int64_t rt = (a.M + BIG_M - 1) / BIG_M, ct = (a.out + per - 1) / per;
+    const int64_t rt = (a.M + BIG_M - 1) / BIG_M, cols = a.gated ? 2 * a.out : a.out;
+    const int64_t ct2 = (cols + 255) / 256, ct1 = (cols + 127) / 128;
     const bool aligned16 = ((uintptr_t)a.qw & 15) == 0;
-    // At 4096 inputs: 64 tiles (512 x 4096) 69 us here and 48 by the other kernel, 128 tiles 70 and 95: this one's time
-    // does not fall with fewer tiles than CUs, the other's does.
-    if (rt * ct >= 88) {
-        if (rt * ct > INT32_MAX) return hipErrorInvalidValue;
-        const dim3 grid((unsigned)(rt * ct));
-        const bool wide = a.out % 4 == 0 && aligned16;
-        if (wide && !a.gated)
-            hipLaunchKernelGGL((many_rows_linear<F16, true, true>), grid, dim3(256), 0, st, a, (int)rt, (int)ct);
-        else if (wide)
-            hipLaunchKernelGGL((many_rows_linear<F16, false, true>), grid, dim3(256), 0, st, a, (int)rt, (int)ct);
-        else
-            hipLaunchKernelGGL((many_rows_linear<F16, false, false>), grid, dim3(256), 0, st, a, (int)rt, (int)ct);
-        return hipGetLastError();
-    }
+    // Columns a workgroup, by 128 x 128 tiles on the chip's 256 CUs (us, 256 | 128 columns): 1024 tiles (4096 x 4096, 4096
+    // inputs) 128 | 138, 896 (2048 x 2 x 3584, 1024) 42.2 | 43.7; 512 (2048 x 4096, 4096) 76 | 73, 256 (1024 x 4096) 71 | 48.
+    // Below, this kernel's time no longer falls and the other's does (128 columns | other kernel): 128 tiles (512 x
+    // 4096, 4096) 47 | 49, (2048 x 1024, 3584) 42 | 45; 64 tiles (256 x 4096, 4096) 42 | 28, (1024 x 1024, 3584) 42 | 23.
+    if (rt * ct1 > 512) return many<F16, 2>(a, rt, ct2, st);
+    if (rt * ct1 >= 112) return many<F16, 1>(a, rt, ct1, st);
     const bool vec = a.gated ? a.out % 2 == 0 && ((uintptr_t)a.qw & 7) == 0 : a.out % 4 == 0 && aligned16;
-    // Rows a tile and waves: 203 rows (4096 -> 809) 14.5 us with 32 rows and 8 waves, 17.3 with 4; 512 rows (4096 -> 4096)
-    // 48 us with 64 rows and 4 waves, 53 with 32 and 8.
+    // Rows a tile and waves: 203 rows (4096 -> 809) 14.5 us with 32 rows and 8 waves, 17.3 with 4; 1024 rows (3584 -> 1024)
+    // 22.7 us with 64 rows and 4 waves, 25.1 with 32 and 8.
     if (a.M <= 16) return few<F16, 1, 8>(a, vec, st);
     if (a.M <= 256) return few<F16, 2, 8>(a, vec, st);
     return few<F16, 4, 4>(a, vec, st);

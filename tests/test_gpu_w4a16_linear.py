@@ -76,6 +76,13 @@ def test_either_side_of_the_border_between_the_kernels(M, out, gated):
     _check(M, out, 128, x="f16" if M % 2 else "bf16", gated=gated, act="silu", bias=True, res=True)
 
 
+@pytest.mark.parametrize("M,out", [(1920, 896), (1921, 896), (2048, 889), (2304, 3456), (2305, 3456), (2433, 3449)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_tiles_of_either_width(M, out, gated):
+    out = out // 2 if gated else out
+    _check(M, out, 384, x="bf16" if M % 2 else "f16", gated=gated, act="gelu", bias=True, y="f32" if gated else None)
+
+
 @pytest.mark.parametrize("M,out", [(1, 64), (30, 33), (300, 65), (4100, 2060), (2049, 4097)])
 @pytest.mark.parametrize("gated", [False, True])
 def test_scales_of_zero_and_of_every_size(M, out, gated):
