@@ -503,7 +503,7 @@ __device__ const uint4 zeros[1] = {};  // what a lane reads for a key or a dimen
 // 64 would not fit into LDS (32 at D = 128: 1290 us in place of 784 at the time).
 //
 // Bound by the vector instructions of the softmax beside the matrix instructions: per 256 x 64 scores a SIMD has 64
-// products of 32 cycles and some 460 vector instructions of 4 to 8, which overlap only in part.  2 requests of up to
+// products of 32 cycles and some 390 vector instructions of 4 to 8, which overlap only in part.  2 requests of up to
 // 2,048 tokens against 16,384 keys (32 heads over 8, D = 128): 680 us, 880 TFLOP/s; 32 requests of 256 tokens (8 heads over
 // 2, D = 256): 47 us.  LDS is busy 19 % of the time, without conflicts.  Measured and not kept: 64 rows a wave with one
 // wave per SIMD and the next scores between the exponentials (792 us); 128 rows a workgroup (766); two groups of waves
