@@ -53,6 +53,7 @@ ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
 MAX_REQUESTS = 4096
 MAX_HEAD_DIM = 256
 _TYPES = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
+_BINARY16 = (torch.int16, torch.float16, torch.uint16)
 _ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH}
 _METHODS = {"exhaustive": EXHAUSTIVE, "candidate": CANDIDATE, "bounded": BOUNDED}
 EXPORTED_SYMBOLS = ("cq_abi_version", "cq_status_string", "cq_workspace_size", "cq_quantize_groups",
@@ -618,7 +619,7 @@ def w4a16_linear(x, qweight, scales, bias=None, residual=None, activation="none"
     columns, then as many others, and y = act(x Wg + bg) * (x Wu + bu) + residual.
 
     x is bfloat16 or float16 [M, in] (rows may be strided: 16-byte aligned, stride a multiple of
-    8), qweight int32 [in/8, cols], scales int16 or float16 [in/128, cols]; bias [cols] and residual
+    8), qweight int32 [in/8, cols], scales int16, uint16 or float16 [in/128, cols]; bias [cols] and residual
     [M, out] have x's type.  activation: "none", "relu", "silu", "gelu" or "gelu_tanh".  The result
     has x's type, or float32 with out_dtype=torch.float32, or goes into ``out`` (which may be the
     residual itself)."""
@@ -629,8 +630,8 @@ def w4a16_linear(x, qweight, scales, bias=None, residual=None, activation="none"
     if qweight.dim() != 2 or qweight.dtype != torch.int32 or qweight.shape[0] * 8 != inp or inp % GROUP:
         raise ValueError("qweight must be int32 [in/8, cols], in a multiple of 128")
     cols = qweight.shape[1]
-    if scales.shape != (inp // GROUP, cols) or scales.element_size() != 2:
-        raise ValueError("scales must be 16-bit [in/128, cols]")
+    if scales.shape != (inp // GROUP, cols) or scales.dtype not in _BINARY16:
+        raise ValueError("scales must be float16, or its bits as int16 or uint16, [in/128, cols]")
     if gated and cols % 2:
         raise ValueError("gated needs an even number of columns")
     n = cols // 2 if gated else cols

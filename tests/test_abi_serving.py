@@ -1,5 +1,6 @@
 """The serving operators' C entry points without a GPU: bad arguments are refused before anything reaches HIP."""
 import pytest
+import torch
 
 import post_weight_quantization_group_amd as cq
 
@@ -26,6 +27,22 @@ def test_linear_rejects_before_launch(kw):
 
 def test_linear_without_rows_or_columns_is_a_no_op():
     assert _linear(M=0, x=None, y=None) == 0 and _linear(out=0, qw=None) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.int32, torch.int8])
+def test_linear_refuses_scales_that_are_not_binary16(dtype):
+    """16 bits of another type (bfloat16) would be read as binary16."""
+    x, qw = torch.zeros((2, 128), dtype=torch.bfloat16), torch.zeros((16, 8), dtype=torch.int32)
+    with pytest.raises(ValueError, match="scales"):
+        cq.w4a16_linear(x, qw, torch.zeros((1, 8), dtype=dtype))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.int16, torch.uint16])
+def test_linear_takes_scales_as_binary16_or_its_bits(dtype):
+    """They pass the check of their type: what is refused on the CPU is where the arrays live."""
+    x, qw = torch.zeros((2, 128), dtype=torch.bfloat16), torch.zeros((16, 8), dtype=torch.int32)
+    with pytest.raises(ValueError, match="GPU"):
+        cq.w4a16_linear(x, qw, torch.zeros((1, 8), dtype=dtype))
 
 
 def _map(**kw):
