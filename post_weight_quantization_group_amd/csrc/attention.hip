@@ -173,6 +173,12 @@ __device__ __forceinline__ bool find_tile(const AttentionArgs& a, int64_t tile, 
     return first >= 0;
 }
 
+// The first key that a token at position pos sees.  A token before position 0 (fewer cached tokens than new ones) counts
+// as at 0, where the answer is 0 too: its own position minus a window of up to 2^31 - 1 would not fit into 32 bits.
+__device__ __forceinline__ int first_seen(const AttentionArgs& a, int pos) {
+    return a.window ? max(0, max(pos, 0) - a.window + 1) : 0;
+}
+
 // One request's rows and keys, as a tile sees them.
 struct Rows {
     int n, kv, pos0;  // new tokens (at most max_q), keys, position of token 0
@@ -190,9 +196,8 @@ __device__ __forceinline__ Rows rows_of(const AttentionArgs& a, int r, int first
     w.n = all < a.max_q ? all : a.max_q;
     const int last = min(w.n * G, first_row + bm) - 1;
     w.key_end = w.kv;
-    w.key_begin = 0;
+    w.key_begin = first_seen(a, w.pos0 + first_row / G);
     if (a.causal) w.key_end = min(w.kv, w.pos0 + last / G + 1);
-    if (a.window) w.key_begin = max(0, w.pos0 + first_row / G - a.window + 1);
     return w;
 }
 
@@ -248,9 +253,9 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
     const bool live = row < rows;
     // the keys this lane's row sees: [see_lo, see_hi)
     const int see_hi = !live ? 0 : a.causal ? min(w.kv, pos + 1) : w.kv;
-    const int see_lo = a.window ? max(0, pos - a.window + 1) : 0;
+    const int see_lo = first_seen(a, pos);
     const int same_hi = a.causal ? min(w.kv, w.pos0 + 1) : w.kv;  // every live row sees keys in
-    const int same_lo = a.window ? max(0, w.pos0 + (rows - 1) / G - a.window + 1) : 0;  // [same_lo, same_hi)
+    const int same_lo = first_seen(a, w.pos0 + (rows - 1) / G);          // [same_lo, same_hi)
 
     int64_t q_at = (int64_t)(w.t0 + tok) * a.q_tok + (int64_t)(kvh * G + row - tok * G) * a.q_head + 8 * quad;
     asm volatile("" : "+v"(q_at));  // worked out once, and not in front of every load
@@ -536,16 +541,16 @@ __global__ __launch_bounds__(2 * MANY, 2) void many_rows_kernel(AttentionArgs a,
     const int row = first + 32 * wave + col, tok = row / G, pos = w.pos0 + tok;
     const bool live = row < rows;
     const int see_hi = !live ? 0 : a.causal ? min(w.kv, pos + 1) : w.kv;
-    const int see_lo = a.window ? max(0, pos - a.window + 1) : 0;
+    const int see_lo = first_seen(a, pos);
     // keys that every row of the workgroup sees, and that every (any) row of the wave sees
     const int last = min(rows, first + BM) - 1;
     const int same_hi = a.causal ? min(w.kv, w.pos0 + first / G + 1) : w.kv;
-    const int same_lo = a.window ? max(0, w.pos0 + last / G - a.window + 1) : 0;
+    const int same_lo = first_seen(a, w.pos0 + last / G);
     const int wfirst = first + 32 * wave, wlast = min(rows - 1, wfirst + 31);
     const int wave_hi = wfirst >= rows ? 0 : a.causal ? min(w.kv, w.pos0 + wlast / G + 1) : w.kv;
-    const int wave_lo = a.window ? max(0, w.pos0 + wfirst / G - a.window + 1) : 0;
+    const int wave_lo = first_seen(a, w.pos0 + wfirst / G);
     const int wsame_hi = a.causal ? min(w.kv, w.pos0 + wfirst / G + 1) : w.kv;
-    const int wsame_lo = a.window ? max(0, w.pos0 + wlast / G - a.window + 1) : 0;
+    const int wsame_lo = first_seen(a, w.pos0 + wlast / G);
 
     const int head = kvh * G + row - tok * G;
     int64_t q_at = (int64_t)(w.t0 + tok) * a.q_tok + (int64_t)head * a.q_head + 8 * half;

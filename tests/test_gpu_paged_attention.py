@@ -103,6 +103,17 @@ def test_no_requests_and_no_tokens():
     assert p.run(cq, q=p.q[:0], cu_q=i32([0, 0])).shape == (0, 2, 64)
 
 
+@pytest.mark.parametrize("window", [(1 << 31) - 1, (1 << 31) - 2, 1 << 30])
+@pytest.mark.parametrize("lens,kv", [([(8, 8), (1, 5)], [3, 5]), ([(200, 200)], [150]), ([(300, 300), (2, 9)], [40, 9])])
+def test_windows_without_an_end(lens, kv, window):
+    """The largest windows equal none, also where the first new tokens stand before position 0."""
+    _say("no end", lens, kv, window)
+    p = Paged(lens, 4, 2, 64, 16, "bf16", seed=len(lens))
+    p.kv_np, p.kv = np.array(kv), i32(kv)
+    p.check(cq, window=window)
+    assert torch.equal(p.run(cq, window=window), p.run(cq))
+
+
 @pytest.mark.parametrize("lens", [[(1, 40), (1, 70)], [(50, 80), (3, 9)]])
 def test_pages_that_are_not_there(lens):
     """Entries outside the pool count as masked, and kv_len past the table's columns is cut there."""
