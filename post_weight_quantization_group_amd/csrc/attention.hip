@@ -206,7 +206,7 @@ __device__ __forceinline__ Rows rows_of(const AttentionArgs& a, int r, int first
 template <bool F16>
 __device__ void zero_rest(const AttentionArgs& a, int kvh) {
     const int G = a.H / a.Hkv;
-    const int begin = a.R > 0 ? a.cu[0] : a.T, end = a.R > 0 ? a.cu[a.R] : a.T;
+    const int begin = a.cu[0], end = a.cu[a.R];  // (no request: equal)
     for (int t = 0; t < a.T; ++t) {
         if (t == begin) t = max(t, end);
         if (t >= a.T) return;
