@@ -150,7 +150,7 @@ struct Plan {
     int splits;       // parts that a row tile's keys are divided into, over workgroups
     int rows_lo, rows_hi;  // this launch takes the requests with rows_lo < rows <= rows_hi
     int64_t tiles;         // row tiles in the grid, per key/value head
-    int zero_rest;         // this launch writes the tokens that belong to no request
+    int zero_rest;         // this launch writes the tokens that belong to no request (workgroups past `splits` only those)
 };
 
 __device__ __forceinline__ int page_of(const Plan& p, int key) {
@@ -201,20 +201,23 @@ __device__ __forceinline__ Rows rows_of(const AttentionArgs& a, int r, int first
     return w;
 }
 
-// Tokens that belong to no request (before the first one's, behind the last one's) get zeros, from the
-// workgroups of the first row tile.
-template <bool F16>
-__device__ void zero_rest(const AttentionArgs& a, int kvh) {
-    const int G = a.H / a.Hkv;
-    const int begin = a.cu[0], end = a.cu[a.R];  // (no request: equal)
-    for (int t = 0; t < a.T; ++t) {
-        if (t == begin) t = max(t, end);
-        if (t >= a.T) return;
-        for (int i = threadIdx.x; i < G * (a.D / 8); i += blockDim.x) {
-            const int h = kvh * G + i / (a.D / 8), d = i % (a.D / 8) * 8;
-            *reinterpret_cast<uint4*>(a.out + t * a.o_tok + (int64_t)h * a.o_head + d) = make_uint4(0, 0, 0, 0);
-            if (a.lse && d == 0) a.lse[(int64_t)t * a.H + h] = -INFINITY;
-        }
+// Tokens that belong to no request (before the first one's, behind the last one's) get zeros: their rows (token and
+// head) go to the grid's workgroups in turn, a piece of 16 bytes per thread.  A step padded to a fixed number of tokens
+// has many of them: a call with 8,192 tokens of which two requests have 2 (32 heads over 8, D = 128, 67 MB of zeros)
+// takes 16 us, without them 13; by one workgroup per key/value head, a token after the other, 1,174.
+template <int DP>
+__device__ __forceinline__ void zero_rest(const AttentionArgs& a) {
+    constexpr int LANES = DP <= 64 ? 8 : DP <= 128 ? 16 : 32;  // a row's
+    const int begin = min(max(a.cu[0], 0), a.T), end = min(max(a.cu[a.R], begin), a.T);  // (no request: equal)
+    const int64_t rows = (int64_t)(begin + a.T - end) * a.H;                               // (below 2^31)
+    if (rows == 0) return;
+    const int64_t wg = blockIdx.x + gridDim.x * (blockIdx.y + (int64_t)gridDim.y * blockIdx.z);
+    const int64_t wgs = (int64_t)gridDim.x * gridDim.y * gridDim.z;
+    const int share = blockDim.x / LANES, d = threadIdx.x % LANES * 8;
+    for (int64_t i = wg * share + threadIdx.x / LANES; i < rows; i += wgs * share) {
+        const int nth = (uint32_t)i / (uint32_t)a.H, h = (uint32_t)i % (uint32_t)a.H, t = nth < begin ? nth : nth - begin + end;
+        if (d < a.D) *reinterpret_cast<uint4*>(a.out + t * a.o_tok + h * a.o_head + d) = make_uint4(0, 0, 0, 0);
+        if (a.lse && d == 0) a.lse[(int64_t)t * a.H + h] = -INFINITY;
     }
 }
 
@@ -242,8 +245,8 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
     __shared__ float wave_m[4][BM], wave_l[4][BM];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, quad = lane >> 4;
     const int G = pl.G, kvh = blockIdx.x, r = blockIdx.y, split = blockIdx.z;
-    if (pl.zero_rest && r == 0 && split == 0) zero_rest<F16>(a, kvh);
-    if (a.R == 0) return;
+    if (pl.zero_rest) zero_rest<DP>(a);
+    if (a.R == 0 || split >= pl.splits) return;
     const Rows w = rows_of(a, r, 0, BM, G);
     const int rows = w.n * G;
     if (rows <= pl.rows_lo || rows > pl.rows_hi) return;
@@ -530,8 +533,8 @@ __global__ __launch_bounds__(2 * MANY, 2) void many_rows_kernel(AttentionArgs a,
     const int kvh = blockIdx.x % a.Hkv;
     const int64_t tile = pl.tiles - 1 - blockIdx.x / a.Hkv;  // the longest rows first
     const int split = blockIdx.y;
-    if (pl.zero_rest && blockIdx.x < (unsigned)a.Hkv && split == 0) zero_rest<F16>(a, kvh);
-    if (a.R == 0) return;
+    if (pl.zero_rest) zero_rest<DP>(a);
+    if (a.R == 0 || split >= pl.splits) return;
     int r, first;
     if (!find_tile(a, tile, G, BM, r, first)) return;
     const Rows w = rows_of(a, r, first, BM, G);
@@ -925,6 +928,15 @@ Parts divide(int R, int T, int max_q, int max_kv, int H, int Hkv, int D) {
     return p;
 }
 
+// Parts to add to a grid of `groups` workgroups a part, so that it can zero all of T tokens in a few steps of each (8
+// rows of 512 threads' pieces or so): none where the grid has the rows of T tokens to work on anyway.
+unsigned parts_to_zero(const AttentionArgs& a, int64_t groups, int parts) {
+    int64_t want = (int64_t)a.T * a.H * a.D / (8 * 8 * 256);
+    if (want > 512) want = 512;
+    const int64_t more = (want + groups - 1) / groups - parts;
+    return more > 0 ? (unsigned)more : 0;
+}
+
 template <bool F16, int DP>
 hipError_t launch_dim(const AttentionArgs& a, Plan pl, const Parts& p, hipStream_t st) {
     pl.zero_rest = 1;
@@ -933,8 +945,9 @@ hipError_t launch_dim(const AttentionArgs& a, Plan pl, const Parts& p, hipStream
         pl.rows_lo = 0;
         pl.rows_hi = FEW;
         pl.tiles = p.few_tiles;
-        hipLaunchKernelGGL((few_rows_kernel<F16, DP>), dim3(a.Hkv, (unsigned)p.few_tiles, p.few_splits), dim3(256), 0,
-                           st, a, pl);
+        const unsigned more = parts_to_zero(a, p.few_tiles * a.Hkv, p.few_splits);
+        hipLaunchKernelGGL((few_rows_kernel<F16, DP>), dim3(a.Hkv, (unsigned)p.few_tiles, p.few_splits + more), dim3(256),
+                           0, st, a, pl);
         if (p.few_splits > 1)
             hipLaunchKernelGGL((join_kernel<F16, DP, FEW, 256>), dim3((unsigned)(p.few_tiles * a.Hkv * FEW)), dim3(256), 0,
                                st, a, pl);
@@ -946,8 +959,9 @@ hipError_t launch_dim(const AttentionArgs& a, Plan pl, const Parts& p, hipStream
         pl.rows_hi = INT32_MAX;
         pl.tiles = p.many_tiles;
         if (p.many_tiles * a.Hkv > UINT32_MAX / (2 * MANY)) return hipErrorInvalidValue;  // threads of a launch
+        const unsigned more = pl.zero_rest ? parts_to_zero(a, p.many_tiles * a.Hkv, p.many_splits) : 0;
         hipLaunchKernelGGL((many_rows_kernel<F16, DP, (DP <= 128 ? 64 : 32)>),
-                           dim3((unsigned)(p.many_tiles * a.Hkv), p.many_splits), dim3(2 * MANY), 0, st, a, pl);
+                           dim3((unsigned)(p.many_tiles * a.Hkv), p.many_splits + more), dim3(2 * MANY), 0, st, a, pl);
         if (p.many_splits > 1)
             hipLaunchKernelGGL((join_kernel<F16, DP, MANY, 64>), dim3((unsigned)(p.many_tiles * a.Hkv * (MANY / 4))), dim3(256),
                                0, st, a, pl);

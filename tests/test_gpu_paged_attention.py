@@ -114,6 +114,57 @@ def test_windows_without_an_end(lens, kv, window):
     assert torch.equal(p.run(cq, window=window), p.run(cq))
 
 
+def _padded(lens, T, front, H, Hkv, D, kind="bf16"):
+    """The requests' tokens from number `front` on among T; the others' queries are NaN."""
+    p = Paged(lens, H, Hkv, D, 16, kind, seed=T)
+    n = p.q.shape[0]
+    q, q_np = torch.full((T, H, D), float("nan"), dtype=p.q.dtype, device="cuda"), np.zeros((T, H, D))
+    q[front:front + n], q_np[front:front + n] = p.q, p.q_np
+    p.q, p.q_np, p.cu_np = q, q_np, p.cu_np + front
+    p.cu = i32(p.cu_np)
+    return p
+
+
+@pytest.mark.parametrize("lens", [[(1, 40), (1, 70)], [(40, 60)], [(90, 100), (1, 500), (0, 3)], [(70, 5000)]])
+@pytest.mark.parametrize("T,front", [(200, 0), (700, 37), (3001, 0), (9000, 4000)])
+@pytest.mark.parametrize("H,Hkv,D", [(8, 2, 128), (5, 1, 80), (3, 3, 256)])
+def test_tokens_of_no_request(lens, T, front, H, Hkv, D):
+    """A step padded to a fixed number of tokens: zeros and -inf in front of the requests' tokens and behind them."""
+    _say("padded", lens, T, front, H, Hkv, D)
+    p = _padded(lens, T, front, H, Hkv, D)
+    wide = torch.full((T, H, D + 8), 3.0, dtype=torch.bfloat16, device="cuda")
+    p.check(cq, out=wide[:, :, :D])
+    assert (wide[:, :, D:] == 3).all()
+
+
+def _least_us(run, calls=10):
+    run()
+    times = []
+    for _ in range(5):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        for _ in range(calls):
+            run()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) * 1000 / calls)
+    return min(times)
+
+
+@pytest.mark.parametrize("lens", [[(1, 40), (1, 70)], [(33, 60)]])
+def test_tokens_of_no_request_cost_their_bytes(lens):
+    """They are zeroed by the whole grid: with 8,192 tokens the call takes a few times its own work and a fill of out
+    (by a workgroup per key/value head it took 50 times that)."""
+    p = _padded(lens, 8192, 0, 32, 8, 128)
+    own = p.q[: sum(n for n, _ in lens)].contiguous()
+    need = max(256, cq.cq_paged_attention_workspace_size(8192, len(lens), p.max_q, p.max_kv, 32, 8, 128))
+    out, ws = torch.empty_like(p.q), torch.empty(need, dtype=torch.uint8, device="cuda")
+    padded = _least_us(lambda: p.run(cq, out=out, workspace=ws))
+    alone, fill = _least_us(lambda: p.run(cq, q=own, out=out[: own.shape[0]], workspace=ws)), _least_us(out.zero_)
+    _say(f"padded {padded:.1f} us, alone {alone:.1f}, fill {fill:.1f}")
+    assert padded < 8 * (alone + fill)
+
+
 @pytest.mark.parametrize("lens", [[(1, 40), (1, 70)], [(50, 80), (3, 9)]])
 def test_pages_that_are_not_there(lens):
     """Entries outside the pool count as masked, and kv_len past the table's columns is cut there."""
