@@ -150,6 +150,7 @@ struct Plan {
     int splits;       // parts that a row tile's keys are divided into, over workgroups
     int rows_lo, rows_hi;  // this launch takes the requests with rows_lo < rows <= rows_hi
     int64_t tiles;         // row tiles in the grid, per key/value head
+    int each;              // many rows: row tiles of every request; 0: as many as it has tokens for
     int zero_rest;         // this launch writes the tokens that belong to no request (workgroups past `splits` only those)
 };
 
@@ -158,8 +159,14 @@ __device__ __forceinline__ int page_of(const Plan& p, int key) {
 }
 
 // Many rows: row tile `tile` of `bm` rows -> its request and its number in it: request r's tiles start at
-// floor(cu[r] G / bm) + r, which leaves room for ceil(n_r G / bm).  Returns false where there is none.
-__device__ __forceinline__ bool find_tile(const AttentionArgs& a, int64_t tile, int G, int bm, int& r, int& first) {
+// floor(cu[r] G / bm) + r, which leaves room for ceil(n_r G / bm), or at `each` r.  Returns false where there is none.
+__device__ __forceinline__ bool find_tile(const AttentionArgs& a, const Plan& pl, int64_t tile, int bm, int& r, int& first) {
+    const int G = pl.G;
+    if (pl.each) {
+        r = (uint32_t)tile / (uint32_t)pl.each;
+        first = ((uint32_t)tile % (uint32_t)pl.each) * bm;
+        return true;
+    }
     int lo = 0;  // the last request whose tiles start at or before `tile`, by 64 probes at a time
     for (int n = a.R; n > 1;) {
         const int step = (n + 63) / 64, lane = threadIdx.x & 63, at = lo + lane * step;
@@ -536,7 +543,7 @@ __global__ __launch_bounds__(2 * MANY, 2) void many_rows_kernel(AttentionArgs a,
     if (pl.zero_rest) zero_rest<DP>(a);
     if (a.R == 0 || split >= pl.splits) return;
     int r, first;
-    if (!find_tile(a, tile, G, BM, r, first)) return;
+    if (!find_tile(a, pl, tile, BM, r, first)) return;
     const Rows w = rows_of(a, r, first, BM, G);
     const int rows = w.n * G;
     if (first >= rows || rows <= pl.rows_lo || rows > pl.rows_hi) return;
@@ -815,7 +822,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttentionArgs a, Plan pl) {
     if (BM == FEW) {
         r = (int)tile;
         first = 0;
-    } else if (!find_tile(a, tile, G, BM, r, first)) {
+    } else if (!find_tile(a, pl, tile, BM, r, first)) {
         return;
     }
     const Rows w = rows_of(a, r, first, BM, G);
@@ -898,6 +905,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttentionArgs a, Plan pl) {
 struct Parts {
     int64_t few_tiles, many_tiles;
     int few_splits, many_splits;  // 0: not launched
+    int many_each;                // Plan::each
 };
 
 int padded_dim(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : D <= 192 ? 192 : 256; }
@@ -912,24 +920,28 @@ Parts divide(int R, int T, int max_q, int max_kv, int H, int Hkv, int D) {
     const int64_t G = H / Hkv, rows = max_q * G;
     Parts p{};
     p.few_tiles = R > 0 ? R : 1;
-    p.many_tiles = T * G / MANY + R + 1;
     if (rows <= FEW || (int64_t)R * max_q != T) {  // some requests may have few rows
         // A workgroup per CU, two up to 64 dimensions; D = 128 (64), us: 32 requests of 4,000 keys 31.0 (21.9) at 256
         // workgroups, 31.4 (19.3) at 512, 33.1 (19.6) at 768; 100 of 9,000: 166 (125), 193 (97), 192 (108).  64 keys at
         // least: one request of 1,000 keys 10.3 us, at 128 11.7, at 256 14.1.
         p.few_splits = splits_for(p.few_tiles * Hkv, D <= 64 ? 512 : 256, max_kv, 64);
     }
-    if (rows > FEW) {
-        const int64_t most = R * ((rows + MANY - 1) / MANY), tiles = most < p.many_tiles ? most : p.many_tiles;
+    if (rows > FEW && R > 0) {
+        // Whichever numbering of the row tiles takes fewer: by the tokens in front of a request, or as many for each as
+        // max_q allows (a step padded to far more tokens than its requests have: 8,192 tokens, one request of 32 at most,
+        // 32 heads over 8: 8 tiles in place of 1,040, and 34 MB of workspace in place of 4.4 GB).
+        const int64_t by_tokens = T * G / MANY + R + 1, each = (rows + MANY - 1) / MANY;
+        p.many_each = R * each <= by_tokens ? (int)each : 0;
+        p.many_tiles = p.many_each ? R * each : by_tokens;
         // A workgroup per CU and no more (D = 128): 32 requests of 16 tokens against 2,000 keys 56 us, at 512 workgroups 88;
         // 4 of 64 against 8,000 77 and 85.  Parts of 128 or 512 keys at least: the same within 1 %.
-        p.many_splits = splits_for(tiles * Hkv, 256, max_kv, 256);
+        p.many_splits = splits_for(p.many_tiles * Hkv, 256, max_kv, 256);
     }
     return p;
 }
 
-// Parts to add to a grid of `groups` workgroups a part, so that it can zero all of T tokens in a few steps of each (8
-// rows of 512 threads' pieces or so): none where the grid has the rows of T tokens to work on anyway.
+// Parts to add to a grid of `groups` workgroups a part, so that it can zero all of T tokens with some 8 pieces a thread:
+// none where the grid has the rows of about T tokens to work on anyway.
 unsigned parts_to_zero(const AttentionArgs& a, int64_t groups, int parts) {
     int64_t want = (int64_t)a.T * a.H * a.D / (8 * 8 * 256);
     if (want > 512) want = 512;
@@ -958,6 +970,7 @@ hipError_t launch_dim(const AttentionArgs& a, Plan pl, const Parts& p, hipStream
         pl.rows_lo = p.few_splits ? FEW : 0;
         pl.rows_hi = INT32_MAX;
         pl.tiles = p.many_tiles;
+        pl.each = p.many_each;
         if (p.many_tiles * a.Hkv > UINT32_MAX / (2 * MANY)) return hipErrorInvalidValue;  // threads of a launch
         const unsigned more = pl.zero_rest ? parts_to_zero(a, p.many_tiles * a.Hkv, p.many_splits) : 0;
         hipLaunchKernelGGL((many_rows_kernel<F16, DP, (DP <= 128 ? 64 : 32)>),

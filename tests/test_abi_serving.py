@@ -114,3 +114,11 @@ def test_attention_workspace():
     assert _attention(n_tokens=0, q=None) == 0
     size = cq.cq_paged_attention_workspace_size
     assert size(-1, 1, 1, 1, 1, 1, 64) == 0 and size(1, 1, 1, 1, 1, 1, 63) == 0 and size(1, 1, 1, 1, 3, 2, 64) == 0
+
+
+@pytest.mark.parametrize("T,R,max_q,max_kv", [(8192, 1, 32, 8192), (8192, 1, 33, 1 << 20), (16384, 8, 64, 4096),
+                                              (1 << 20, 3, 100, 9000), (60, 1, 60, 8192), (8192, 0, 32, 8192)])
+@pytest.mark.parametrize("H,Hkv,D", [(32, 8, 128), (8, 1, 256), (16, 16, 64)])
+def test_attention_workspace_goes_by_the_rows_that_can_exist(T, R, max_q, max_kv, H, Hkv, D):
+    """A step padded to T tokens needs no more than 256 workgroups' rows, D sums and two statistics each."""
+    assert cq.cq_paged_attention_workspace_size(T, R, max_q, max_kv, H, Hkv, D) <= 256 * 256 * (D + 2) * 4

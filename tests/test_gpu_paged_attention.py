@@ -137,6 +137,27 @@ def test_tokens_of_no_request(lens, T, front, H, Hkv, D):
     assert (wide[:, :, D:] == 3).all()
 
 
+@pytest.mark.parametrize("lens", [[(40, 3000), (1, 2000), (90, 2500)], [(90, 700)] * 3 + [(0, 40)], [(300, 900), (20, 30)]])
+@pytest.mark.parametrize("T", [640, 6000])
+def test_parts_and_row_tiles_of_a_padded_step(lens, T):
+    """Row tiles numbered by the tokens in front of a request and by request, with parts of the keys and without."""
+    _say("padded parts", lens, T)
+    _padded(lens, T, 0, 8, 2, 64).check(cq)
+    _padded(lens, T, 100, 4, 4, 128, "f16").check(cq)
+
+
+@pytest.mark.parametrize("n,max_q", [(300, 100), (100, 3), (9, 8)])
+def test_tokens_past_the_bound_are_left(n, max_q):
+    p = Paged([(n, n + 20), (2, 9)], 4, 2, 64, 16, "bf16")
+    want, _, tol, _ = p.want()
+    out = torch.full_like(p.q, 3.0)
+    p.run(cq, max_q=max_q, out=out)
+    torch.cuda.synchronize()
+    rows = [*range(max_q), n, n + 1]
+    close(out[rows], want[rows], tol[rows])
+    assert (out[max_q:n] == 3).all()
+
+
 def _least_us(run, calls=10):
     run()
     times = []
