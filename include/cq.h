@@ -451,7 +451,9 @@ int32_t cq_kv_cache_write(const void *k, int64_t k_token_stride, int64_t k_head_
  *                     NULL).
  * q, k_cache, v_cache and out 16-byte aligned, all strides multiples of 8; head_dim a multiple of 8 up
  * to CQ_MAX_HEAD_DIM; heads a multiple of kv_heads; max_pages * page_size <= 2^30; window > 0 needs
- * causal; scale finite.
+ * causal; scale finite; n_requests and heads < 2^16, n_tokens * heads < 2^31.  CQ_EUNSUPPORTED, with nothing enqueued,
+ * where requests may have more than 16 rows (tokens times heads / kv_heads) and (n_tokens * heads / 256 + (n_requests
+ * + 1) * kv_heads) is 2^23 or more, unless n_requests * ceil(max_q * heads / kv_heads / 256) * kv_heads is less.
  */
 #define CQ_MAX_HEAD_DIM 256
 typedef struct cq_paged_attention_args {

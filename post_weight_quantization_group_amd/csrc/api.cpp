@@ -469,6 +469,8 @@ int32_t cq_paged_attention(const cq_paged_attention_args* args, void* workspace,
     if (!aligned(p.q, 16) || !aligned(p.k_cache, 16) || !aligned(p.v_cache, 16) || !aligned(p.out, 16) ||
         !aligned(p.block_table, 4) || !aligned(p.cu_q, 4) || !aligned(p.kv_len, 4) || !aligned(p.lse, 4))
         return CQ_EINVAL;
+    if (!cqk::attention_fits(p.n_requests, p.n_tokens, p.max_q, p.max_kv, p.heads, p.kv_heads, p.head_dim))
+        return CQ_EUNSUPPORTED;
     const size_t need = cq_paged_attention_workspace_size(p.n_tokens, p.n_requests, p.max_q, p.max_kv, p.heads,
                                                           p.kv_heads, p.head_dim);
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, ALIGN))) return CQ_EWORKSPACE;

@@ -971,7 +971,6 @@ hipError_t launch_dim(const AttentionArgs& a, Plan pl, const Parts& p, hipStream
         pl.rows_hi = INT32_MAX;
         pl.tiles = p.many_tiles;
         pl.each = p.many_each;
-        if (p.many_tiles * a.Hkv > UINT32_MAX / (2 * MANY)) return hipErrorInvalidValue;  // threads of a launch
         const unsigned more = pl.zero_rest ? parts_to_zero(a, p.many_tiles * a.Hkv, p.many_splits) : 0;
         hipLaunchKernelGGL((many_rows_kernel<F16, DP, (DP <= 128 ? 64 : 32)>),
                            dim3((unsigned)(p.many_tiles * a.Hkv), p.many_splits + more), dim3(2 * MANY), 0, st, a, pl);
@@ -994,6 +993,10 @@ hipError_t launch_type(const AttentionArgs& a, const Plan& pl, const Parts& p, h
 }
 
 }  // namespace
+
+bool attention_fits(int32_t R, int32_t T, int32_t max_q, int32_t max_kv, int32_t H, int32_t Hkv, int32_t D) {
+    return divide(R, T, max_q, max_kv, H, Hkv, D).many_tiles * Hkv <= UINT32_MAX / (2 * MANY);
+}
 
 int64_t attention_ws(int32_t R, int32_t T, int32_t max_q, int32_t max_kv, int32_t H, int32_t Hkv, int32_t D) {
     const Parts p = divide(R, T, max_q, max_kv, H, Hkv, D);

@@ -53,6 +53,8 @@ struct AttentionArgs {
     float scale;
     float* ws;
 };
+// Whether the grid for these sizes (its threads numbered in 32 bits) can be launched.
+bool attention_fits(int32_t R, int32_t T, int32_t max_q, int32_t max_kv, int32_t H, int32_t Hkv, int32_t D);
 // Floats of workspace the launch for these sizes uses (0: none).
 int64_t attention_ws(int32_t R, int32_t T, int32_t max_q, int32_t max_kv, int32_t H, int32_t Hkv, int32_t D);
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t st);

@@ -122,3 +122,10 @@ def test_attention_workspace():
 def test_attention_workspace_goes_by_the_rows_that_can_exist(T, R, max_q, max_kv, H, Hkv, D):
     """A step padded to T tokens needs no more than 256 workgroups' rows, D sums and two statistics each."""
     assert cq.cq_paged_attention_workspace_size(T, R, max_q, max_kv, H, Hkv, D) <= 256 * 256 * (D + 2) * 4
+
+
+@pytest.mark.parametrize("kw", [dict(n_requests=65535, heads=256, kv_heads=256, max_q=17),
+                                dict(n_tokens=(1 << 30) - 1, heads=2, kv_heads=2, max_q=(1 << 30) - 1, n_requests=2)])
+def test_attention_grid_too_large_is_refused_before_launch(kw):
+    """More row tiles than a launch can number: refused by the entry point, not by a launch in the middle of the call."""
+    assert _attention(ws=FAKE, ws_bytes=1 << 50, **kw) == -4
