@@ -440,9 +440,11 @@ int32_t cq_kv_cache_write(const void *k, int64_t k_token_stride, int64_t k_head_
  *   q, out            [n_tokens][heads][head_dim], strides as given, head_dim contiguous.
  *   k_cache, v_cache  as for cq_kv_cache_write.
  *   block_table       int32 rows of max_pages, table_stride apart: position j is in page
- *                     block_table[r][j / page_size]; keys of a page outside [0, n_pages) or past
- *                     max_pages count as masked.
- *   cu_q, kv_len      int32 [n_requests + 1], [n_requests], cu_q non-decreasing.
+ *                     block_table[r][j / page_size]; keys of a page outside [0, n_pages) count as
+ *                     masked.
+ *   cu_q, kv_len      int32 [n_requests + 1], [n_requests], cu_q non-decreasing.  A kv_len below 0 is
+ *                     taken as 0, one beyond max_pages * page_size (0 where n_pages is 0) as that: the
+ *                     new tokens are then the last ones of the table's.
  *   max_q, max_kv     bounds of n and kv_len, from the host: they set how the work is divided.  Query
  *                     tokens past max_q are not computed (their out is left as it is); kv_len may
  *                     exceed max_kv, at a loss of speed.

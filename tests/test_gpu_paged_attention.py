@@ -114,6 +114,23 @@ def test_windows_without_an_end(lens, kv, window):
     assert torch.equal(p.run(cq, window=window), p.run(cq))
 
 
+@pytest.mark.parametrize("lens", [[(3, 60), (1, 9)], [(70, 90), (2, 9)]])
+@pytest.mark.parametrize("window", [0, 20])
+def test_lengths_past_the_table_are_those_of_the_table(lens, window):
+    """Positions go by the length cut to the table's room: with several new tokens or a window it shows."""
+    p = Paged(lens, 4, 2, 64, 8, "bf16")
+    room = p.table_np.shape[1] * 8
+    for c, t in ((p.kc_np, p.kc), (p.vc_np, p.vc)):          # the request sees the whole last page
+        t.copy_(torch.nan_to_num(t, nan=0.5))
+        c[np.isnan(c)] = 0.5
+    p.kv_np[0] = room
+    for past in (1, 1000, (1 << 31) - 1 - room):
+        p.kv = i32([room + past, 9])
+        p.check(cq, window=window)
+    p.kv, p.kv_np[1] = i32([room + 1, -5]), 0
+    p.check(cq, window=window)
+
+
 def _padded(lens, T, front, H, Hkv, D, kind="bf16"):
     """The requests' tokens from number `front` on among T; the others' queries are NaN."""
     p = Paged(lens, H, Hkv, D, 16, kind, seed=T)

@@ -106,6 +106,15 @@ def test_attention_empty_rows():
     assert np.all(out[[0, 1, 4, 5]] == 0) and np.all(np.isneginf(lse[[0, 1, 4, 5]])) and np.all(lse[2:4] > -50)
 
 
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 3), (False, 0)])
+def test_attention_lengths_past_the_table_are_those_of_the_table(causal, window):
+    q, kc, vc, table, cu, kv = _attention_inputs(np.random.default_rng(4), [(4, 8), (2, 5)], 2, 1, 8, 4)
+    assert table.shape[1] == 2
+    want = serving.paged_attention(q, kc, vc, table, cu, kv, 1.0, causal, window)[0]
+    got = serving.paged_attention(q, kc, vc, table, cu, np.array([8 + 100, kv[1]]), 1.0, causal, window)[0]
+    assert np.array_equal(got, want)
+
+
 def test_planted_mistakes_exceed_the_bounds():
     """A mask one key too wide, a head group off by one and a nibble order reversed all leave the bounds."""
     rng = np.random.default_rng(3)
