@@ -19,6 +19,10 @@ _erf = np.vectorize(math.erf, otypes=[np.float64])
 _erfc = np.vectorize(math.erfc, otypes=[np.float64])
 
 
+def _tanh_argument(z):
+    return 2.0 * math.sqrt(2.0 / math.pi) * (z + 0.044715 * z ** 3)
+
+
 def activation(z, act):
     z = np.asarray(z, np.float64)
     if act == "none":
@@ -31,7 +35,7 @@ def activation(z, act):
         if act == "gelu":
             return 0.5 * z * _erfc(-z / math.sqrt(2.0))
         if act == "gelu_tanh":
-            return 0.5 * z * (1.0 + np.tanh(math.sqrt(2.0 / math.pi) * (z + 0.044715 * z ** 3)))
+            return z / (1.0 + np.exp(-_tanh_argument(z)))  # (1 + tanh(u / 2)) / 2, without its cancellation
     raise ValueError(act)
 
 

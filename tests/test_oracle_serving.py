@@ -35,6 +35,14 @@ def test_activations_at_known_points():
     assert serving.activation(-2.0, "relu") == 0 and serving.activation(2.0, "relu") == 2
 
 
+def test_tanh_gelu_keeps_its_tail():
+    """z (1 + tanh(u / 2)) / 2 = z / (1 + e^-u), whose value far below 0 is z e^u (1 + tanh itself cancels there)."""
+    for z in (-2.0, -5.0, -7.0, -9.0):
+        u = 2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+        want = z * math.exp(u) / (1 + math.exp(u))
+        assert math.isclose(serving.activation(z, "gelu_tanh"), want, rel_tol=1e-13)
+
+
 def test_gated_takes_the_gate_first():
     codes = np.zeros((2, 128), np.int8)
     codes[0, 0], codes[1, 0] = 3, 5
