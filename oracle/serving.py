@@ -39,6 +39,43 @@ def activation(z, act):
     raise ValueError(act)
 
 
+def _slope(z, ez, act):
+    """Bound of |act'| over [z - ez, z + ez].  Everywhere at most 1.13.  Left of 0 it falls with the value: for
+    g(z) = z S(z), S the sigmoid or the normal distribution function, |g'| <= S + |z| S', where S' is at most S u'
+    (sigmoid of u) or, of the distribution, (|z| + 1 / |z|) S; all grow with z or |z|, taken at their ends."""
+    if act in ("none", "relu"):
+        return np.ones_like(z)
+    hi, far = z + ez, np.abs(z) + ez
+    with np.errstate(over="ignore"):
+        if act == "silu":
+            left = (1.0 + far) / (1.0 + np.exp(-hi))
+        elif act == "gelu":
+            left = (far * far + 2.0) * 0.5 * _erfc(-hi / math.sqrt(2.0))
+        else:
+            left = (1.0 + far * (1.6 + 0.22 * far * far)) / (1.0 + np.exp(-_tanh_argument(hi)))
+    return np.where(hi < 0, np.minimum(left, 1.13), 1.13)
+
+
+def _activation_error(z, y, act):
+    """Bound of the fp32 evaluation's own error at z, y = act(z): each rounding 2^-24, the hardware's exponential
+    2^-23, the tail of the normal distribution 16 units (2^-19).  A relative error of an argument moves the exponential or erfc by that times the
+    argument, left of 0 as much in relative terms of the value:
+      silu       z / (1 + e^-z): two roundings of the exponent, then 8 at most;
+      gelu       z erfc(-z / sqrt 2) / 2: two roundings of the argument, whose factor is at most z^2 + 1;
+      gelu_tanh  z / (1 + e^-u): eight roundings of u, two of the exponent, then 9;
+    and what lies below the smallest normal numbers (e^-88 z and less) may be 0."""
+    if act in ("none", "relu"):
+        return np.zeros_like(z)
+    left = np.maximum(-z, 0.0)
+    if act == "silu":
+        rel = 2.0 ** -24 * (2.0 * left + 8.0)
+    elif act == "gelu":
+        rel = 2.0 ** -19 + 2.0 ** -23 * (left * left + 1.0)
+    else:
+        rel = 2.0 ** -24 * (10.0 * np.maximum(-_tanh_argument(z), 0.0) + 9.0)
+    return rel * np.abs(y) + 2.0 ** -120
+
+
 def w4a16_linear(x, qweight, scales, bias=None, residual=None, act="none", gated=False, out_type="bf16"):
     """(y, tol): x float64 [M, in] holding the 16-bit values, qweight int32 [in/8, cols], scales
     uint16 binary16 bits [in/128, cols].
@@ -48,9 +85,8 @@ def w4a16_linear(x, qweight, scales, bias=None, residual=None, act="none", gated
     31 |x| in size, against which the code's own |u - 8| may be as small as 0), one rounding for the scale and
     one for adding the group, one for the bias:
         |dz| <= 2^-24 ((130 + G) sum |x| |W| + 2 * 130 * sum_g s_g * 31 sum_{k in g} |x|) + 2^-24 |z|.
-    The activations' slope is at most 1.13; their own evaluation is within 2^-19 of their value (exp of an
-    argument of size 17 or less where the sigmoid is not yet saturated) and 2^-22 |z| (1 + erf
-    near -1); then the product with the up half, the residual's sum and the rounding of y."""
+    The activation then has _slope and its own _activation_error; then the product with the up half, the
+    residual's sum and the rounding of y."""
     x = np.asarray(x, np.float64)
     codes, sbits = oracle.unpack_gptq_v1(qweight, scales)      # [cols, in], [cols, in/128]
     s = np.asarray(sbits).view(np.float16).astype(np.float64)
@@ -64,8 +100,7 @@ def w4a16_linear(x, qweight, scales, bias=None, residual=None, act="none", gated
         ez = ez + 2.0 ** -23 * np.abs(z)
     n = z.shape[1] // 2 if gated else z.shape[1]
     y = activation(z[:, :n], act)
-    e = ez[:, :n] if act in ("none", "relu") else \
-        1.13 * ez[:, :n] + 2.0 ** -19 * np.abs(y) + 2.0 ** -22 * np.abs(z[:, :n])
+    e = _slope(z[:, :n], ez[:, :n], act) * ez[:, :n] + _activation_error(z[:, :n], y, act)
     if gated:
         up, eu = z[:, n:], ez[:, n:]
         e = e * np.abs(up) + (np.abs(y) + e) * eu + 2.0 ** -24 * np.abs(y * up)

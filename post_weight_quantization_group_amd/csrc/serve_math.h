@@ -24,11 +24,32 @@ enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4
 // until it underflows.
 __device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
 
+// z N(z), N the normal distribution function: |z| (1 - N(|z|)) is subtracted from z, or is the negative of the value
+// where z < 0 (z (1 + erf(z / sqrt 2)) / 2 cancels there: at -5 a tenth of it is gone, below -5.6 all).  The tail is
+// 1 - N(a) = e^(-a^2 / 2) t p(t), t = 1 / (1 + 0.3 a): what is left of it without the exponential, over t, is smooth in t
+// down to t -> 0, and p is its polynomial of degree 7 by reweighted least squares for a up to 14.5 (relative error
+// 1.7e-7; behind it the exponential is 0).  8192 rows, 1024 -> 4096 with f32 outputs: 106 us, with erfcf
+// 126, with 1 + erff 113.
+__device__ __forceinline__ float gelu(float z) {
+    const float a = fminf(fabsf(z), 20.0f);  // (an infinity times t would be a NaN)
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(a, 0.3f, 1.0f));
+    float p = 0.0354238881f;
+    p = __builtin_fmaf(p, t, -0.156159045f);
+    p = __builtin_fmaf(p, t, 0.204557739f);
+    p = __builtin_fmaf(p, t, -0.0520348236f);
+    p = __builtin_fmaf(p, t, 0.12769216f);
+    p = __builtin_fmaf(p, t, 0.100175842f);
+    p = __builtin_fmaf(p, t, 0.120712151f);
+    p = __builtin_fmaf(p, t, 0.119632006f);
+    const float tail = a * t * (p * __builtin_amdgcn_exp2f(z * z * -0.72134752f));
+    return z < 0.0f ? -tail : z - tail;  // (a NaN stays one)
+}
+
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
     if constexpr (ACT == ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
     if constexpr (ACT == ACT_SILU) return z * sigmoid(z);
-    if constexpr (ACT == ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+    if constexpr (ACT == ACT_GELU) return gelu(z);
     if constexpr (ACT == ACT_GELU_TANH) return z * sigmoid(1.5957691f * (z + 0.044715f * z * z * z));
     return z;
 }

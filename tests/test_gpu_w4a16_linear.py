@@ -54,6 +54,37 @@ def test_epilogues(M, x, y, gated, act):
     _check(M, 136, 512, x, y, act, gated, bias=True, res=True)
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M,out", [(1, 500), (40, 500), (16500, 120)])
+def test_tails_of_the_activations(M, out, gated, act):
+    """x = 0, so the bias alone: arguments down to where an fp32 value of the activation is no longer a normal number
+    keep their relative accuracy."""
+    rng = np.random.default_rng(out)
+    cols = 2 * out if gated else out
+    qw, sc = _weights(rng, cols, 128)
+    z = np.linspace(-11.5 if act == "gelu" else -9.0 if act == "gelu_tanh" else -80.0, 6.0, out)
+    bt, bn = t16(np.concatenate([z, np.full(out, 3.0)]) if gated else z, "bf16")
+    got = cq.w4a16_linear(torch.zeros((M, 128), dtype=torch.bfloat16, device="cuda"), dev(qw), dev(sc.view(np.int16)),
+                          bias=bt, activation=act, gated=gated, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    want, tol = ref.w4a16_linear(np.zeros((M, 128)), qw, sc, bn, None, act, gated, "f32")
+    assert np.all(tol[want != 0] <= 2.0 ** -10 * np.abs(want[want != 0]))
+    close(got, want, tol)
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("M", [1, 16500])
+def test_activations_of_infinity_and_nan(M, act):
+    qw, sc = _weights(np.random.default_rng(1), 4 * 32, 128)
+    bias = torch.tensor([np.inf, np.nan, 60000.0, 3e38] * 32, device="cuda").bfloat16()
+    y = cq.w4a16_linear(torch.zeros((M, 128), dtype=torch.bfloat16, device="cuda"), dev(qw), dev(sc.view(np.int16)),
+                        bias=bias, activation=act, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert (y[:, 0::4] == np.inf).all() and torch.isnan(y[:, 1::4]).all()
+    assert torch.equal(y[:, 2::4], bias[2::4].float().expand(M, -1)) and (y[:, 3::4] > 2.9e38).all()
+
+
 @pytest.mark.parametrize("M,out,inp", [(1, 1024, 3584), (4, 809, 4096), (200, 100, 4096), (1024, 1024, 1024),
                                        (700, 1030, 640)])
 @pytest.mark.parametrize("x", ["bf16", "f16"])

@@ -43,6 +43,26 @@ def test_tanh_gelu_keeps_its_tail():
         assert math.isclose(serving.activation(z, "gelu_tanh"), want, rel_tol=1e-13)
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_slope_bounds_the_differences(act):
+    z = np.concatenate([np.linspace(-12, 6, 4001), np.linspace(-1e-3, 1e-3, 101)])
+    for ez in (1e-9, 1e-4, 0.1, 2.0):
+        s = serving._slope(z, np.full_like(z, ez), act)
+        y = serving.activation(z, act)
+        for dz in (-ez, -ez / 3, ez / 2, ez):
+            assert np.all(np.abs(serving.activation(z + dz, act) - y) <= s * abs(dz) * (1 + 1e-6) + 1e-15 * np.abs(y))
+
+
+@pytest.mark.parametrize("act,lost", [("gelu", lambda z: 0.5 * z * (1 + math.erf(z / math.sqrt(2)))),
+                                      ("gelu_tanh", lambda z: 0.5 * z * (1 + math.tanh(0.7978845608 * (z + 0.044715 * z ** 3))))])
+def test_planted_cancellation_exceeds_the_bound(act, lost):
+    """1 + erf and 1 + tanh in binary32 leave the bound of a negative argument's value."""
+    for z in (-4.0, -5.0, -6.0):
+        want = serving.activation(z, act)
+        bad = np.float32(0.5 * z) * (np.float32(1) + np.float32(lost(z) / (0.5 * z) - 1))
+        assert abs(bad - want) > serving._activation_error(np.array(z), want, act)
+
+
 def test_gated_takes_the_gate_first():
     codes = np.zeros((2, 128), np.int8)
     codes[0, 0], codes[1, 0] = 3, 5
