@@ -76,25 +76,47 @@ def _activation_error(z, y, act):
     return rel * np.abs(y) + 2.0 ** -120
 
 
+def _sum_error(x, W):
+    """(z, bound): z = x W^T and how far fp32 sums of its exact products may be off.
+
+    The matrix cores add blocks of products to a sum: 32 additions a block of 32 and the block's own two roundings,
+    each within 2^-23 (they need not round to nearest) of what the sum or the block can reach, |S| + A with S the sum in
+    front of the block and A the block's sum of |x| |W|.  What is rounded is S itself, in one of two orders: group by
+    group, each group's sum scaled and added (an fma each, and a join of up to 8), or one running sum over all
+    groups, held in units of the group's scale: two roundings more a group for the change of units and two at
+    the end.  The bound is the larger of the two, with 2^-10 of itself for the sums' own deviations."""
+    total, own = (np.zeros((x.shape[0], W.shape[0])) for _ in range(2))  # sums over all groups, over this one
+    blocks = np.zeros_like(total)                                        # sum of A
+    running, within, turns, groups = (np.zeros_like(total) for _ in range(4))
+    for k in range(0, x.shape[1], 32):
+        if k % 128 == 0:
+            turns += np.abs(total)
+            groups += np.abs(own)
+            own[:] = 0
+        running += np.abs(total)
+        within += np.abs(own)
+        blocks += np.abs(x[:, k:k + 32]) @ np.abs(W[:, k:k + 32]).T
+        part = x[:, k:k + 32] @ W[:, k:k + 32].T
+        total += part
+        own += part
+    groups += np.abs(own)
+    G = x.shape[1] // 128
+    chain = 34 * 2.0 ** -23 * (running + blocks) + 2.0 ** -23 * (turns + np.abs(total))
+    apart = 34 * 2.0 ** -23 * (within + blocks) + 2.0 ** -24 * (G + 8) * groups
+    return total, (1 + 2.0 ** -10) * np.maximum(chain, apart)
+
+
 def w4a16_linear(x, qweight, scales, bias=None, residual=None, act="none", gated=False, out_type="bf16"):
     """(y, tol): x float64 [M, in] holding the 16-bit values, qweight int32 [in/8, cols], scales
     uint16 binary16 bits [in/128, cols].
 
-    tol: a group's 128 exact products are summed in fp32 (128 roundings), the codes possibly as
-    16 + u with 24 times the row's sum taken off (its products and partial sums are then at most
-    31 |x| in size, against which the code's own |u - 8| may be as small as 0), one rounding for the scale and
-    one for adding the group, one for the bias:
-        |dz| <= 2^-24 ((130 + G) sum |x| |W| + 2 * 130 * sum_g s_g * 31 sum_{k in g} |x|) + 2^-24 |z|.
-    The activation then has _slope and its own _activation_error; then the product with the up half, the
-    residual's sum and the rounding of y."""
+    tol: _sum_error for z and a rounding for the bias; the activation has _slope and its own _activation_error;
+    then the product with the up half, the residual's sum and the rounding of y."""
     x = np.asarray(x, np.float64)
     codes, sbits = oracle.unpack_gptq_v1(qweight, scales)      # [cols, in], [cols, in/128]
     s = np.asarray(sbits).view(np.float16).astype(np.float64)
     W = codes.astype(np.float64) * np.repeat(s, 128, axis=1)
-    G = x.shape[1] // 128
-    ax = np.abs(x).reshape(x.shape[0], G, 128).sum(2)          # [M, G]
-    z = x @ W.T
-    ez = 2.0 ** -24 * ((130 + G) * (np.abs(x) @ np.abs(W).T) + 260 * 31 * (ax @ np.abs(s).T))
+    z, ez = _sum_error(x, W)
     if bias is not None:
         z = z + bias
         ez = ez + 2.0 ** -23 * np.abs(z)

@@ -159,3 +159,46 @@ def test_planted_mistakes_exceed_the_bounds():
     rev = codes.reshape(16, 32, 8)[:, :, ::-1].reshape(16, 256)
     bad, _ = serving.w4a16_linear(x, *_packed(np.ascontiguousarray(rev), sv))
     assert np.mean(np.abs(bad - y) > tol) > 0.9
+
+
+def _summed_in_fp32(x, codes, sv, chain, inner=np.float32, outer=np.float32):
+    """x W^T as the kernels sum it: blocks of 16 exact products, one rounding a block (``inner``); groups of their own
+    scaled in (``outer``), or one chain in units of the group's scale that is rescaled between groups."""
+    x, codes = x.astype(np.float64), codes.astype(np.float64)
+    s = sv.astype(np.float64)
+    total, acc, last = np.zeros((len(x), len(codes)), outer), np.zeros((len(x), len(codes)), inner), None
+    for g in range(s.shape[1]):
+        if chain and g:
+            ratio = (np.float32(s[:, g - 1]) / np.float32(s[:, g])).astype(np.float32)
+            acc = (acc.astype(np.float64) * ratio).astype(inner)
+        elif not chain:
+            acc = np.zeros_like(acc)
+        for k in range(128 * g, 128 * g + 128, 16):
+            acc = (acc + x[:, k:k + 16] @ codes[:, k:k + 16].T).astype(inner)
+        if not chain:
+            total = (total + acc * s[:, g]).astype(outer)
+    return (acc * s[:, -1]).astype(np.float32) if chain else total
+
+
+@pytest.mark.parametrize("inp", [128, 1024, 4096])
+def test_linear_bound_holds_for_fp32_sums_and_for_no_less(inp):
+    """Both orders of the kernels' sums in fp32 stay within the bound; group sums or running sums held in binary16, a
+    result rounded to binary16 in front of an fp32 store, and one code off by one leave it."""
+    rng = np.random.default_rng(inp)
+    codes = rng.integers(-8, 8, (48, inp)).astype(np.int8)
+    sv = rng.uniform(1e-3, 2e-2, (48, inp // 128)).astype(np.float16)
+    x = np.asarray(rng.standard_normal((64, inp)), np.float16).astype(np.float64)
+    y, tol = serving.w4a16_linear(x, *_packed(codes, sv), out_type="f32")
+
+    def outside(z):
+        return np.mean(np.abs(z - y) > tol)
+
+    for chain in (False, True):
+        assert outside(_summed_in_fp32(x, codes, sv, chain)) == 0
+        assert outside(_summed_in_fp32(x, codes, sv, chain, inner=np.float16)) > 0.2
+    assert outside(_summed_in_fp32(x, codes, sv, False, outer=np.float16)) > 0.2
+    assert outside(y.astype(np.float16).astype(np.float64)) > 0.01
+    off = codes.copy()
+    at = np.arange(48), rng.integers(0, inp, 48)
+    off[at] += np.where(off[at] < 0, 1, -1).astype(np.int8)
+    assert outside(_summed_in_fp32(x, off, sv, False)) > 0.7
