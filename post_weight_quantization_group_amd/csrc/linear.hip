@@ -481,12 +481,17 @@ hipError_t launch_type(const LinearArgs& a, hipStream_t st) {
     const int64_t rt = (a.M + BIG_M - 1) / BIG_M, cols = a.gated ? 2 * a.out : a.out;
     const int64_t ct2 = (cols + 255) / 256, ct1 = (cols + 127) / 128;
     const bool aligned16 = ((uintptr_t)a.qw & 15) == 0;
+    // Up to 32 rows the other kernel reads the words once where this one multiplies 128 rows, and is faster at any width;
+    // up to 64 it reads them twice, and is faster up to 192 tiles (us, the other | 128 columns): 1 row, 4096 -> 16,384
+    // 10.7 | 39, 4096 -> 2 x 14,336 17.5 | 44, 4096 -> 128,256 60 | 144 (256 columns: 131); 32 rows, 4096 -> 16,384 16 | 41,
+    // 128,256 120 | 146 (134); 1024 -> 65,536 24.1 | 25.2; 64 rows, 4096 -> 24,576 43 | 45, 32,768 57 | 46; 1024 -> 24,576
+    // 17.2 | 16.9.  96 rows, 4096 -> 14,592 41 | 45, 18,432 55 | 47.
+    const int64_t least = a.M <= 32 ? (int64_t)1 << 22 : a.M <= 64 ? 193 : 112;  // (2^22: the grid's threads)
     // Columns a workgroup, by 128 x 128 tiles on the chip's 256 CUs (us, 256 | 128 columns): 1024 tiles (4096 x 4096, 4096
     // inputs) 128 | 138, 896 (2048 x 2 x 3584, 1024) 42.2 | 43.7; 512 (2048 x 4096, 4096) 76 | 73, 256 (1024 x 4096) 71 | 48.
     // Below, this kernel's time no longer falls and the other's does (128 columns | other kernel): 128 tiles (512 x
     // 4096, 4096) 47 | 49, (2048 x 1024, 3584) 42 | 45; 64 tiles (256 x 4096, 4096) 42 | 28, (1024 x 1024, 3584) 42 | 23.
-    if (rt * ct1 > 512) return many<F16, 2>(a, rt, ct2, st);
-    if (rt * ct1 >= 112) return many<F16, 1>(a, rt, ct1, st);
+    if (rt * ct1 >= least) return rt * ct1 > 512 ? many<F16, 2>(a, rt, ct2, st) : many<F16, 1>(a, rt, ct1, st);
     const bool vec = a.gated ? a.out % 2 == 0 && ((uintptr_t)a.qw & 7) == 0 : a.out % 4 == 0 && aligned16;
     // Rows a tile and waves: 203 rows (4096 -> 809) 14.5 us with 32 rows and 8 waves, 17.3 with 4; 1024 rows (3584 -> 1024)
     // 22.7 us with 64 rows and 4 waves, 25.1 with 32 and 8.

@@ -114,6 +114,39 @@ def test_tiles_of_either_width(M, out, gated):
     _check(M, out, 384, x="bf16" if M % 2 else "f16", gated=gated, act="gelu", bias=True, y="f32" if gated else None)
 
 
+@pytest.mark.parametrize("M", [1, 32, 33, 64, 65])
+@pytest.mark.parametrize("out,gated", [(14208, False), (14209, False), (14212, False), (7110, True), (24576, False),
+                                       (24580, False), (12289, True), (12290, True)])
+def test_few_rows_and_many_columns(M, out, gated):
+    """Either side of the borders between the kernels at few rows: 111 and 112 tiles, 192 and 193."""
+    _check(M, out, 128, x="f16" if M % 2 else "bf16", gated=gated, act="silu", res=True)
+
+
+@pytest.mark.parametrize("M", [1, 16])
+def test_few_rows_do_not_pay_for_128(M):
+    """Few rows through a wide layer take the kernel that reads its words and little else."""
+    qw = torch.randint(-2 ** 31, 2 ** 31 - 1, (512, 16384), device="cuda").int()
+    sc = torch.rand((32, 16384), device="cuda").half()
+    x = torch.randn((128, 4096), device="cuda").bfloat16()
+    y = torch.empty((128, 16384), device="cuda").bfloat16()
+
+    def least(m):
+        times = []
+        for _ in range(6):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(20):
+                cq.w4a16_linear(x[:m], qw, sc, out=y[:m])
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    few, many = least(M), least(128)
+    say(f"linear: {M} rows {50 * few:.1f} us, 128 rows {50 * many:.1f}")
+    assert few < 0.5 * many
+
+
 @pytest.mark.parametrize("M,out", [(1, 64), (30, 33), (300, 65), (4100, 2060), (2049, 4097)])
 @pytest.mark.parametrize("gated", [False, True])
 def test_scales_of_zero_and_of_every_size(M, out, gated):
