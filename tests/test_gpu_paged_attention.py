@@ -272,6 +272,27 @@ def test_infinite_and_nan_values_that_are_seen():
     assert (out[5:, :, 2] == -np.inf).all() and torch.isfinite(out[:, :, 3:]).all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("lens", [[(60, 60)], [(4, 45)], [(1, 3001)], [(100, 2990)], [(150, 1000), (1, 777)]])
+def test_infinities_and_nans_at_every_head_dimension(lens, D, kind):
+    """Few rows and many, the keys in one part and in several: an infinite value or a NaN reaches the rows that see it,
+    in its own dimension, and nothing else."""
+    _say("special", lens, D, kind)
+    p = Paged(lens, 2, 1, D, 16, kind, seed=D)
+    want, _, tol, _ = p.want()
+    n, kv = lens[0]
+    seen = np.zeros(want.shape, np.int64)  # 1: an infinity, 2: its negative, 3: both or a NaN
+    pos = np.arange(kv - n, kv)[:, None]
+    for at, d, what in ((kv - 1 - n // 2, 0, 1), (kv - 1, D - 1, 2), (kv - 1 - n // 3, D // 2 + 1, 3), (kv // 2, 5, 2),
+                        (kv // 3, 5, 2), (kv - 1 - n // 4, 7, 1), (kv // 2 + 3, 7, 2), (0, D - 3, 1), (kv - 1, D - 6, 3)):
+        p.vc[p.table[0, at // 16].long(), :, at % 16, d] = (np.inf, -np.inf, np.nan)[what - 1]
+        seen[:n, :, d] |= np.where(pos >= at, what, 0)
+    out = p.run(cq).double().cpu().numpy()
+    assert (np.abs(out - want) <= tol)[seen == 0].all()
+    assert (out[seen == 1] == np.inf).all() and (out[seen == 2] == -np.inf).all() and np.isnan(out[seen == 3]).all()
+
+
 @pytest.mark.parametrize("R", [66, 150])
 def test_many_requests_of_every_kind(R):
     """More requests than one search step covers: none, one, few and many new tokens in turn."""

@@ -165,6 +165,13 @@ def test_scales_of_zero_and_of_every_size(M, out, gated):
     close(got, *ref.w4a16_linear(xn, qw, sc, gated=gated, out_type="f32"))
 
 
+@pytest.mark.parametrize("M,out,gated", [(2048, 1030, False), (2048, 1024, False), (2100, 515, True), (2048, 512, True),
+                                         (16, 14400, False), (3, 9000, True)])
+def test_such_scales_at_other_tiles(M, out, gated):
+    """128 columns a workgroup, and few rows of many columns."""
+    test_scales_of_zero_and_of_every_size(M, out, gated)
+
+
 @pytest.mark.parametrize("M", [1, 20, 300])
 def test_rows_with_a_common_offset(M):
     """All activations near 3: the row's sum is 100 times its entries' spread."""
