@@ -2,8 +2,9 @@
 
     python examples/packed_block.py
 
-The weights (random) are quantized with the minimax scales of this library on calibration activations, packed as
-GPTQ-v1 tensors, and run by the serving operators: one block map per step, the q-k-v projection, the cache write,
+The weights (random) are quantized with the minimax scales of this library and packed as GPTQ-v1 tensors, layer by
+layer: each on the activations that the calibration windows have behind the layers packed before it, which the serving
+operators run.  The block is then run by them: one block map per step, the q-k-v projection, the cache write,
 attention over the pages, the output projection with its residual, the gated feed-forward layer.  The result is
 compared with the same block in float32 on the dequantized weights and the whole sequences at once, and a step of
 one token per request is timed, call by call and replayed as a graph.
@@ -54,28 +55,47 @@ class Block:
             return torch.randn(shape, generator=g, device=device)
 
         self.H, self.Hkv, self.D, self.page, self.max_kv = heads, kv_heads, head_dim, page, max_kv
-        calib = rand(4, 64, dim).bfloat16()
-        self.qkv = PackedLinear(rand((heads + 2 * kv_heads) * head_dim, dim) * dim ** -0.5, calib)
-        self.out = PackedLinear(rand(dim, heads * head_dim) * dim ** -0.5, rand(4, 64, heads * head_dim).bfloat16())
-        self.gate_up = PackedLinear(rand(2 * ffn, dim) * dim ** -0.5, calib)
-        self.down = PackedLinear(rand(dim, ffn) * ffn ** -0.5, rand(4, 64, ffn).bfloat16())
         self.k, self.v = (torch.zeros((pages, kv_heads, page, head_dim), dtype=torch.bfloat16, device=device)
                           for _ in range(2))
-        self.table = torch.full((requests, max_kv // page), -1, dtype=torch.int32, device=device)
         self.free = torch.randperm(pages, generator=g, device=device).int()
-        self.n_free = torch.tensor([pages], dtype=torch.int32, device=device)
-        self.ctx = torch.zeros(requests, dtype=torch.int32, device=device)
+        # four environments of a window each, through every layer as soon as it is packed
+        E, n = 4, 64
+        self._requests(E)
+        x = rand(E * n, dim).bfloat16()
+        m = cq.kv_block_map(self.ctx, torch.full_like(self.ctx, n), self.free, self.n_free, self.table, page, E * n)
+        h = F.rms_norm(x, x.shape[-1:])
+        self.qkv = PackedLinear(rand((heads + 2 * kv_heads) * head_dim, dim) * dim ** -0.5, h.view(E, n, -1))
+        a = self._attend(self.qkv(h), m, n)
+        self.out = PackedLinear(rand(dim, heads * head_dim) * dim ** -0.5, a.view(E, n, -1))
+        x = self.out(a, residual=x)
+        h = F.rms_norm(x, x.shape[-1:])
+        self.gate_up = PackedLinear(rand(2 * ffn, dim) * dim ** -0.5, h.view(E, n, -1))
+        h = self.gate_up(h, activation="silu", gated=True)
+        self.down = PackedLinear(rand(dim, ffn) * ffn ** -0.5, h.view(E, n, -1))
+        self._requests(requests)
+
+    def _requests(self, n):
+        """n empty requests, all pages free."""
+        device = self.k.device
+        self.table = torch.full((n, self.max_kv // self.page), -1, dtype=torch.int32, device=device)
+        self.n_free = torch.tensor([self.k.shape[0]], dtype=torch.int32, device=device)
+        self.ctx = torch.zeros(n, dtype=torch.int32, device=device)
+
+    def _attend(self, qkv, m, max_q):
+        """Attention's output [T, heads * D] of the packed rows qkv, whose keys and values go into the cache."""
+        T = qkv.shape[0]
+        qkv = qkv.view(T, self.H + 2 * self.Hkv, self.D)
+        q = rotate(qkv[:, : self.H], m["positions"])
+        k = rotate(qkv[:, self.H: self.H + self.Hkv], m["positions"])
+        cq.kv_cache_write(k, qkv[:, self.H + self.Hkv:], self.k, self.v, m["slots"])
+        return cq.paged_attention(q, self.k, self.v, self.table, m["cu_q"], m["kv_len"], max_q, self.max_kv).view(T, -1)
 
     def step(self, x, new, max_q):
         """x [T, dim] of the requests' new tokens (int32 [R] of them, at most max_q each), packed."""
         T = x.shape[0]
         m = cq.kv_block_map(self.ctx, new, self.free, self.n_free, self.table, self.page, T)
-        qkv = self.qkv(F.rms_norm(x, x.shape[-1:])).view(T, self.H + 2 * self.Hkv, self.D)
-        q = rotate(qkv[:, : self.H], m["positions"])
-        k = rotate(qkv[:, self.H: self.H + self.Hkv], m["positions"])
-        cq.kv_cache_write(k, qkv[:, self.H + self.Hkv:], self.k, self.v, m["slots"])
-        a = cq.paged_attention(q, self.k, self.v, self.table, m["cu_q"], m["kv_len"], max_q, self.max_kv)
-        x = self.out(a.view(T, -1), residual=x)
+        a = self._attend(self.qkv(F.rms_norm(x, x.shape[-1:])), m, max_q)
+        x = self.out(a, residual=x)
         h = self.gate_up(F.rms_norm(x, x.shape[-1:]), activation="silu", gated=True)
         x = self.down(h, residual=x)
         self.ctx.copy_(m["kv_len"])
