@@ -940,10 +940,12 @@ Parts divide(int R, int T, int max_q, int max_kv, int H, int Hkv, int D) {
     return p;
 }
 
-// Parts to add to a grid of `groups` workgroups a part, so that it can zero all of T tokens with some 8 pieces a thread:
-// none where the grid has the rows of about T tokens to work on anyway.
+// Parts to add to a grid of `groups` workgroups a part, so that some 8 pieces a thread zero the tokens that cannot be a
+// request's.  Where all may be one's, the grid has their rows to work on anyway.
 unsigned parts_to_zero(const AttentionArgs& a, int64_t groups, int parts) {
-    int64_t want = (int64_t)a.T * a.H * a.D / (8 * 8 * 256);
+    const int64_t spare = a.T - (int64_t)a.R * a.max_q;
+    if (spare <= 0) return 0;
+    int64_t want = spare * a.H * a.D / (8 * 8 * 256);
     if (want > 512) want = 512;
     const int64_t more = (want + groups - 1) / groups - parts;
     return more > 0 ? (unsigned)more : 0;
