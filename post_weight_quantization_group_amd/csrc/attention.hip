@@ -16,6 +16,11 @@
 // e][l % 32], D[8 (r / 4) + 4 (l / 32) + r % 4][l % 32].  16x16x32: A[l % 16][8 (l / 16) + e], B
 // likewise, D[4 (l / 16) + r][l % 16].
 //
+// The weights are rounded to the 16-bit type for the product with V, which the matrix cores take at 16 times the rate of
+// fp32 operands; scores, maxima, sums (of the weights before that rounding) and outputs are fp32.  Their rounding is of the
+// size of the output's own: relative to 64 bits the outputs are off by 2.1e-3 to 2.3e-3 (bf16; f16 2.5e-4), an fp32
+// evaluation that is rounded at the end by 1.7e-3 (2.0e-4).
+//
 // A masked key has weight 0, and 0 times an infinity or a NaN in V would be a NaN: keys that no row
 // of the tile sees are loaded as zeros, and where a tile's mask differs between its rows, what is not
 // finite in its V is staged as 0 and read again, key by key, into two bits per output (an infinity of
@@ -240,8 +245,9 @@ __device__ __forceinline__ float max_of_halves(float x) {
 // from memory to registers in pieces of 16 bytes a lane, the next tile's while this one is worked on; V passes through
 // the wave's own LDS to be transposed, so the waves never wait for each other.  64 requests of up to 8,192 keys (32
 // heads over 8, D = 128): 323 us, 5.3 TB/s (a copy of 2 GiB reaches 4.9).  One request of some 400 keys: 7.2 us, of
-// which three loads that wait for each other (lengths, table, keys) take the most, and 4.0 for the join.  Eight waves a
-// workgroup gained nothing (7.0 / 6.8 us for 100 keys, D = 256 12.4 / 9.5).
+// which three loads that wait for each other (lengths, table, keys) take the most, and 4.0 for the join.  D = 256 (one wave
+// per SIMD): the same 64 requests 646 us, 5.3 TB/s.  Four waves a workgroup | eight, us: one request of 100 keys 6.5 | 6.6,
+// at D = 256 8.7 | 11.4, the 64 requests at D = 256 646 | 757 (eight spill), at D = 128 and 64 the same.
 template <bool F16, int DP>
 __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl) {
     constexpr int BM = FEW, BN = 32, KS = DP / 32, DT = DP / 16;
@@ -519,8 +525,8 @@ __device__ const uint4 zeros[1] = {};  // what a lane reads for a key or a dimen
 //
 // Bound by the vector instructions of the softmax beside the matrix instructions: per 256 x 64 scores a SIMD has 64
 // products of 32 cycles and some 390 vector instructions of 4 to 8, which overlap only in part.  2 requests of up to
-// 2,048 tokens against 16,384 keys (32 heads over 8, D = 128): 680 us, 880 TFLOP/s; 32 requests of 256 tokens (8 heads over
-// 2, D = 256): 47 us.  LDS is busy 19 % of the time, without conflicts.  Measured and not kept: 64 rows a wave with one
+// 2,048 tokens against 16,384 keys (32 heads over 8, D = 128): 672 to 760 us by the card and its clock, 790 to 890
+// TFLOP/s; 32 requests of 256 tokens (8 heads over 2, D = 256): 44 us.  LDS is busy 19 % of the time, without conflicts.  Measured and not kept: 64 rows a wave with one
 // wave per SIMD and the next scores between the exponentials (792 us); 128 rows a workgroup (766); two groups of waves
 // in turns (712 to 740).
 template <bool F16, int DP, int BN>

@@ -124,7 +124,7 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, int64_t m, int64_t 
 // of the waves.  For one row the weights' words are all there is to read, and each lane reads 16
 // bytes of them at a time (VEC); x comes straight from memory, no wave needs another's.  Bound by the latency of its
 // few rounds of loads: 1 row, 3584 -> 1024 8.0 us (16 waves in place of 8: 7.7); 16 rows, 1024 -> 2 x 3584 gated 5.3
-// (5.5); 203 rows, 4096 -> 809 14.5.
+// (5.5); 203 rows, 4096 -> 809 14.3.  With enough columns by the words' bytes: 1 row, 4096 -> 128,256 59 us, 4.6 TB/s.
 template <bool F16, int MT, int W, bool VEC>
 __global__ __launch_bounds__(64 * W) void few_rows_linear(LinearArgs a, int col_tiles) {
     __shared__ __align__(16) float sums[W * MT * 16 * 64];
@@ -244,13 +244,13 @@ __global__ __launch_bounds__(64 * W) void few_rows_linear(LinearArgs a, int col_
 //
 // The accumulators hold z / s_g: at a group's start they are multiplied by s_{g-1} / s_g, and the
 // matrix cores add the group's products on top.  Sums per group beside them, scaled in by an fma,
-// would take another 128 registers and leave one wave per SIMD instead of two.  A scale of 0 leaves the
-// accumulators as they are and masks its codes to 0.
+// would take another 128 registers and leave one wave per SIMD instead of two.  It costs a group two more
+// fp32 roundings (the ratio and its product).  A scale of 0 leaves the accumulators as they are and masks its codes to 0.
 //
 // A group's 64 products per wave (32 cycles each, T = 2) come with 15 instructions per word (240) and 128
 // multiplications: 5.8 vector instructions a product, of which 6 run beside one for nothing where
-// they stand between the products; so the order is written out, slot by slot.  8192 rows, 4096 -> 4096 bf16: 268 to 276 us,
-// 1.0 PFLOP/s (the library's product of dense bf16 matrices of these sizes 211); without the loads it took 211, so what
+// they stand between the products; so the order is written out, slot by slot.  8192 rows, 4096 -> 4096 bf16: 268 to 305 us by the card
+// and its clock, 0.9 to 1.0 PFLOP/s (the library's product of dense bf16 matrices of these sizes 211); without the loads it took 211, so what
 // bounds it is their issue between the products (all in a row: 290).
 constexpr int BIG_M = 128;
 
