@@ -413,18 +413,12 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
             o[d] = mfma16<F16>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), pb, o[d]);
         }
         if (special) {
-            uint32_t mine = 0;  // which of this lane's keys its row sees
-#pragma unroll
-            for (int e = 7; e >= 0; --e) mine = 2 * mine + !(p[e] == 0.0f);
 #pragma unroll 1
-            for (int k = 0; k < BN; ++k) {
-                const int key = t * BN + k;
-                const uint32_t of = __shfl(mine, col + 16 * ((k & 15) >> 2));
-                if (key < w.key_begin || key >= w.key_end) continue;
+            for (int key = max(t * BN, w.key_begin); key < min((t + 1) * BN, w.key_end); ++key) {
                 const int id = table[page_of(pl, key)];
                 if (id < 0 || id >= a.n_pages) continue;
                 const uint16_t* v = a.vc + id * a.c_page + kvh * a.c_head + (int64_t)(key - page_of(pl, key) * a.page) * a.c_row;
-                if ((of >> (4 * (k >> 4) + (k & 3))) & 1)
+                if (key >= see_lo && key < see_hi)  // (also where its weight is 0)
 #pragma unroll 1
                     for (int d = 0; d < DT; ++d)
                         if (16 * d + 4 * quad < a.D) seen.template add<F16>(d, *reinterpret_cast<const uint2*>(v + 16 * d + 4 * quad));
@@ -740,22 +734,15 @@ __global__ __launch_bounds__(2 * MANY, 2) void many_rows_kernel(AttentionArgs a,
             }
         }
         if (special) {
-            uint32_t mine = 0;  // which of this lane's keys its row sees
-#pragma unroll
-            for (int e = 16 * KT - 1; e >= 0; --e) mine = 2 * mine + !(s[e / 16][e % 16] == 0.0f);
-            const uint32_t theirs = __shfl_xor(mine, 32);
             Special<(16 * DT + 31) / 32> seen = {};
             if (seen_yet) seen = seen_at[tid];
             seen_yet = true;
 #pragma unroll 1
-            for (int k = 0; k < BN; ++k) {
-                const int key = t * BN + k;
-                if (key < w.key_begin || key >= w.key_end) continue;
+            for (int key = max(t * BN, w.key_begin); key < min((t + 1) * BN, w.key_end); ++key) {
                 const int page = table[page_of(pl, key)];
                 if (page < 0 || page >= a.n_pages) continue;
                 const uint16_t* v = a.vc + page * a.c_page + kvh * a.c_head + (int64_t)(key - page_of(pl, key) * a.page) * a.c_row;
-                const uint32_t of = ((k >> 2) & 1) == half ? mine : theirs;
-                if ((of >> (16 * (k >> 5) + 4 * ((k >> 3) & 3) + (k & 3))) & 1)
+                if (key >= see_lo && key < see_hi)  // (also where its weight is 0)
 #pragma unroll 1
                     for (int j = 0; j < 4 * DT; ++j)  // accumulators 4 j .. of the lane: d = 8 j + 4 half ..
                         if (8 * j + 4 * half < a.D) seen.template add<F16>(j, *reinterpret_cast<const uint2*>(v + 8 * j + 4 * half));

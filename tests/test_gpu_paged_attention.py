@@ -293,6 +293,25 @@ def test_infinities_and_nans_at_every_head_dimension(lens, D, kind):
     assert (out[seen == 1] == np.inf).all() and (out[seen == 2] == -np.inf).all() and np.isnan(out[seen == 3]).all()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[(4, 45)], [(60, 60)], [(100, 2990)]])
+def test_nans_seen_with_a_weight_of_nothing(lens, D):
+    """A key whose weight underflows is seen all the same: 0 times a NaN or an infinity is not a number."""
+    _say("weight 0", lens, D)
+    p = Paged(lens, 2, 1, D, 16, "bf16", seed=D)
+    n, kv = lens[0]
+    p.q.fill_(1.0)
+    at = kv - 1 - n // 2                                  # seen from the middle row on, its score 400 below the others
+    p.kc[p.table[0, at // 16].long(), :, at % 16] = -400.0 * D ** -0.5
+    p.vc[p.table[0, at // 16].long(), :, at % 16, :8] = float("nan")
+    p.vc[p.table[0, at // 16].long(), :, at % 16, 8:16] = float("inf")
+    out = p.run(cq)
+    torch.cuda.synchronize()
+    first = at - (kv - n)
+    assert torch.isfinite(out[:first]).all() and torch.isfinite(out[..., 16:]).all()
+    assert torch.isnan(out[first:, :, :8]).all() and not torch.isfinite(out[first:, :, 8:16]).any()
+
+
 @pytest.mark.parametrize("R", [66, 150])
 def test_many_requests_of_every_kind(R):
     """More requests than one search step covers: none, one, few and many new tokens in turn."""
