@@ -185,6 +185,11 @@ def _rows(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+# The helpers on a hot path call themselves with their arrays' GPU current where another one is: the default stream is
+# that of the current GPU, whose kernels would work on another one's memory.
+_device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream_on(stream, device: int):
     """_stream for the helpers on a hot path: the current stream of `device` without building an object."""
     if stream is None and _raw_stream is not None:
@@ -646,6 +651,9 @@ def w4a16_linear(x, qweight, scales, bias=None, residual=None, activation="none"
     if bias is not None:
         _contiguous(bias=bias)
     device = _gpu(x)
+    if device != _device_now():
+        with torch.cuda.device(device):
+            return w4a16_linear(x, qweight, scales, bias, residual, activation, gated, out_dtype, out, stream)
     if out is None:
         out = _empty((M, n), out_dtype or dt, x, stream)
     elif out.shape != (M, n) or (out_dtype is not None and out.dtype != out_dtype):
@@ -675,6 +683,9 @@ def kv_block_map(ctx_len, new_len, free_pages, n_free, block_table, page_size, m
         raise ValueError("ctx_len and new_len must be [R], n_free [1], block_table [R, max_pages]")
     _contiguous(ctx_len=ctx_len, new_len=new_len, free_pages=free_pages)
     device, most = _gpu(ctx_len), block_table.shape[1]
+    if device != _device_now():
+        with torch.cuda.device(device):
+            return kv_block_map(ctx_len, new_len, free_pages, n_free, block_table, page_size, max_tokens, stream)
     sizes = (R + 1, R, max_tokens, max_tokens, R, 1)
     buf = _empty(2 * R + R + 2 + 2 * max_tokens, torch.int32, ctx_len, stream)
     cu, kv, slots, pos, status, left = buf.split_with_sizes(sizes)
@@ -717,6 +728,9 @@ def kv_cache_write(k, v, k_cache, v_cache, slots, stream=None):
         raise ValueError("head_dim must be contiguous")
     _contiguous(slots=slots)
     device = _gpu(k_cache)
+    if device != _device_now():
+        with torch.cuda.device(device):
+            return kv_cache_write(k, v, k_cache, v_cache, slots, stream)
     pk, pv, pkc, pvc, ps = _on(device, ("k", k), ("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("slots", slots))
     _check((_lib or load()).cq_kv_cache_write(pk, _step(k, 0), _step(k, 1), pv, _step(v, 0), _step(v, 1), pkc, pvc,
                                               c_page, c_head, c_row, pages, page, heads, D, ps, T,
@@ -751,6 +765,10 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_k
             raise ValueError("lse must be float32 [T, heads]")
         _contiguous(lse=lse)
     device = _gpu(q)
+    if device != _device_now():
+        with torch.cuda.device(device):
+            return paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_kv, scale, causal, window,
+                                   out, lse, workspace, stream)
     if out is None:
         out = _empty((T, H, D), dt, q, stream)
     elif out.shape != q.shape or out.dtype != dt or out.stride(2) != 1:
