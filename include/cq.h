@@ -484,6 +484,60 @@ int32_t cq_paged_attention(const cq_paged_attention_args *args, void *workspace,
                            void *stream);
 
 /*
+ * Microscaled blocks: 32 neighbouring values with a shared power of two as a byte b (2^(b - 127); 255: all 32 are NaN)
+ * and an element of 4 or 8 bits each.
+ *   CQ_MXFP4  e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives (bit 3), two a byte, the first in the low four bits.
+ *   CQ_MXFP8  e4m3: up to 448 (0x7f, 0xff: NaN), one a byte.
+ * A value is its element times 2^(b - 127).
+ */
+#define CQ_MXFP4 3
+#define CQ_MXFP8 4
+#define CQ_MX_BLOCK 32
+
+/*
+ * Rows of values as microscaled blocks along the row.  With A the largest magnitude of a block, its scale is
+ * 2^(floor(log2 A) - 2) (CQ_MXFP8: - 8), at least 2^-127 (b = 0, also where A = 0), and its elements are the values over
+ * the scale rounded to nearest, ties to the even code, and at most 6 (448) in magnitude.  A block with an infinity or
+ * a NaN becomes NaN (b = 255, codes 0).
+ *   x       x_type (CQ_BF16, CQ_F16 or CQ_F32) [rows] of `len`, ldx elements apart; 16-byte aligned, ldx a multiple of 8.
+ *   codes   out, [rows] of len / 2 bytes (CQ_MXFP8: len), ldc bytes apart; 16-byte aligned, ldc a multiple of 16.
+ *   scales  out, [rows] of len / 32 bytes, lds apart.
+ * len a positive multiple of 32; rows * len < 2^35; rows == 0 enqueues nothing.
+ */
+int32_t cq_mx_quantize(const void *x, int64_t ldx, int32_t x_type, int64_t rows, int64_t len, int32_t format,
+                       uint8_t *codes, int64_t ldc, uint8_t *scales, int64_t lds, void *stream);
+/*
+ * The values that microscaled blocks stand for, rounded once to y_type (what a 16-bit type cannot hold becomes an
+ * infinity or a subnormal number, as the type has it).  Arguments as for cq_mx_quantize, y in x's place.
+ */
+int32_t cq_mx_dequantize(const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t lds, int32_t format,
+                         int64_t rows, int64_t len, void *y, int64_t ldy, int32_t y_type, void *stream);
+
+/*
+ * A paged cache whose keys and values are microscaled blocks along head_dim (a multiple of 32 up to CQ_MAX_HEAD_DIM).
+ *   k_codes, v_codes    [n_pages][kv_heads][page_size] rows of head_dim / 2 bytes (CQ_MXFP8: head_dim), 16-byte aligned:
+ *                       page_stride, head_stride and row_stride bytes apart (multiples of 16, the same for both).
+ *   k_scales, v_scales  [n_pages][kv_heads][page_size] rows of head_dim / 32 bytes: scale_*_stride bytes apart.
+ * Strides >= 0; that the rows do not overlap is the caller's care.
+ */
+typedef struct cq_mx_cache {
+    void *k_codes, *v_codes, *k_scales, *v_scales;
+    int64_t page_stride, head_stride, row_stride;
+    int64_t scale_page_stride, scale_head_stride, scale_row_stride;
+    int32_t format;
+    int32_t n_pages, page_size, kv_heads, head_dim;
+} cq_mx_cache;
+
+/*
+ * New keys and values into the pages of such a cache, each block quantized as by cq_mx_quantize.
+ *   type   CQ_BF16 or CQ_F16, of k and v; they and slots as for cq_kv_cache_write.
+ * n_tokens * kv_heads * head_dim < 2^34.
+ */
+int32_t cq_kv_cache_write_mx(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                             int64_t v_token_stride, int64_t v_head_stride, int32_t type, const cq_mx_cache *cache,
+                             const int32_t *slots, int32_t n_tokens, void *stream);
+
+/*
  * Separately normalized environment diagonals from calibration activations
  * (CliffQuant README, "What CliffQuant changes": each channel's sensitivity
  * weighted by its activations, per calibration environment, each environment

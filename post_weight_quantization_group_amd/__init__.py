@@ -41,6 +41,8 @@ __all__ = [
     "MAX_HEAD_DIM", "PagedAttentionArgs", "cq_w4a16_linear", "w4a16_linear", "cq_kv_block_map", "kv_block_map",
     "cq_kv_cache_write", "kv_cache_write", "cq_paged_attention_workspace_size", "cq_paged_attention",
     "paged_attention",
+    "MXFP4", "MXFP8", "MX_BLOCK", "MxCache", "cq_mx_quantize", "mx_quantize", "cq_mx_dequantize", "mx_dequantize",
+    "cq_kv_cache_write_mx", "kv_cache_write_mx",
 ]
 
 GROUP = 128
@@ -50,10 +52,15 @@ ABSMAX, POOLED_WMSE = 0, 1
 FLAG_BAD_INPUT, FLAG_NEAR_TIE, FLAG_EXACT_TIE, FLAG_FALLBACK, FLAG_FP64_SWEEP = 1, 2, 4, 8, 16
 BF16, F16, F32 = 0, 1, 2
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
+MXFP4, MXFP8 = 3, 4
+MX_BLOCK = 32
 MAX_REQUESTS = 4096
 MAX_HEAD_DIM = 256
 _TYPES = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
 _BINARY16 = (torch.int16, torch.float16, torch.uint16)
+_MX_FORMATS = {"mxfp4": MXFP4, "mxfp8": MXFP8}
+_MX_CODES = (torch.uint8, torch.float8_e4m3fn)
+_MX_SCALES = (torch.uint8, torch.float8_e8m0fnu)
 _ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH}
 _METHODS = {"exhaustive": EXHAUSTIVE, "candidate": CANDIDATE, "bounded": BOUNDED}
 EXPORTED_SYMBOLS = ("cq_abi_version", "cq_status_string", "cq_workspace_size", "cq_quantize_groups",
@@ -64,7 +71,8 @@ EXPORTED_SYMBOLS = ("cq_abi_version", "cq_status_string", "cq_workspace_size", "
                     "cq_proxy_worst_env_wmse", "cq_proxy_worst_env_wmse_multi", "cq_heldout_workspace_size",
                     "cq_heldout_compare", "cq_diagonals_workspace_size", "cq_environment_diagonals",
                     "cq_w4a16_matmul", "cq_probe_valu_fma", "cq_w4a16_linear", "cq_kv_block_map",
-                    "cq_kv_cache_write", "cq_paged_attention_workspace_size", "cq_paged_attention")
+                    "cq_kv_cache_write", "cq_paged_attention_workspace_size", "cq_paged_attention",
+                    "cq_mx_quantize", "cq_mx_dequantize", "cq_kv_cache_write_mx")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lib = None
@@ -86,6 +94,14 @@ class PagedAttentionArgs(ctypes.Structure):
                [(n, ctypes.c_int32) for n in ("type", "n_tokens", "n_requests", "max_q", "max_kv", "heads",
                                               "kv_heads", "head_dim", "page_size", "n_pages", "max_pages",
                                               "causal", "window")] + [("scale", ctypes.c_float)]
+
+
+class MxCache(ctypes.Structure):
+    """cq_mx_cache of cq.h: device pointers as integers, strides in bytes."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scales", "v_scales")] + \
+               [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "row_stride", "scale_page_stride",
+                                              "scale_head_stride", "scale_row_stride")] + \
+               [(n, ctypes.c_int32) for n in ("format", "n_pages", "page_size", "kv_heads", "head_dim")]
 
 
 def library_path() -> str:
@@ -155,6 +171,12 @@ def load():
         lib.cq_paged_attention_workspace_size.argtypes = [I32] * 7
         lib.cq_paged_attention.restype = I32
         lib.cq_paged_attention.argtypes = [ctypes.POINTER(PagedAttentionArgs), P, SZ, P]
+        lib.cq_mx_quantize.restype = I32
+        lib.cq_mx_quantize.argtypes = [P, I64, I32, I64, I64, I32, P, I64, P, I64, P]
+        lib.cq_mx_dequantize.restype = I32
+        lib.cq_mx_dequantize.argtypes = [P, I64, P, I64, I32, I64, I64, P, I64, I32, P]
+        lib.cq_kv_cache_write_mx.restype = I32
+        lib.cq_kv_cache_write_mx.argtypes = [P, I64, I64, P, I64, I64, I32, ctypes.POINTER(MxCache), P, I32, P]
         _lib = lib
     return _lib
 
@@ -406,6 +428,23 @@ def cq_paged_attention_workspace_size(n_tokens: int, n_requests: int, max_q: int
 def cq_paged_attention(args: PagedAttentionArgs, workspace=None, stream=None):
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(load().cq_paged_attention(args, _p(workspace), ws_bytes, _stream(stream)), "cq_paged_attention")
+
+
+def cq_mx_quantize(x, ldx, x_type, rows, length, format, codes, ldc, scales, lds, stream=None):
+    _check(load().cq_mx_quantize(_rows(x), ldx, x_type, rows, length, format, _rows(codes), ldc, _rows(scales), lds,
+                                 _stream(stream)), "cq_mx_quantize")
+
+
+def cq_mx_dequantize(codes, ldc, scales, lds, format, rows, length, y, ldy, y_type, stream=None):
+    _check(load().cq_mx_dequantize(_rows(codes), ldc, _rows(scales), lds, format, rows, length, _rows(y), ldy, y_type,
+                                   _stream(stream)), "cq_mx_dequantize")
+
+
+def cq_kv_cache_write_mx(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, type, cache: MxCache,
+                         slots, n_tokens, stream=None):
+    _check(load().cq_kv_cache_write_mx(_rows(k), k_token_stride, k_head_stride, _rows(v), v_token_stride,
+                                       v_head_stride, type, cache, _p(slots), n_tokens, _stream(stream)),
+           "cq_kv_cache_write_mx")
 
 
 # ---------------------------------------------------------------- helpers
@@ -787,6 +826,138 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_len, max_q, max_k
     _check(lib.cq_paged_attention(args, pw, 0 if workspace is None else workspace.numel() * workspace.element_size(),
                                   _stream_on(stream, device)), "cq_paged_attention")
     return out
+
+
+def _mx_format(format):
+    form = _MX_FORMATS.get(format)
+    if form is None:
+        raise ValueError(f"format must be one of {', '.join(_MX_FORMATS)}")
+    return form
+
+
+def _mx_rows(t, name):
+    """(rows, leading dimension) of an array of rows: contiguous, or a matrix whose rows are."""
+    n = t.shape[-1]
+    if t.is_contiguous():
+        return t.numel() // n, n
+    if t.dim() != 2 or (n > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be contiguous, or a matrix with contiguous rows")
+    return t.shape[0], _ld(t)
+
+
+def mx_quantize(x, format="mxfp4", stream=None):
+    """Values as microscaled blocks of 32 along the last axis: (codes, scales), both uint8.
+
+    x is bfloat16, float16 or float32 [..., n], n a multiple of 32 (contiguous, or a matrix with strided rows: 16-byte
+    aligned, stride a multiple of 8).  format "mxfp4": e2m1 elements, codes [..., n/2] with the first of two in the low
+    four bits; "mxfp8": e4m3, [..., n] (view it as torch.float8_e4m3fn).  scales [..., n/32] hold powers of two with a
+    bias of 127: 2^(floor(log2 of the block's largest magnitude) - 2) (mxfp8: - 8); 255 (NaN) for a block with an
+    infinity or a NaN.  Elements are rounded to nearest even and saturate at 6 (448)."""
+    form = _mx_format(format)
+    if x.dim() < 1 or x.dtype not in _TYPES or x.shape[-1] % MX_BLOCK or not x.shape[-1]:
+        raise ValueError("x must be bfloat16, float16 or float32 [..., n], n a multiple of 32")
+    n = x.shape[-1]
+    rows, ldx = _mx_rows(x, "x")
+    device = _gpu(x)
+    if device != _device_now():
+        with torch.cuda.device(device):
+            return mx_quantize(x, format, stream)
+    width = n // 2 if form == MXFP4 else n
+    codes = _empty(x.shape[:-1] + (width,), torch.uint8, x, stream)
+    scales = _empty(x.shape[:-1] + (n // MX_BLOCK,), torch.uint8, x, stream)
+    _check((_lib or load()).cq_mx_quantize(x.data_ptr(), ldx, _TYPES[x.dtype], rows, n, form, codes.data_ptr(), width,
+                                           scales.data_ptr(), n // MX_BLOCK, _stream_on(stream, device)),
+           "cq_mx_quantize")
+    return codes, scales
+
+
+def _mx_pair(codes, scales, form, what="codes"):
+    """Values a row of codes stands for, with the types and shapes of codes and scales checked."""
+    if codes.dim() < 1 or codes.dtype not in _MX_CODES or (form == MXFP4 and codes.dtype != torch.uint8):
+        raise ValueError(f"{what} must be uint8 (mxfp8: or float8_e4m3fn)")
+    n = codes.shape[-1] * (2 if form == MXFP4 else 1)
+    if n % MX_BLOCK or scales.dtype not in _MX_SCALES or scales.shape != codes.shape[:-1] + (n // MX_BLOCK,):
+        raise ValueError(f"the scales of {what} must be uint8 or float8_e8m0fnu, one for each 32 values of a row")
+    return n
+
+
+def mx_dequantize(codes, scales, format="mxfp4", out_dtype=torch.bfloat16, stream=None):
+    """The values [..., n] that the blocks of mx_quantize stand for, as bfloat16, float16 or float32 (rounded once)."""
+    form = _mx_format(format)
+    n = _mx_pair(codes, scales, form)
+    if out_dtype not in _TYPES:
+        raise ValueError("out_dtype must be bfloat16, float16 or float32")
+    if not n:
+        raise ValueError("rows without values")
+    rows, ldc = _mx_rows(codes, "codes")
+    _, lds = _mx_rows(scales, "scales")
+    device = _gpu(codes)
+    if device != _device_now():
+        with torch.cuda.device(device):
+            return mx_dequantize(codes, scales, format, out_dtype, stream)
+    y = _empty(codes.shape[:-1] + (n,), out_dtype, codes, stream)
+    pc, ps = _on(device, ("codes", codes), ("scales", scales))
+    _check((_lib or load()).cq_mx_dequantize(pc, ldc, ps, lds, form, rows, n, y.data_ptr(), n, _TYPES[out_dtype],
+                                             _stream_on(stream, device)), "cq_mx_dequantize")
+    return y
+
+
+_MX_CACHE = struct.Struct("@4P6q5i4x")  # MxCache, field by field
+assert _MX_CACHE.size == ctypes.sizeof(MxCache)
+
+
+def _like(a, b):
+    """Whether b has a's shape and, where it matters, its strides."""
+    return a.shape == b.shape and (a.stride() == b.stride() or
+                                   all(n == 1 or i == j for n, i, j in zip(a.shape, a.stride(), b.stride())))
+
+
+def _mx_cache(k_cache, k_scales, v_cache, v_scales, heads, D, device):
+    """The cache that a call reads or writes: its format follows from the width of its rows."""
+    shape, sshape = k_cache.shape, k_scales.shape
+    if len(shape) != 4 or not _like(k_cache, v_cache) or shape[3] not in (D, D // 2) or shape[1] != heads:
+        raise ValueError("k_cache and v_cache must be [pages, kv_heads, page_size, head_dim (mxfp8) or head_dim / 2 "
+                         "(mxfp4)], strided alike")
+    form = MXFP8 if shape[3] == D else MXFP4
+    if D % MX_BLOCK or not 0 < D <= MAX_HEAD_DIM:
+        raise ValueError("head_dim must be a multiple of 32 up to 256")
+    if sshape != shape[:3] + (D // MX_BLOCK,) or not _like(k_scales, v_scales):
+        raise ValueError("k_scales and v_scales must be [pages, kv_heads, page_size, head_dim / 32], strided alike")
+    for c, e in ((k_cache, k_scales), (v_cache, v_scales)):
+        if c.dtype not in _MX_CODES or (form == MXFP4 and c.dtype != torch.uint8) or e.dtype not in _MX_SCALES:
+            raise ValueError("caches must be uint8 (mxfp8: or float8_e4m3fn), their scales uint8 or float8_e8m0fnu")
+    if k_cache.stride(3) != 1 or (sshape[3] > 1 and k_scales.stride(3) != 1):
+        raise ValueError("the rows of caches and scales must be contiguous")
+    pk, pv, pks, pvs = _on(device, ("k_cache", k_cache), ("v_cache", v_cache), ("k_scales", k_scales),
+                           ("v_scales", v_scales))
+    st = [k_cache.stride(i) if shape[i] > 1 else 0 for i in range(3)]
+    st += [k_scales.stride(i) if shape[i] > 1 else 0 for i in range(3)]
+    return MxCache.from_buffer_copy(_MX_CACHE.pack(pk, pv, pks, pvs, *st, form, shape[0], shape[2], heads, D))
+
+
+def kv_cache_write_mx(k, v, k_cache, k_scales, v_cache, v_scales, slots, stream=None):
+    """Quantizes k, v [T, kv_heads, head_dim] (bfloat16 or float16, strided views allowed) in blocks of 32 into caches of
+    codes uint8 [pages, kv_heads, page_size, head_dim] (mxfp8) or [.., head_dim / 2] (mxfp4) and of scales uint8 [..,
+    head_dim / 32], each block as by mx_quantize, at slots int32 [T] (page * page_size + offset; a negative slot is
+    skipped)."""
+    if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("k and v must be bfloat16 or float16 [T, kv_heads, head_dim]")
+    T, heads, D = k.shape
+    _int32(slots=slots)
+    if slots.numel() != T:
+        raise ValueError("slots must be int32 [T]")
+    if k.stride(2) != 1 or v.stride(2) != 1:
+        raise ValueError("head_dim must be contiguous")
+    _contiguous(slots=slots)
+    device = _gpu(k_cache)
+    if device != _device_now():
+        with torch.cuda.device(device):
+            return kv_cache_write_mx(k, v, k_cache, k_scales, v_cache, v_scales, slots, stream)
+    cache = _mx_cache(k_cache, k_scales, v_cache, v_scales, heads, D, device)
+    pk, pv, ps = _on(device, ("k", k), ("v", v), ("slots", slots))
+    _check((_lib or load()).cq_kv_cache_write_mx(pk, _step(k, 0), _step(k, 1), pv, _step(v, 0), _step(v, 1),
+                                                 _TYPES[k.dtype], cache, ps, T, _stream_on(stream, device)),
+           "cq_kv_cache_write_mx")
 
 
 def environment_diagonals(x, stream=None):

@@ -434,6 +434,76 @@ int32_t cq_kv_cache_write(const void* k, int64_t k_token_stride, int64_t k_head_
     return hip_status(cqk::launch_cache_write(a, (hipStream_t)stream));
 }
 
+static bool mx_rows_ok(const void* values, int64_t ldx, int32_t type, int64_t rows, int64_t len, int32_t format,
+                       const void* codes, int64_t ldc, const void* scales, int64_t lds) {
+    if ((type != CQ_BF16 && type != CQ_F16 && type != CQ_F32) || (format != CQ_MXFP4 && format != CQ_MXFP8)) return false;
+    if (rows < 0 || len <= 0 || len % CQ_MX_BLOCK != 0 || len >= (int64_t)1 << 35) return false;
+    if (rows > 0 && rows > (((int64_t)1 << 35) - 1) / len) return false;
+    if (rows == 0) return true;
+    if (!values || !codes || !scales || !aligned(values, 16) || !aligned(codes, 16)) return false;
+    return ldx >= len && ldx % 8 == 0 && ldc >= (format == CQ_MXFP4 ? len / 2 : len) && ldc % 16 == 0 &&
+           lds >= len / CQ_MX_BLOCK;
+}
+
+static cqk::MxRowsArgs mx_rows(const void* values, int64_t ldx, int32_t type, int64_t rows, int64_t len, int32_t format,
+                               const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds) {
+    cqk::MxRowsArgs a{};
+    a.values = const_cast<void*>(values); a.codes = const_cast<uint8_t*>(codes); a.scales = const_cast<uint8_t*>(scales);
+    a.rows = rows; a.len = len; a.ldx = ldx; a.ldc = ldc; a.lds = lds; a.form = format; a.type = type;
+    return a;
+}
+
+int32_t cq_mx_quantize(const void* x, int64_t ldx, int32_t x_type, int64_t rows, int64_t len, int32_t format,
+                       uint8_t* codes, int64_t ldc, uint8_t* scales, int64_t lds, void* stream) {
+    if (!mx_rows_ok(x, ldx, x_type, rows, len, format, codes, ldc, scales, lds)) return CQ_EINVAL;
+    if (rows == 0) return CQ_OK;
+    return hip_status(cqk::launch_mx_rows(mx_rows(x, ldx, x_type, rows, len, format, codes, ldc, scales, lds), false,
+                                          (hipStream_t)stream));
+}
+
+int32_t cq_mx_dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* scales, int64_t lds, int32_t format,
+                         int64_t rows, int64_t len, void* y, int64_t ldy, int32_t y_type, void* stream) {
+    if (!mx_rows_ok(y, ldy, y_type, rows, len, format, codes, ldc, scales, lds)) return CQ_EINVAL;
+    if (rows == 0) return CQ_OK;
+    return hip_status(cqk::launch_mx_rows(mx_rows(y, ldy, y_type, rows, len, format, codes, ldc, scales, lds), true,
+                                          (hipStream_t)stream));
+}
+
+static bool mx_cache_ok(const cq_mx_cache& c) {
+    if (c.format != CQ_MXFP4 && c.format != CQ_MXFP8) return false;
+    if (c.n_pages < 0 || c.page_size < 1 || c.kv_heads < 1) return false;
+    if (c.head_dim < CQ_MX_BLOCK || c.head_dim > CQ_MAX_HEAD_DIM || c.head_dim % CQ_MX_BLOCK != 0) return false;
+    if ((c.page_stride | c.head_stride | c.row_stride | c.scale_page_stride | c.scale_head_stride | c.scale_row_stride) < 0)
+        return false;
+    return (c.page_stride | c.head_stride | c.row_stride) % 16 == 0 && aligned(c.k_codes, 16) && aligned(c.v_codes, 16);
+}
+
+static cqk::MxCache mx_cache(const cq_mx_cache& c) {
+    cqk::MxCache m{};
+    m.kc = (uint8_t*)c.k_codes; m.vc = (uint8_t*)c.v_codes; m.ks = (uint8_t*)c.k_scales; m.vs = (uint8_t*)c.v_scales;
+    m.c_page = c.page_stride; m.c_head = c.head_stride; m.c_row = c.row_stride;
+    m.s_page = c.scale_page_stride; m.s_head = c.scale_head_stride; m.s_row = c.scale_row_stride;
+    m.form = c.format; m.n_pages = c.n_pages; m.page = c.page_size; m.H = c.kv_heads; m.D = c.head_dim;
+    return m;
+}
+
+int32_t cq_kv_cache_write_mx(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                             int64_t v_token_stride, int64_t v_head_stride, int32_t type, const cq_mx_cache* cache,
+                             const int32_t* slots, int32_t n_tokens, void* stream) {
+    if (!cache || !mx_cache_ok(*cache) || (type != CQ_BF16 && type != CQ_F16) || n_tokens < 0) return CQ_EINVAL;
+    const cq_mx_cache& c = *cache;
+    if ((k_token_stride | k_head_stride | v_token_stride | v_head_stride) < 0) return CQ_EINVAL;
+    if ((int64_t)n_tokens > (((int64_t)1 << 34) - 1) / c.head_dim / c.kv_heads) return CQ_EINVAL;
+    if (n_tokens == 0 || c.n_pages == 0) return CQ_OK;
+    if (!k || !v || !c.k_codes || !c.v_codes || !c.k_scales || !c.v_scales || !slots) return CQ_EINVAL;
+    if (!aligned(k, 2) || !aligned(v, 2) || !aligned(slots, 4)) return CQ_EINVAL;
+    cqk::MxCacheWriteArgs a{};
+    a.k = (const uint16_t*)k; a.v = (const uint16_t*)v; a.k_tok = k_token_stride; a.k_head = k_head_stride;
+    a.v_tok = v_token_stride; a.v_head = v_head_stride; a.c = mx_cache(c); a.slots = slots;
+    a.n_slots = (int64_t)c.n_pages * c.page_size; a.T = n_tokens; a.f16 = type == CQ_F16;
+    return hip_status(cqk::launch_cache_write_mx(a, (hipStream_t)stream));
+}
+
 static bool attention_sizes_ok(int32_t T, int32_t R, int32_t max_q, int32_t max_kv, int32_t H, int32_t Hkv, int32_t D) {
     return T >= 0 && R >= 0 && max_q >= 0 && max_kv >= 0 && Hkv >= 1 && H >= Hkv && H % Hkv == 0 && H <= 65535 &&
            D >= 8 && D <= CQ_MAX_HEAD_DIM && D % 8 == 0 && (int64_t)T * H <= INT32_MAX && R <= 65535;

@@ -40,6 +40,32 @@ struct CacheWriteArgs {
 };
 hipError_t launch_cache_write(const CacheWriteArgs& a, hipStream_t st);
 
+// Rows of values and their microscaled blocks; `values` is read or written, of type 0 bf16, 1 f16, 2 f32.  Strides in
+// elements (of codes and scales: bytes).
+struct MxRowsArgs {
+    void* values;
+    uint8_t *codes, *scales;
+    int64_t rows, len, ldx, ldc, lds;
+    int form, type;
+};
+hipError_t launch_mx_rows(const MxRowsArgs& a, bool back, hipStream_t st);  // back: codes to values
+
+// A paged cache of microscaled blocks; strides in bytes.
+struct MxCache {
+    uint8_t *kc, *vc, *ks, *vs;
+    int64_t c_page, c_head, c_row, s_page, s_head, s_row;
+    int32_t form, n_pages, page, H, D;
+};
+struct MxCacheWriteArgs {
+    const uint16_t *k, *v;
+    int64_t k_tok, k_head, v_tok, v_head;
+    MxCache c;
+    const int32_t* slots;
+    int64_t n_slots;
+    int32_t T, f16;
+};
+hipError_t launch_cache_write_mx(const MxCacheWriteArgs& a, hipStream_t st);
+
 struct AttentionArgs {
     const uint16_t *q, *kc, *vc;
     uint16_t* out;

@@ -1,0 +1,99 @@
+"""The microscaled formats' C entry points and helpers without a GPU: bad arguments are refused before anything reaches
+HIP."""
+import pytest
+import torch
+
+import post_weight_quantization_group_amd as cq
+
+FAKE = 1 << 20  # a 16-byte-aligned address that is never dereferenced: every call below fails its checks
+
+
+def _rows(entry, **kw):
+    a = dict(x=FAKE, ldx=128, xt=cq.BF16, rows=4, len=128, form=cq.MXFP4, codes=FAKE, ldc=64, scales=FAKE, lds=4)
+    a.update(kw)
+    lib = cq.load()
+    if entry == "quantize":
+        return lib.cq_mx_quantize(a["x"], a["ldx"], a["xt"], a["rows"], a["len"], a["form"], a["codes"], a["ldc"],
+                                  a["scales"], a["lds"], None)
+    return lib.cq_mx_dequantize(a["codes"], a["ldc"], a["scales"], a["lds"], a["form"], a["rows"], a["len"], a["x"],
+                                a["ldx"], a["xt"], None)
+
+
+@pytest.mark.parametrize("entry", ["quantize", "dequantize"])
+@pytest.mark.parametrize("kw", [
+    dict(xt=3), dict(xt=-1), dict(form=2), dict(form=5), dict(rows=-1), dict(len=0), dict(len=-32), dict(len=48),
+    dict(len=1 << 35, ldx=1 << 35, ldc=1 << 34, lds=1 << 30), dict(rows=1 << 28), dict(rows=1 << 62), dict(x=None),
+    dict(codes=None), dict(scales=None), dict(x=FAKE + 8), dict(codes=FAKE + 8), dict(ldx=120), dict(ldx=132),
+    dict(ldc=48), dict(ldc=72), dict(lds=3), dict(form=cq.MXFP8),
+])
+def test_rows_reject_before_launch(entry, kw):
+    assert _rows(entry, **kw) == -1
+
+
+@pytest.mark.parametrize("entry", ["quantize", "dequantize"])
+def test_no_rows_are_a_no_op(entry):
+    assert _rows(entry, rows=0, x=None, codes=None, scales=None) == 0
+
+
+def _cache(**kw):
+    a = dict(k_codes=FAKE, v_codes=FAKE, k_scales=FAKE, v_scales=FAKE, page_stride=2048, head_stride=1024, row_stride=64,
+             scale_page_stride=64, scale_head_stride=32, scale_row_stride=2, format=cq.MXFP8, n_pages=9, page_size=16,
+             kv_heads=2, head_dim=64)
+    a.update({k: v for k, v in kw.items() if k in a})
+    return cq.MxCache(**a)
+
+
+def _write(**kw):
+    a = dict(k=FAKE, kt=128, kh=64, v=FAKE, vt=128, vh=64, type=cq.BF16, slots=FAKE, T=3)
+    a.update({k: v for k, v in kw.items() if k in a})
+    return cq.load().cq_kv_cache_write_mx(a["k"], a["kt"], a["kh"], a["v"], a["vt"], a["vh"], a["type"],
+                                          None if kw.get("cache", 1) is None else _cache(**kw), a["slots"], a["T"], None)
+
+
+BAD_CACHES = [dict(format=0), dict(format=5), dict(n_pages=-1), dict(page_size=0), dict(kv_heads=0), dict(head_dim=0),
+              dict(head_dim=80), dict(head_dim=288), dict(page_stride=-16), dict(head_stride=1000), dict(row_stride=8),
+              dict(scale_row_stride=-1), dict(scale_page_stride=-1), dict(k_codes=FAKE + 8), dict(v_codes=FAKE + 4)]
+
+
+@pytest.mark.parametrize("kw", BAD_CACHES + [
+    dict(cache=None), dict(type=cq.F32), dict(T=-1), dict(kt=-1), dict(vh=-2), dict(k=None), dict(v=None),
+    dict(k_codes=None), dict(v_codes=None), dict(k_scales=None), dict(v_scales=None), dict(slots=None), dict(k=FAKE + 1),
+    dict(v=FAKE + 1), dict(slots=FAKE + 2), dict(T=1 << 27), dict(T=(1 << 31) - 1, kv_heads=1 << 20),
+])
+def test_cache_write_rejects_before_launch(kw):
+    assert _write(**kw) == -1
+
+
+def test_cache_write_of_nothing_is_a_no_op():
+    assert _write(T=0, k=None) == 0 and _write(n_pages=0, k_codes=None, k_scales=None) == 0
+
+
+def _refused(match, call, *args, **kw):
+    with pytest.raises(ValueError, match=match):
+        call(*args, **kw)
+
+
+def test_helpers_refuse():
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    codes, scales = torch.zeros((4, 32), dtype=torch.uint8), torch.zeros((4, 2), dtype=torch.uint8)
+    _refused("format", cq.mx_quantize, x, "mxfp6")
+    _refused("multiple of 32", cq.mx_quantize, x[:, :48], "mxfp4")
+    _refused("multiple of 32", cq.mx_quantize, x[:, :0], "mxfp4")
+    _refused("multiple of 32", cq.mx_quantize, x.double(), "mxfp4")
+    _refused("contiguous", cq.mx_quantize, torch.zeros((64, 64), dtype=torch.bfloat16).t(), "mxfp4")
+    _refused("contiguous", cq.mx_quantize, torch.zeros((2, 4, 128), dtype=torch.bfloat16)[:, :, :64], "mxfp4")
+    _refused("GPU", cq.mx_quantize, x)
+    _refused("GPU", cq.mx_dequantize, codes, scales)
+    _refused("scales", cq.mx_dequantize, codes, scales, "mxfp8")
+    _refused("uint8", cq.mx_dequantize, codes.view(torch.float8_e4m3fn), scales, "mxfp4")
+    _refused("uint8", cq.mx_dequantize, codes.int(), scales)
+    _refused("scales", cq.mx_dequantize, codes, scales.int())
+    _refused("out_dtype", cq.mx_dequantize, codes, scales, out_dtype=torch.float64)
+    k, slots = torch.zeros((3, 2, 64), dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    c, e = torch.zeros((5, 2, 16, 64), dtype=torch.uint8), torch.zeros((5, 2, 16, 2), dtype=torch.uint8)
+    _refused("bfloat16 or float16", cq.kv_cache_write_mx, k.float(), k.float(), c, e, c, e, slots)
+    _refused("bfloat16 or float16", cq.kv_cache_write_mx, k, k[:2], c, e, c, e, slots)
+    _refused("int32", cq.kv_cache_write_mx, k, k, c, e, c, e, slots.long())
+    _refused("slots", cq.kv_cache_write_mx, k, k, c, e, c, e, slots[:2])
+    _refused("contiguous", cq.kv_cache_write_mx, k.transpose(1, 2).contiguous().transpose(1, 2), k, c, e, c, e, slots)
+    _refused("GPU", cq.kv_cache_write_mx, k, k, c, e, c, e, slots)
