@@ -514,6 +514,36 @@ int32_t cq_mx_dequantize(const uint8_t *codes, int64_t ldc, const uint8_t *scale
                          int64_t rows, int64_t len, void *y, int64_t ldy, int32_t y_type, void *stream);
 
 /*
+ * Linear layer over MXFP4 weights with its epilogue:
+ *        z[m][c] = sum_k X[m][k] W[c][k] + bias[c],   y as for cq_w4a16_linear,
+ * X being x's rows as cq_mx_quantize gives them in x_format, or those given as codes.  The products are exact and summed
+ * in fp32 on the matrix cores, the epilogue is in fp32, with one rounding into y's type.  A block that is NaN (of x or
+ * W) makes the outputs NaN that it takes part in.
+ *   type       CQ_BF16 or CQ_F16: of bias and residual, of x where it is not codes, and of y unless y_type is CQ_F32.
+ *   x_format   CQ_MXFP4 or CQ_MXFP8.
+ *   x          x_scales NULL: [M] rows of `in` values, ldx elements apart (a multiple of 8).  Else [M] rows of codes, in / 2
+ *              (CQ_MXFP8: in) bytes, ldx bytes apart (a multiple of 16).  16-byte aligned.
+ *   x_scales   nullable, [M] rows of in / 32 bytes, ldxs apart.
+ *   qweight    [cols] rows of in / 2 bytes without gaps, 16-byte aligned; scales [cols] rows of in / 32 bytes: W in
+ *              MXFP4, as cq_mx_quantize gives them for [cols][in].  cols = out, or 2 out when gated (the gate's first).
+ *   bias, residual, y, activation, gated   as for cq_w4a16_linear.
+ *   workspace  cq_mxfp4_linear_workspace_size(...) bytes for the same sizes (0: may be NULL); `codes`: whether x is.
+ * in a positive multiple of 128 up to 2^24; cols <= 2^25, M * cols < 2^38, M * in < 2^35, M < 2^31; M == 0 or out == 0 enqueues nothing.
+ */
+typedef struct cq_mxfp4_linear_args {
+    const void *x;
+    const uint8_t *x_scales, *qweight, *scales;
+    const void *bias, *residual;
+    void *y;
+    int64_t ldx, ldxs, ldr, ldy;
+    int64_t M, out, in;
+    int32_t type, x_format, y_type, activation, gated;
+} cq_mxfp4_linear_args;
+size_t cq_mxfp4_linear_workspace_size(int64_t M, int64_t out, int64_t in, int32_t gated, int32_t x_format,
+                                      int32_t codes);
+int32_t cq_mxfp4_linear(const cq_mxfp4_linear_args *args, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * A paged cache whose keys and values are microscaled blocks along head_dim (a multiple of 32 up to CQ_MAX_HEAD_DIM).
  *   k_codes, v_codes    [n_pages][kv_heads][page_size] rows of head_dim / 2 bytes (CQ_MXFP8: head_dim), 16-byte aligned:
  *                       page_stride, head_stride and row_stride bytes apart (multiples of 16, the same for both).

@@ -56,18 +56,26 @@ def dequantize(codes, scales, form):
 def _sum_error(x, W):
     """(z, bound): z = x W^T and how far sums of its products in fp32 on the matrix cores may be off.
 
-    Products of elements and their scales are exact.  An instruction adds 64 or 128 of them to a sum; each of its
-    additions, in whatever order, is within 2^-23 (they need not round to nearest) of what it can reach: |S| + A, S the sum
-    in front of the instruction, A its sum of |x| |W|.  65 additions an instruction of 64 (an instruction of 128 counts as
-    two), in one of the kernels' orders: a running sum over all instructions, or up to 16 of them over every 16th or so,
-    joined by as many additions more.  |S| is bounded by the running sum of |x W| over a block of 64 either way, taken
-    here as the sum of A so far: an upper bound of both."""
-    z = x @ W.T
-    reach, bound = np.zeros_like(z), np.zeros_like(z)
-    for k in range(0, x.shape[1], 64):
-        reach += np.abs(x[:, k:k + 64]) @ np.abs(W[:, k:k + 64]).T
-        bound += reach
-    return z, 2.0 ** -23 * (65 * bound + 16 * reach)
+    Products of elements with their scales are exact.  128 of them are added to a sum by one instruction or two: at most
+    130 additions, in whatever order, each within 2^-23 (they need not round to nearest) of what the sum can reach on the
+    way, |S| + A with S the sum in front of the 128 and A the sum of their |x| |W|.  The 128s go one after the other to
+    one sum, or in turn to 2, 4, 8 or 16 of them, which are then added up one by one; the bound is the largest of these
+    orders'."""
+    z, bound = x @ W.T, np.zeros((x.shape[0], W.shape[0]))
+    steps = range(0, x.shape[1], 128)
+    parts = [x[:, k:k + 128] @ W[:, k:k + 128].T for k in steps]
+    sizes = [np.abs(x[:, k:k + 128]) @ np.abs(W[:, k:k + 128]).T for k in steps]
+    for n in (1, 2, 4, 8, 16):
+        err, joined, size = np.zeros_like(z), np.zeros_like(z), np.zeros_like(z)
+        for w in range(min(n, len(parts))):
+            S = np.zeros_like(z)
+            for part, A in zip(parts[w::n], sizes[w::n]):
+                err += 130 * 2.0 ** -23 * (np.abs(S) + A)
+                S = S + part
+            joined = joined + S
+            size += np.abs(joined)
+        bound = np.maximum(bound, err + 2.0 ** -24 * (size if n > 1 else 0.0))
+    return z, (1 + 2.0 ** -10) * bound
 
 
 def mxfp4_linear(x, W, bias=None, residual=None, act="none", gated=False, out_type="bf16"):

@@ -42,7 +42,8 @@ __all__ = [
     "cq_kv_cache_write", "kv_cache_write", "cq_paged_attention_workspace_size", "cq_paged_attention",
     "paged_attention",
     "MXFP4", "MXFP8", "MX_BLOCK", "MxCache", "cq_mx_quantize", "mx_quantize", "cq_mx_dequantize", "mx_dequantize",
-    "cq_kv_cache_write_mx", "kv_cache_write_mx",
+    "cq_kv_cache_write_mx", "kv_cache_write_mx", "Mxfp4LinearArgs", "cq_mxfp4_linear_workspace_size", "cq_mxfp4_linear",
+    "mxfp4_linear",
 ]
 
 GROUP = 128
@@ -72,7 +73,8 @@ EXPORTED_SYMBOLS = ("cq_abi_version", "cq_status_string", "cq_workspace_size", "
                     "cq_heldout_compare", "cq_diagonals_workspace_size", "cq_environment_diagonals",
                     "cq_w4a16_matmul", "cq_probe_valu_fma", "cq_w4a16_linear", "cq_kv_block_map",
                     "cq_kv_cache_write", "cq_paged_attention_workspace_size", "cq_paged_attention",
-                    "cq_mx_quantize", "cq_mx_dequantize", "cq_kv_cache_write_mx")
+                    "cq_mx_quantize", "cq_mx_dequantize", "cq_kv_cache_write_mx", "cq_mxfp4_linear_workspace_size",
+                    "cq_mxfp4_linear")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lib = None
@@ -102,6 +104,13 @@ class MxCache(ctypes.Structure):
                [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "row_stride", "scale_page_stride",
                                               "scale_head_stride", "scale_row_stride")] + \
                [(n, ctypes.c_int32) for n in ("format", "n_pages", "page_size", "kv_heads", "head_dim")]
+
+
+class Mxfp4LinearArgs(ctypes.Structure):
+    """cq_mxfp4_linear_args of cq.h: device pointers as integers, leading dimensions in elements (of codes: bytes)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "x_scales", "qweight", "scales", "bias", "residual", "y")] + \
+               [(n, ctypes.c_int64) for n in ("ldx", "ldxs", "ldr", "ldy", "M", "out", "inp")] + \
+               [(n, ctypes.c_int32) for n in ("type", "x_format", "y_type", "activation", "gated")]
 
 
 def library_path() -> str:
@@ -177,6 +186,10 @@ def load():
         lib.cq_mx_dequantize.argtypes = [P, I64, P, I64, I32, I64, I64, P, I64, I32, P]
         lib.cq_kv_cache_write_mx.restype = I32
         lib.cq_kv_cache_write_mx.argtypes = [P, I64, I64, P, I64, I64, I32, ctypes.POINTER(MxCache), P, I32, P]
+        lib.cq_mxfp4_linear_workspace_size.restype = SZ
+        lib.cq_mxfp4_linear_workspace_size.argtypes = [I64, I64, I64, I32, I32, I32]
+        lib.cq_mxfp4_linear.restype = I32
+        lib.cq_mxfp4_linear.argtypes = [ctypes.POINTER(Mxfp4LinearArgs), P, SZ, P]
         _lib = lib
     return _lib
 
@@ -445,6 +458,15 @@ def cq_kv_cache_write_mx(k, k_token_stride, k_head_stride, v, v_token_stride, v_
     _check(load().cq_kv_cache_write_mx(_rows(k), k_token_stride, k_head_stride, _rows(v), v_token_stride,
                                        v_head_stride, type, cache, _p(slots), n_tokens, _stream(stream)),
            "cq_kv_cache_write_mx")
+
+
+def cq_mxfp4_linear_workspace_size(M: int, out: int, inp: int, gated: int, x_format: int, codes: int) -> int:
+    return load().cq_mxfp4_linear_workspace_size(M, out, inp, gated, x_format, codes)
+
+
+def cq_mxfp4_linear(args: Mxfp4LinearArgs, workspace=None, stream=None):
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().cq_mxfp4_linear(args, _p(workspace), ws_bytes, _stream(stream)), "cq_mxfp4_linear")
 
 
 # ---------------------------------------------------------------- helpers
@@ -900,6 +922,82 @@ def mx_dequantize(codes, scales, format="mxfp4", out_dtype=torch.bfloat16, strea
     _check((_lib or load()).cq_mx_dequantize(pc, ldc, ps, lds, form, rows, n, y.data_ptr(), n, _TYPES[out_dtype],
                                              _stream_on(stream, device)), "cq_mx_dequantize")
     return y
+
+
+_MXFP4_LINEAR = struct.Struct("@7P7q5i4x")  # Mxfp4LinearArgs, field by field
+assert _MXFP4_LINEAR.size == ctypes.sizeof(Mxfp4LinearArgs)
+
+
+def mxfp4_linear(x, qweight, scales, x_scales=None, x_format="mxfp8", bias=None, residual=None, activation="none",
+                 gated=False, out_dtype=None, out=None, workspace=None, stream=None):
+    """y [M, out] = act(X W^T + bias) + residual over MXFP4 weights; gated: W holds the gate's rows, then as many others,
+    and y = act(X Wg^T + bg) * (X Wu^T + bu) + residual.
+
+    qweight uint8 [cols, in/2] and scales uint8 [cols, in/32] are mx_quantize's of a [cols, in] matrix, in a multiple of
+    128.  x is bfloat16 or float16 [M, in] (rows may be strided: 16-byte aligned, stride a multiple of 8), and X its rows
+    quantized to x_format ("mxfp8" or "mxfp4") as mx_quantize does; or x holds codes of x_format with their x_scales.
+    bias [cols] and residual [M, out] have x's type; beside codes they have one 16-bit type, which is the result's too
+    (bfloat16 where there is neither).  activation: "none", "relu", "silu", "gelu" or "gelu_tanh".  The result has that
+    type, or float32 with out_dtype=torch.float32, or goes into ``out`` (which may be the residual itself)."""
+    form = _mx_format(x_format)
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix [M, in], of values or of codes")
+    M = x.shape[0]
+    if x_scales is None:
+        dt, inp = x.dtype, x.shape[1]
+        if dt != torch.bfloat16 and dt != torch.float16:
+            raise ValueError("x must be bfloat16 or float16 [M, in], or codes with x_scales")
+    else:
+        inp = _mx_pair(x, x_scales, form, "x")
+        dt = next((t.dtype for t in (bias, residual) if t is not None), None)
+        if dt is None:
+            dt = next((d for d in (out_dtype, None if out is None else out.dtype) if d not in (None, torch.float32)),
+                      torch.bfloat16)
+        if dt != torch.bfloat16 and dt != torch.float16:
+            raise ValueError("bias, residual and result must be bfloat16 or float16 (the result also float32)")
+    if qweight.dim() != 2 or qweight.dtype != torch.uint8 or qweight.shape[1] * 2 != inp or inp % GROUP or not inp:
+        raise ValueError("qweight must be uint8 [cols, in/2], in a multiple of 128")
+    cols = qweight.shape[0]
+    if scales.shape != (cols, inp // MX_BLOCK) or scales.dtype not in _MX_SCALES:
+        raise ValueError("scales must be uint8 or float8_e8m0fnu [cols, in/32]")
+    if gated and cols % 2:
+        raise ValueError("gated needs an even number of columns")
+    n = cols // 2 if gated else cols
+    if bias is not None and (bias.shape != (cols,) or bias.dtype != dt):
+        raise ValueError("bias must be [cols], of x's type (beside codes: of the residual's)")
+    if residual is not None and (residual.shape != (M, n) or residual.dtype != dt):
+        raise ValueError("residual must be [M, out], of x's type (beside codes: of the bias's)")
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
+    _contiguous(qweight=qweight, scales=scales)
+    if bias is not None:
+        _contiguous(bias=bias)
+    device = _gpu(x)
+    if device != _device_now():
+        with torch.cuda.device(device):
+            return mxfp4_linear(x, qweight, scales, x_scales, x_format, bias, residual, activation, gated, out_dtype,
+                                out, workspace, stream)
+    if out is None:
+        out = _empty((M, n), out_dtype or dt, x, stream)
+    elif out.shape != (M, n) or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out must be [M, out], of the type asked for")
+    if out.dtype != dt and out.dtype != torch.float32:
+        raise ValueError("the result has the 16-bit type of the other arrays, or float32")
+    lib = _lib or load()
+    need = lib.cq_mxfp4_linear_workspace_size(M, n, inp, int(gated), form, int(x_scales is not None))
+    if need and workspace is None:
+        workspace = _empty(need, torch.uint8, x, stream)
+    px, pxs, pq, ps, pb, pr, py, pw = _on(
+        device, ("x", x), ("x_scales", x_scales), ("qweight", qweight), ("scales", scales), ("bias", bias),
+        ("residual", residual), ("out", out), ("workspace", workspace))
+    args = Mxfp4LinearArgs.from_buffer_copy(_MXFP4_LINEAR.pack(
+        px, pxs or 0, pq, ps, pb or 0, pr or 0, py, _ld(x), 0 if x_scales is None else _ld(x_scales),
+        0 if residual is None else _ld(residual), _ld(out), M, n, inp, _TYPES[dt], form, _TYPES[out.dtype], act,
+        int(gated)))
+    _check(lib.cq_mxfp4_linear(args, pw, 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                               _stream_on(stream, device)), "cq_mxfp4_linear")
+    return out
 
 
 _MX_CACHE = struct.Struct("@4P6q5i4x")  # MxCache, field by field

@@ -469,6 +469,46 @@ int32_t cq_mx_dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* scale
                                           (hipStream_t)stream));
 }
 
+static bool mx_linear_sizes_ok(int64_t M, int64_t out, int64_t in, int32_t gated, int32_t x_format) {
+    if ((x_format != CQ_MXFP4 && x_format != CQ_MXFP8) || (gated != 0 && gated != 1)) return false;
+    if (M < 0 || out < 0 || in <= 0 || in % CQ_GROUP != 0 || in > (int64_t)1 << 24) return false;
+    if (M > INT32_MAX || out > (int64_t)1 << (gated ? 24 : 25)) return false;
+    return M * (gated ? 2 * out : out) < (int64_t)1 << 38 && M * in < (int64_t)1 << 35;
+}
+
+size_t cq_mxfp4_linear_workspace_size(int64_t M, int64_t out, int64_t in, int32_t gated, int32_t x_format,
+                                      int32_t codes) {
+    if (!mx_linear_sizes_ok(M, out, in, gated, x_format) || M == 0 || out == 0) return 0;
+    return (size_t)cqk::mx_linear_ws(M, out, in, gated, x_format, codes != 0);
+}
+
+int32_t cq_mxfp4_linear(const cq_mxfp4_linear_args* args, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!args) return CQ_EINVAL;
+    const cq_mxfp4_linear_args& p = *args;
+    if ((p.type != CQ_BF16 && p.type != CQ_F16) || (p.y_type != p.type && p.y_type != CQ_F32)) return CQ_EINVAL;
+    if (p.activation < CQ_ACT_NONE || p.activation > CQ_ACT_GELU_TANH) return CQ_EINVAL;
+    if (!mx_linear_sizes_ok(p.M, p.out, p.in, p.gated, p.x_format)) return CQ_EINVAL;
+    if (p.M == 0 || p.out == 0) return CQ_OK;
+    if (!p.x || !p.qweight || !p.scales || !p.y) return CQ_EINVAL;
+    const bool codes = p.x_scales != nullptr;
+    if (codes ? p.ldx < (p.x_format == CQ_MXFP4 ? p.in / 2 : p.in) || p.ldx % 16 != 0 || p.ldxs < p.in / CQ_MX_BLOCK
+              : p.ldx < p.in || p.ldx % 8 != 0)
+        return CQ_EINVAL;
+    if (p.ldy < p.out || (p.residual && p.ldr < p.out)) return CQ_EINVAL;
+    if (!aligned(p.x, 16) || !aligned(p.qweight, 16) || !aligned(p.bias, 2) || !aligned(p.residual, 2) ||
+        !aligned(p.y, p.y_type == CQ_F32 ? 4 : 2))
+        return CQ_EINVAL;
+    const size_t need = cq_mxfp4_linear_workspace_size(p.M, p.out, p.in, p.gated, p.x_format, codes);
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, ALIGN))) return CQ_EWORKSPACE;
+    cqk::MxLinearArgs a{};
+    a.x = p.x; a.xs = p.x_scales; a.w = p.qweight; a.ws = p.scales;
+    a.bias = (const uint16_t*)p.bias; a.residual = (const uint16_t*)p.residual; a.y = p.y;
+    a.M = p.M; a.out = p.out; a.in = p.in; a.ldx = p.ldx; a.ldxs = p.ldxs; a.ldr = p.ldr; a.ldy = p.ldy;
+    a.form = p.x_format; a.f16 = p.type == CQ_F16; a.y_f32 = p.y_type == CQ_F32; a.act = p.activation; a.gated = p.gated;
+    a.work = (uint8_t*)workspace;
+    return hip_status(cqk::launch_mx_linear(a, (hipStream_t)stream));
+}
+
 static bool mx_cache_ok(const cq_mx_cache& c) {
     if (c.format != CQ_MXFP4 && c.format != CQ_MXFP8) return false;
     if (c.n_pages < 0 || c.page_size < 1 || c.kv_heads < 1) return false;

@@ -10,6 +10,7 @@
 // Lane layouts (checked on gfx950).  16x16x32: lane l holds A[l % 16][8 (l / 16) + e], B[8 (l / 16) +
 // e][l % 16], D[4 (l / 16) + r][l % 16].  32x32x16: A[l % 32][8 (l / 32) + e], B likewise,
 // D[8 (r / 4) + 4 (l / 32) + r % 4][l % 32].
+#include "epilogue.h"
 #include "serve_args.h"
 #include "serve_math.h"
 
@@ -18,7 +19,6 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 template <bool F16>
@@ -60,63 +60,6 @@ __device__ __forceinline__ uint4 codes(uint32_t word) {
 }
 
 __device__ __forceinline__ float scale_of(uint16_t bits) { return (float)__builtin_bit_cast(_Float16, bits); }
-
-// act(z + b) [* (z' + b')] + r of output (m, o) and its store.
-template <bool F16>
-__device__ __forceinline__ void finish(const LinearArgs& a, int64_t m, int64_t o, float z, float up) {
-    if (a.bias) z += to_f32<F16>(a.bias[o]);
-    z = activate(a.act, z);
-    if (a.gated) {
-        if (a.bias) up += to_f32<F16>(a.bias[a.out + o]);
-        z *= up;
-    }
-    if (a.residual) z += to_f32<F16>(a.residual[m * a.ldr + o]);
-    if (a.y_f32) reinterpret_cast<float*>(a.y)[m * a.ldy + o] = z;
-    else reinterpret_cast<uint16_t*>(a.y)[m * a.ldy + o] = from_f32<F16>(z);
-}
-
-// Whether four neighbouring outputs from a multiple of 4 on can be moved at once.
-__device__ __forceinline__ bool outputs_in_fours(const LinearArgs& a) {
-    bool ok = a.out % 4 == 0 && a.ldy % 4 == 0 && ((uintptr_t)a.y & (a.y_f32 ? 15 : 7)) == 0;
-    if (a.residual) ok = ok && a.ldr % 4 == 0 && ((uintptr_t)a.residual & 7) == 0;
-    if (a.bias) ok = ok && ((uintptr_t)a.bias & 7) == 0;
-    return ok;
-}
-
-template <bool F16>
-__device__ __forceinline__ f32x4 four(const uint16_t* p) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    return f32x4{to_f32<F16>((uint16_t)v.x), to_f32<F16>((uint16_t)(v.x >> 16)), to_f32<F16>((uint16_t)v.y),
-                 to_f32<F16>((uint16_t)(v.y >> 16))};
-}
-
-// finish() of the outputs (m, o .. o + 3) that exist.
-template <bool F16>
-__device__ __forceinline__ void finish4(const LinearArgs& a, int64_t m, int64_t o, f32x4 z, f32x4 up, bool wide) {
-    if (m >= a.M || o >= a.out) return;
-    if (!wide) {
-        for (int e = 0; e < 4; ++e)
-            if (o + e < a.out) finish<F16>(a, m, o + e, z[0], up[0]), z = z.yzwx, up = up.yzwx;
-        return;
-    }
-    if (a.bias) {
-        z += four<F16>(a.bias + o);
-        if (a.gated) up += four<F16>(a.bias + a.out + o);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) z[e] = activate(a.act, z[e]);
-    if (a.gated) z *= up;
-    if (a.residual) z += four<F16>(a.residual + m * a.ldr + o);
-    if (a.y_f32) {
-        *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.y) + m * a.ldy + o) = z;
-    } else {
-        uint32_t b[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) b[e] = from_f32<F16>(z[e]);
-        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.y) + m * a.ldy + o) =
-            make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
-    }
-}
 
 // ---------------------------------------------------------------------------------------------
 // Few rows, or few tiles: a workgroup takes 16 MT rows and 4 x 16 columns (gated: 2 x 16 of the gate and

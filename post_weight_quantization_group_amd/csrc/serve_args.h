@@ -50,6 +50,20 @@ struct MxRowsArgs {
 };
 hipError_t launch_mx_rows(const MxRowsArgs& a, bool back, hipStream_t st);  // back: codes to values
 
+// y [M][out] = act(Q(x) W^T + bias) + residual over MXFP4 weights [cols][in / 2] with scales [cols][in / 32]; gated as for
+// LinearArgs.  x: 16-bit values (xs null), quantized to `form`, or codes of it with their scales xs.
+struct MxLinearArgs {
+    const void* x;
+    const uint8_t *xs, *w, *ws;
+    const uint16_t *bias, *residual;  // of the 16-bit type, or null
+    void* y;
+    int64_t M, out, in, ldx, ldxs, ldr, ldy;
+    int form, f16, y_f32, act, gated;
+    uint8_t* work;  // mx_linear_ws(...) bytes
+};
+int64_t mx_linear_ws(int64_t M, int64_t out, int64_t in, int gated, int form, bool codes);
+hipError_t launch_mx_linear(const MxLinearArgs& a, hipStream_t st);
+
 // A paged cache of microscaled blocks; strides in bytes.
 struct MxCache {
     uint8_t *kc, *vc, *ks, *vs;

@@ -97,3 +97,65 @@ def test_helpers_refuse():
     _refused("slots", cq.kv_cache_write_mx, k, k, c, e, c, e, slots[:2])
     _refused("contiguous", cq.kv_cache_write_mx, k.transpose(1, 2).contiguous().transpose(1, 2), k, c, e, c, e, slots)
     _refused("GPU", cq.kv_cache_write_mx, k, k, c, e, c, e, slots)
+
+
+def _linear(ws=None, ws_bytes=0, **kw):
+    a = dict(x=FAKE, x_scales=None, qweight=FAKE, scales=FAKE, bias=None, residual=None, y=FAKE, ldx=256, ldxs=0, ldr=0,
+             ldy=8, M=4, out=8, inp=256, type=cq.BF16, x_format=cq.MXFP8, y_type=cq.BF16, activation=0, gated=0)
+    a.update(kw)
+    return cq.load().cq_mxfp4_linear(cq.Mxfp4LinearArgs(**a), ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(type=2), dict(type=-1), dict(y_type=cq.F16), dict(y_type=3), dict(activation=-1), dict(activation=5),
+    dict(gated=2), dict(x_format=2), dict(x_format=5), dict(M=-1), dict(out=-1), dict(inp=0), dict(inp=160),
+    dict(inp=-128), dict(M=1 << 31), dict(out=(1 << 25) + 1), dict(out=(1 << 24) + 1, gated=1), dict(inp=1 << 25),
+    dict(M=1 << 20, out=1 << 18), dict(M=1 << 20, inp=1 << 15, ldx=1 << 15), dict(x=None), dict(qweight=None), dict(scales=None), dict(y=None), dict(ldx=128),
+    dict(ldx=260), dict(ldy=7), dict(residual=FAKE, ldr=7), dict(x=FAKE + 8), dict(qweight=FAKE + 8),
+    dict(bias=FAKE + 1), dict(residual=FAKE + 1, ldr=8), dict(y=FAKE + 1), dict(y=FAKE + 2, y_type=cq.F32),
+    dict(x_scales=FAKE, ldxs=7), dict(x_scales=FAKE, ldxs=8, ldx=255), dict(x_scales=FAKE, ldxs=8, ldx=264),
+    dict(x_scales=FAKE, ldxs=8, ldx=112, x_format=cq.MXFP4),
+])
+def test_linear_rejects_before_launch(kw):
+    assert _linear(**kw) == -1
+
+
+def test_linear_without_rows_or_columns_is_a_no_op():
+    assert cq.load().cq_mxfp4_linear(None, None, 0, None) == -1
+    assert _linear(M=0, x=None, y=None) == 0 and _linear(out=0, qweight=None) == 0
+
+
+def test_linear_workspace():
+    size = cq.cq_mxfp4_linear_workspace_size
+    assert size(8192, 4096, 4096, 0, cq.MXFP4, 1) == 0 and size(1, 4096, 4096, 0, cq.MXFP8, 0) == 0
+    for form, each in ((cq.MXFP4, 0.5), (cq.MXFP8, 1.0)):
+        need = size(8192, 4096, 4096, 0, form, 0)
+        assert 8192 * 4096 * (each + 1 / 32) <= need <= 8192 * 4096 * (each + 1 / 32) + 4096
+        assert _linear(M=8192, out=4096, inp=4096, ldx=4096, ldy=4096, x_format=form) == -2
+        assert _linear(FAKE, need - 1, M=8192, out=4096, inp=4096, ldx=4096, ldy=4096, x_format=form) == -2
+        assert _linear(FAKE + 16, need, M=8192, out=4096, inp=4096, ldx=4096, ldy=4096, x_format=form) == -2
+    for bad in ((-1, 8, 128, 0, 3, 0), (4, -8, 128, 0, 3, 0), (4, 8, 100, 0, 3, 0), (4, 8, 128, 2, 3, 0), (4, 8, 128, 0, 0, 0)):
+        assert size(*bad) == 0
+
+
+def test_linear_helper_refuses():
+    x, w, s = torch.zeros((2, 128), dtype=torch.bfloat16), torch.zeros((6, 64), dtype=torch.uint8), \
+        torch.zeros((6, 4), dtype=torch.uint8)
+    _refused("format", cq.mxfp4_linear, x, w, s, x_format="e4m3")
+    _refused("matrix", cq.mxfp4_linear, x[0], w, s)
+    _refused("bfloat16 or float16", cq.mxfp4_linear, x.float(), w, s)
+    _refused("qweight", cq.mxfp4_linear, x, w.int(), s)
+    _refused("qweight", cq.mxfp4_linear, x[:, :64], w, s)
+    _refused("scales", cq.mxfp4_linear, x, w, s[:, :2])
+    _refused("scales", cq.mxfp4_linear, x, w, s.to(torch.bfloat16))
+    _refused("even", cq.mxfp4_linear, x, w[:5], s[:5], gated=True)
+    _refused("bias", cq.mxfp4_linear, x, w, s, bias=torch.zeros(6))
+    _refused("residual", cq.mxfp4_linear, x, w, s, residual=torch.zeros((2, 6)))
+    _refused("activation", cq.mxfp4_linear, x, w, s, activation="tanh")
+    _refused("contiguous", cq.mxfp4_linear, x, torch.zeros((64, 6), dtype=torch.uint8).t(), s)
+    _refused("GPU", cq.mxfp4_linear, x, w, s)
+    codes, xs = torch.zeros((2, 128), dtype=torch.uint8), torch.zeros((2, 4), dtype=torch.uint8)
+    _refused("scales of x", cq.mxfp4_linear, codes, w, s, x_scales=xs, x_format="mxfp4")
+    _refused("uint8", cq.mxfp4_linear, x, w, s, x_scales=xs)
+    _refused("residual", cq.mxfp4_linear, codes, w, s, x_scales=xs, bias=torch.zeros(6).half(),
+             residual=torch.zeros((2, 6)).bfloat16())
