@@ -581,10 +581,11 @@ __global__ __launch_bounds__(2 * MANY, 2) void many_rows_kernel(AttentionArgs a,
     const int t0 = t_begin + split * per, t1 = min(t_end, t0 + per);
     const int32_t* table = a.table + r * a.table_stride;
 
-    // Where the rows of a block of keys lie, a thread per key: find() starts the table's load, note() ends it.
+    // Where the rows of a block of keys lie, a thread per key: find() starts the table's load, note() ends it.  A key that
+    // is not this part's has the page INT32_MIN, which no entry of the table may be taken for.
     auto find = [&](int b) {
         const int key = b * BLOCK + tid;
-        return key >= t0 * BN && key < t1 * BN && key >= w.key_begin && key < w.key_end ? table[page_of(pl, key)] : INT32_MIN;
+        return key >= t0 * BN && key < t1 * BN && key >= w.key_begin && key < w.key_end ? max(table[page_of(pl, key)], -1) : INT32_MIN;
     };
     auto note = [&](int b, int id) {
         const int key = b * BLOCK + tid;
