@@ -568,6 +568,16 @@ int32_t cq_kv_cache_write_mx(const void *k, int64_t k_token_stride, int64_t k_he
                              const int32_t *slots, int32_t n_tokens, void *stream);
 
 /*
+ * cq_paged_attention over such a cache.  Keys and values are those the blocks stand for, in q's 16-bit type: exact in
+ * bfloat16; where type is CQ_F16, what it cannot hold is an infinity or rounded (values quantized from binary16 are exact).
+ *   args   as for cq_paged_attention, whose k_cache, v_cache and their strides are not read; kv_heads, head_dim, page_size
+ *          and n_pages are the cache's.
+ * Masks, outputs, workspace, limits and errors as there; a NaN block has no effect on a row that does not see it.
+ */
+int32_t cq_paged_attention_mx(const cq_paged_attention_args *args, const cq_mx_cache *cache, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
  * Separately normalized environment diagonals from calibration activations
  * (CliffQuant README, "What CliffQuant changes": each channel's sensitivity
  * weighted by its activations, per calibration environment, each environment

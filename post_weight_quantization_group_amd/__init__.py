@@ -43,7 +43,7 @@ __all__ = [
     "paged_attention",
     "MXFP4", "MXFP8", "MX_BLOCK", "MxCache", "cq_mx_quantize", "mx_quantize", "cq_mx_dequantize", "mx_dequantize",
     "cq_kv_cache_write_mx", "kv_cache_write_mx", "Mxfp4LinearArgs", "cq_mxfp4_linear_workspace_size", "cq_mxfp4_linear",
-    "mxfp4_linear",
+    "mxfp4_linear", "cq_paged_attention_mx", "paged_attention_mx",
 ]
 
 GROUP = 128
@@ -74,7 +74,7 @@ EXPORTED_SYMBOLS = ("cq_abi_version", "cq_status_string", "cq_workspace_size", "
                     "cq_w4a16_matmul", "cq_probe_valu_fma", "cq_w4a16_linear", "cq_kv_block_map",
                     "cq_kv_cache_write", "cq_paged_attention_workspace_size", "cq_paged_attention",
                     "cq_mx_quantize", "cq_mx_dequantize", "cq_kv_cache_write_mx", "cq_mxfp4_linear_workspace_size",
-                    "cq_mxfp4_linear")
+                    "cq_mxfp4_linear", "cq_paged_attention_mx")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lib = None
@@ -190,6 +190,8 @@ def load():
         lib.cq_mxfp4_linear_workspace_size.argtypes = [I64, I64, I64, I32, I32, I32]
         lib.cq_mxfp4_linear.restype = I32
         lib.cq_mxfp4_linear.argtypes = [ctypes.POINTER(Mxfp4LinearArgs), P, SZ, P]
+        lib.cq_paged_attention_mx.restype = I32
+        lib.cq_paged_attention_mx.argtypes = [ctypes.POINTER(PagedAttentionArgs), ctypes.POINTER(MxCache), P, SZ, P]
         _lib = lib
     return _lib
 
@@ -467,6 +469,11 @@ def cq_mxfp4_linear_workspace_size(M: int, out: int, inp: int, gated: int, x_for
 def cq_mxfp4_linear(args: Mxfp4LinearArgs, workspace=None, stream=None):
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(load().cq_mxfp4_linear(args, _p(workspace), ws_bytes, _stream(stream)), "cq_mxfp4_linear")
+
+
+def cq_paged_attention_mx(args: PagedAttentionArgs, cache: MxCache, workspace=None, stream=None):
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().cq_paged_attention_mx(args, cache, _p(workspace), ws_bytes, _stream(stream)), "cq_paged_attention_mx")
 
 
 # ---------------------------------------------------------------- helpers
@@ -1056,6 +1063,53 @@ def kv_cache_write_mx(k, v, k_cache, k_scales, v_cache, v_scales, slots, stream=
     _check((_lib or load()).cq_kv_cache_write_mx(pk, _step(k, 0), _step(k, 1), pv, _step(v, 0), _step(v, 1),
                                                  _TYPES[k.dtype], cache, ps, T, _stream_on(stream, device)),
            "cq_kv_cache_write_mx")
+
+
+def paged_attention_mx(q, k_cache, k_scales, v_cache, v_scales, block_table, cu_q, kv_len, max_q, max_kv, scale=None,
+                       causal=True, window=0, out=None, lse=None, workspace=None, stream=None):
+    """paged_attention over a cache of microscaled blocks, as kv_cache_write_mx fills it: codes uint8 [pages, kv_heads,
+    page_size, head_dim] (mxfp8) or [.., head_dim / 2] (mxfp4), scales uint8 [.., head_dim / 32]; head_dim a multiple of
+    32.  Everything else as there."""
+    dt = q.dtype
+    if q.dim() != 3 or dt not in (torch.bfloat16, torch.float16) or q.stride(2) != 1:
+        raise ValueError("q must be bfloat16 or float16 [T, heads, head_dim], head_dim contiguous")
+    _int32(block_table=block_table, cu_q=cu_q, kv_len=kv_len)
+    T, H, D = q.shape
+    R = kv_len.numel()
+    if cu_q.numel() != R + 1 or block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("cu_q must be [R + 1], kv_len [R], block_table [R, max_pages]")
+    _contiguous(cu_q=cu_q, kv_len=kv_len)
+    if lse is not None:
+        if lse.shape != (T, H) or lse.dtype != torch.float32:
+            raise ValueError("lse must be float32 [T, heads]")
+        _contiguous(lse=lse)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages, kv_heads, page_size, head_dim (mxfp8) or head_dim / 2 (mxfp4)]")
+    device = _gpu(q)
+    if device != _device_now():
+        with torch.cuda.device(device):
+            return paged_attention_mx(q, k_cache, k_scales, v_cache, v_scales, block_table, cu_q, kv_len, max_q, max_kv,
+                                      scale, causal, window, out, lse, workspace, stream)
+    pages, Hkv, page, _ = k_cache.shape
+    cache = _mx_cache(k_cache, k_scales, v_cache, v_scales, Hkv, D, device)
+    if out is None:
+        out = _empty((T, H, D), dt, q, stream)
+    elif out.shape != q.shape or out.dtype != dt or out.stride(2) != 1:
+        raise ValueError("out must be [T, heads, head_dim] of q's type, head_dim contiguous")
+    lib = _lib or load()
+    need = lib.cq_paged_attention_workspace_size(T, R, max_q, max_kv, H, Hkv, D)
+    if need and workspace is None:
+        workspace = _empty(need, torch.uint8, q, stream)
+    pq, pt, pcu, pkv, po, pl, pw = _on(device, ("q", q), ("block_table", block_table), ("cu_q", cu_q),
+                                       ("kv_len", kv_len), ("out", out), ("lse", lse), ("workspace", workspace))
+    args = PagedAttentionArgs.from_buffer_copy(_ATTENTION_ARGS.pack(
+        pq, 0, 0, pt, pcu, pkv, po, pl or 0, _step(q, 0), _step(q, 1), _step(out, 0), _step(out, 1), 0, 0, 0,
+        _ld(block_table), _TYPES[dt], T, R, max_q, max_kv, H, Hkv, D, page, pages, block_table.shape[1], int(causal),
+        window, D ** -0.5 if scale is None else scale))
+    _check(lib.cq_paged_attention_mx(args, cache, pw,
+                                     0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                     _stream_on(stream, device)), "cq_paged_attention_mx")
+    return out
 
 
 def environment_diagonals(x, stream=None):

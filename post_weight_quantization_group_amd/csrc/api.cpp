@@ -555,10 +555,11 @@ size_t cq_paged_attention_workspace_size(int32_t n_tokens, int32_t n_requests, i
     return (size_t)cqk::attention_ws(n_requests, n_tokens, max_q, max_kv, heads, kv_heads, head_dim) * 4u;
 }
 
-int32_t cq_paged_attention(const cq_paged_attention_args* args, void* workspace, size_t workspace_bytes,
-                           void* stream) {
-    if (!args) return CQ_EINVAL;
-    const cq_paged_attention_args& p = *args;
+// Checks of what both attentions take (the cache's own arrays and strides apart) and the kernels' arguments; `nothing`:
+// there is no token.
+static int32_t attention_args(const cq_paged_attention_args& p, void* workspace, size_t workspace_bytes,
+                              cqk::AttentionArgs& a, bool& nothing) {
+    nothing = false;
     if (p.type != CQ_BF16 && p.type != CQ_F16) return CQ_EINVAL;
     if (!attention_sizes_ok(p.n_tokens, p.n_requests, p.max_q, p.max_kv, p.heads, p.kv_heads, p.head_dim))
         return CQ_EINVAL;
@@ -566,34 +567,70 @@ int32_t cq_paged_attention(const cq_paged_attention_args* args, void* workspace,
     if ((int64_t)p.max_pages * p.page_size > (int64_t)1 << 30) return CQ_EINVAL;
     if ((p.causal != 0 && p.causal != 1) || p.window < 0 || (p.window > 0 && !p.causal)) return CQ_EINVAL;
     if (!(p.scale - p.scale == 0.0f)) return CQ_EINVAL;
-    if ((p.q_token_stride | p.q_head_stride | p.out_token_stride | p.out_head_stride | p.page_stride | p.head_stride |
-         p.row_stride) < 0 ||
-        (p.q_token_stride | p.q_head_stride | p.out_token_stride | p.out_head_stride | p.page_stride | p.head_stride |
-         p.row_stride) % 8 != 0)
-        return CQ_EINVAL;
-    if (p.n_tokens == 0) return CQ_OK;
+    const int64_t strides = p.q_token_stride | p.q_head_stride | p.out_token_stride | p.out_head_stride;
+    if (strides < 0 || strides % 8 != 0) return CQ_EINVAL;
+    nothing = p.n_tokens == 0;
+    if (nothing) return CQ_OK;
     if (!p.q || !p.out || !p.cu_q) return CQ_EINVAL;
     if (p.n_requests > 0 && !p.kv_len) return CQ_EINVAL;
-    if (p.n_pages > 0 && p.max_pages > 0 && p.n_requests > 0 && (!p.k_cache || !p.v_cache || !p.block_table))
-        return CQ_EINVAL;
-    if (!aligned(p.q, 16) || !aligned(p.k_cache, 16) || !aligned(p.v_cache, 16) || !aligned(p.out, 16) ||
-        !aligned(p.block_table, 4) || !aligned(p.cu_q, 4) || !aligned(p.kv_len, 4) || !aligned(p.lse, 4))
+    if (p.n_pages > 0 && p.max_pages > 0 && p.n_requests > 0 && !p.block_table) return CQ_EINVAL;
+    if (!aligned(p.q, 16) || !aligned(p.out, 16) || !aligned(p.block_table, 4) || !aligned(p.cu_q, 4) ||
+        !aligned(p.kv_len, 4) || !aligned(p.lse, 4))
         return CQ_EINVAL;
     if (!cqk::attention_fits(p.n_requests, p.n_tokens, p.max_q, p.max_kv, p.heads, p.kv_heads, p.head_dim))
         return CQ_EUNSUPPORTED;
     const size_t need = cq_paged_attention_workspace_size(p.n_tokens, p.n_requests, p.max_q, p.max_kv, p.heads,
                                                           p.kv_heads, p.head_dim);
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, ALIGN))) return CQ_EWORKSPACE;
-    cqk::AttentionArgs a{};
-    a.q = (const uint16_t*)p.q; a.kc = (const uint16_t*)p.k_cache; a.vc = (const uint16_t*)p.v_cache;
-    a.out = (uint16_t*)p.out; a.lse = p.lse; a.table = p.block_table; a.cu = p.cu_q; a.kv_len = p.kv_len;
+    a = cqk::AttentionArgs{};
+    a.q = (const uint16_t*)p.q; a.out = (uint16_t*)p.out; a.lse = p.lse;
+    a.table = p.block_table; a.cu = p.cu_q; a.kv_len = p.kv_len;
     a.q_tok = p.q_token_stride; a.q_head = p.q_head_stride; a.o_tok = p.out_token_stride; a.o_head = p.out_head_stride;
-    a.c_page = p.page_stride; a.c_head = p.head_stride; a.c_row = p.row_stride; a.table_stride = p.table_stride;
-    a.page = p.page_size; a.n_pages = p.n_pages; a.max_pages = p.max_pages;
+    a.table_stride = p.table_stride; a.page = p.page_size; a.n_pages = p.n_pages; a.max_pages = p.max_pages;
     a.R = p.n_requests; a.T = p.n_tokens; a.max_q = p.max_q; a.max_kv = p.max_kv;
     a.H = p.heads; a.Hkv = p.kv_heads; a.D = p.head_dim; a.causal = p.causal; a.window = p.window;
     a.f16 = p.type == CQ_F16; a.scale = p.scale; a.ws = (float*)workspace;
+    return CQ_OK;
+}
+
+int32_t cq_paged_attention(const cq_paged_attention_args* args, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+    if (!args) return CQ_EINVAL;
+    const cq_paged_attention_args& p = *args;
+    if ((p.page_stride | p.head_stride | p.row_stride) < 0 || (p.page_stride | p.head_stride | p.row_stride) % 8 != 0)
+        return CQ_EINVAL;
+    if (p.n_tokens > 0) {
+        if (p.n_pages > 0 && p.max_pages > 0 && p.n_requests > 0 && (!p.k_cache || !p.v_cache)) return CQ_EINVAL;
+        if (!aligned(p.k_cache, 16) || !aligned(p.v_cache, 16)) return CQ_EINVAL;
+    }
+    cqk::AttentionArgs a;
+    bool nothing;
+    const int32_t status = attention_args(p, workspace, workspace_bytes, a, nothing);
+    if (status != CQ_OK || nothing) return status;
+    a.kc = (const uint16_t*)p.k_cache; a.vc = (const uint16_t*)p.v_cache;
+    a.c_page = p.page_stride; a.c_head = p.head_stride; a.c_row = p.row_stride;
     return hip_status(cqk::launch_attention(a, (hipStream_t)stream));
+}
+
+int32_t cq_paged_attention_mx(const cq_paged_attention_args* args, const cq_mx_cache* cache, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+    if (!args || !cache || !mx_cache_ok(*cache)) return CQ_EINVAL;
+    const cq_paged_attention_args& p = *args;
+    const cq_mx_cache& c = *cache;
+    if (p.kv_heads != c.kv_heads || p.head_dim != c.head_dim || p.page_size != c.page_size || p.n_pages != c.n_pages)
+        return CQ_EINVAL;
+    if (p.n_tokens > 0 && p.n_pages > 0 && p.max_pages > 0 && p.n_requests > 0 &&
+        (!c.k_codes || !c.v_codes || !c.k_scales || !c.v_scales))
+        return CQ_EINVAL;
+    cqk::AttentionArgs a;
+    bool nothing;
+    const int32_t status = attention_args(p, workspace, workspace_bytes, a, nothing);
+    if (status != CQ_OK || nothing) return status;
+    const cqk::MxCache m = mx_cache(c);
+    a.kc = (const uint16_t*)m.kc; a.vc = (const uint16_t*)m.vc; a.ks = m.ks; a.vs = m.vs;
+    a.c_page = m.c_page; a.c_head = m.c_head; a.c_row = m.c_row;
+    a.s_page = m.s_page; a.s_head = m.s_head; a.s_row = m.s_row;
+    return hip_status(cqk::launch_attention_mx(a, m.form, (hipStream_t)stream));
 }
 
 size_t cq_diagonals_workspace_size(int32_t E, int64_t T, int64_t in) {

@@ -87,6 +87,8 @@ struct AttentionArgs {
     const int32_t *table, *cu, *kv_len;
     int64_t q_tok, q_head, o_tok, o_head;
     int64_t c_page, c_head, c_row;
+    const uint8_t *ks, *vs;  // microscaled blocks: their scales; kc, vc and all strides of the cache are then of bytes
+    int64_t s_page, s_head, s_row;
     int64_t table_stride;
     int32_t page, n_pages, max_pages;
     int32_t R, T, max_q, max_kv, H, Hkv, D, causal, window, f16;
@@ -98,5 +100,6 @@ bool attention_fits(int32_t R, int32_t T, int32_t max_q, int32_t max_kv, int32_t
 // Floats of workspace the launch for these sizes uses (0: none).
 int64_t attention_ws(int32_t R, int32_t T, int32_t max_q, int32_t max_kv, int32_t H, int32_t Hkv, int32_t D);
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t st);
+hipError_t launch_attention_mx(const AttentionArgs& a, int form, hipStream_t st);
 
 }  // namespace cqk

@@ -159,3 +159,54 @@ def test_linear_helper_refuses():
     _refused("uint8", cq.mxfp4_linear, x, w, s, x_scales=xs)
     _refused("residual", cq.mxfp4_linear, codes, w, s, x_scales=xs, bias=torch.zeros(6).half(),
              residual=torch.zeros((2, 6)).bfloat16())
+
+
+def _attention(ws=None, ws_bytes=0, **kw):
+    a = dict(q=FAKE, k_cache=None, v_cache=None, block_table=FAKE, cu_q=FAKE, kv_len=FAKE, out=FAKE, lse=None,
+             q_token_stride=256, q_head_stride=64, out_token_stride=256, out_head_stride=64, page_stride=0,
+             head_stride=0, row_stride=0, table_stride=4, type=cq.BF16, n_tokens=3, n_requests=2, max_q=2, max_kv=64,
+             heads=4, kv_heads=2, head_dim=64, page_size=16, n_pages=9, max_pages=4, causal=1, window=0, scale=0.125)
+    cache = _cache(**kw.pop("mx", {}))
+    a.update(kw)
+    return cq.load().cq_paged_attention_mx(cq.PagedAttentionArgs(**a), cache, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw", [dict(mx=m) for m in BAD_CACHES] + [
+    dict(mx=dict(n_pages=8)), dict(mx=dict(kv_heads=4)), dict(mx=dict(page_size=8)), dict(mx=dict(head_dim=128)),
+    dict(mx=dict(k_codes=None)), dict(mx=dict(v_codes=None)), dict(mx=dict(k_scales=None)), dict(mx=dict(v_scales=None)),
+    dict(type=cq.F32), dict(n_tokens=-1), dict(n_requests=65536), dict(max_q=-1), dict(heads=3), dict(table_stride=3),
+    dict(max_pages=1 << 28, table_stride=1 << 28), dict(causal=2), dict(window=3, causal=0), dict(scale=float("nan")),
+    dict(q_token_stride=-256), dict(q_head_stride=60), dict(q=None), dict(out=None), dict(cu_q=None), dict(kv_len=None),
+    dict(block_table=None), dict(q=FAKE + 8), dict(out=FAKE + 8), dict(lse=FAKE + 2), dict(cu_q=FAKE + 1),
+])
+def test_attention_rejects_before_launch(kw):
+    assert _attention(**kw) == -1
+
+
+def test_attention_workspace_and_limits():
+    assert cq.load().cq_paged_attention_mx(None, _cache(), None, 0, None) == -1
+    assert cq.load().cq_paged_attention_mx(cq.PagedAttentionArgs(), None, None, 0, None) == -1
+    assert _attention(n_tokens=0, q=None) == 0
+    assert _attention(max_kv=4096, max_pages=256, table_stride=256) == -2
+    assert _attention(ws=FAKE, ws_bytes=1 << 50, n_requests=65535, heads=256, kv_heads=256, max_q=17,
+                      mx=dict(kv_heads=256)) == -4
+
+
+def test_attention_helper_refuses():
+    q, t = torch.zeros((3, 4, 64), dtype=torch.bfloat16), torch.zeros((2, 4), dtype=torch.int32)
+    cu, kv = torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    c, e = torch.zeros((9, 2, 16, 64), dtype=torch.uint8), torch.zeros((9, 2, 16, 2), dtype=torch.uint8)
+    _refused("bfloat16 or float16", cq.paged_attention_mx, q.float(), c, e, c, e, t, cu, kv, 2, 64)
+    _refused("int32", cq.paged_attention_mx, q, c, e, c, e, t.long(), cu, kv, 2, 64)
+    _refused("cu_q", cq.paged_attention_mx, q, c, e, c, e, t, cu[:2], kv, 2, 64)
+    _refused("lse", cq.paged_attention_mx, q, c, e, c, e, t, cu, kv, 2, 64, lse=torch.zeros(3, 4).half())
+    _refused("k_cache", cq.paged_attention_mx, q, c[0], e, c, e, t, cu, kv, 2, 64)
+    _refused("GPU", cq.paged_attention_mx, q, c, e, c, e, t, cu, kv, 2, 64)
+    _refused("strided alike", cq._mx_cache, c, e, c[:8], e, 2, 64, -1)
+    _refused("strided alike", cq._mx_cache, c, e, c.transpose(1, 2).contiguous().transpose(1, 2), e, 2, 64, -1)
+    _refused("mxfp8", cq._mx_cache, c, e, c, e, 2, 256, -1)
+    _refused("multiple of 32", cq._mx_cache, c[..., :48], e, c[..., :48], e, 2, 48, -1)
+    _refused("k_scales", cq._mx_cache, c, e[..., :1], c, e, 2, 64, -1)
+    _refused("k_scales", cq._mx_cache, c, e, c, e[:, :, :8], 2, 64, -1)
+    _refused("uint8", cq._mx_cache, c.view(torch.int8), e, c, e, 2, 64, -1)
+    _refused("contiguous", cq._mx_cache, *[torch.zeros((9, 2, 64, 16), dtype=torch.uint8).transpose(2, 3), e] * 2, 2, 64, -1)

@@ -1,0 +1,257 @@
+"""GPU: attention over a paged cache of microscaled blocks (cq_paged_attention_mx) against its definition in 64 bits over
+the values that the blocks stand for, within the bound of oracle.serving.paged_attention.  Every slot that no request
+holds is NaN."""
+import numpy as np
+import pytest
+import torch
+
+import post_weight_quantization_group_amd as cq
+from oracle import microscaling as mx
+from parity import dev, say
+from serving import Paged, close, i32
+
+pytestmark = pytest.mark.gpu
+
+FORMS = ["mxfp4", "mxfp8"]
+
+
+class PagedMx(Paged):
+    def __init__(self, lens, H, Hkv, D, page, kind, form, seed=0, order="hnd", spread=0, **kw):
+        say("attention mx:", lens, H, Hkv, D, page, kind, form, order)
+        super().__init__(lens, H, Hkv, D, page, kind, seed=seed, **kw)
+        self.form = form
+        rng = np.random.default_rng(seed + 1)
+        for name in ("kc", "vc"):
+            values = getattr(self, name + "_np")
+            if spread:  # blocks of different sizes
+                values = values * 2.0 ** rng.integers(-spread, spread + 1, values.shape[:3] + (1,))
+            codes, scales = mx.quantize(values, form)
+            codes = np.where(np.repeat(scales, codes.shape[-1] * 32 // D, -1) == 255,
+                             rng.integers(0, 256, codes.shape), codes).astype(np.uint8)  # (what lies there is anything)
+            setattr(self, name + "_np", mx.dequantize(codes, scales, form))
+            arrays = [dev(codes), dev(scales)]
+            if order == "nhd":
+                arrays = [a.transpose(1, 2).contiguous().transpose(1, 2) for a in arrays]
+            setattr(self, name + "_mx", arrays)
+
+    def run(self, cq, **kw):
+        kw = dict(dict(q=self.q, k_cache=self.kc_mx[0], k_scales=self.kc_mx[1], v_cache=self.vc_mx[0],
+                       v_scales=self.vc_mx[1], block_table=self.table, cu_q=self.cu, kv_len=self.kv, max_q=self.max_q,
+                       max_kv=self.max_kv), **kw)
+        return cq.paged_attention_mx(**kw)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("H,Hkv,D,page", [(8, 2, 128, 16), (4, 4, 64, 16), (5, 1, 96, 24), (16, 2, 256, 64),
+                                          (2, 1, 32, 1), (32, 1, 96, 8), (6, 2, 192, 128)])
+def test_single_tokens(H, Hkv, D, page, kind, form):
+    PagedMx([(1, 1), (1, 2), (1, 17), (1, 64), (1, 65), (1, 300)], H, Hkv, D, page, kind, form).check(cq)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("lens", [[(1, 1)], [(5, 5), (3, 40), (1, 9)], [(33, 33), (0, 20), (64, 130)], [(130, 200)],
+                                  [(257, 300), (2, 2)]])
+@pytest.mark.parametrize("H,Hkv,D,page", [(8, 2, 128, 16), (3, 3, 64, 8), (2, 1, 256, 48)])
+def test_chunks(lens, H, Hkv, D, page, kind, form):
+    PagedMx(lens, H, Hkv, D, page, kind, form, seed=len(lens)).check(cq)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("D", [32, 64, 96, 128, 160, 192, 224, 256])
+def test_head_dims(D, form):
+    PagedMx([(40, 70), (1, 90)], 4, 2, D, 16, "bf16", form, seed=D, spread=3).check(cq)
+    PagedMx([(1, 70), (1, 90)], 4, 2, D, 16, "f16", form, seed=D, spread=3).check(cq)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("group", [1, 2, 3, 7, 8, 16, 17, 33])
+def test_head_groups(group, form):
+    PagedMx([(20, 50), (1, 33)], 2 * group, 2, 64, 16, "bf16", form, seed=group).check(cq)
+    PagedMx([(1, 50), (1, 33)], 2 * group, 2, 64, 16, "bf16", form, seed=group).check(cq)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("page", [1, 3, 16, 31, 32, 33, 100, 512])
+def test_pages_that_end_inside_a_tile(page, form):
+    PagedMx([(1, 129), (1, 31)], 4, 1, 64, page, "bf16", form, seed=page).check(cq)
+    PagedMx([(70, 129), (1, 31)], 4, 1, 128, page, "bf16", form, seed=page).check(cq)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("window", [1, 2, 16, 50, 1000])
+@pytest.mark.parametrize("lens", [[(1, 200), (1, 3)], [(90, 200), (7, 7)]])
+def test_window(lens, window, form):
+    PagedMx(lens, 4, 2, 128, 16, "f16", form, seed=window).check(cq, window=window)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("lens", [[(1, 200)], [(9, 20), (40, 70)], [(150, 150)]])
+def test_not_causal_and_other_scales(lens, form):
+    p = PagedMx(lens, 4, 2, 64, 16, "bf16", form)
+    p.check(cq, causal=False)
+    p.check(cq, scale=-0.3)
+    p.check(cq, scale=0.0)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("lens", [[(1, 5000), (1, 1)], [(1, 20000)], [(3, 4097), (2, 600)], [(100, 2500), (1, 4000)]])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_longer_caches(lens, D, form):
+    PagedMx(lens, 2, 1, D, 16, "bf16", form, seed=len(lens)).check(cq)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("lens", [[(4, 4), (1, 1)], [(1, 1), (1, 3)], [(200, 200)]])
+def test_rows_that_see_nothing(lens, form):
+    p = PagedMx(lens, 4, 2, 64, 16, "bf16", form)
+    for kv in ([n - 1 for n, _ in lens], [0] * len(lens), [n // 2 for n, _ in lens]):
+        p.kv_np = np.array(kv)
+        p.kv = i32(kv)
+        p.check(cq)
+        p.check(cq, causal=True, window=2)
+    p.cu_np = np.minimum(p.cu_np, 1)
+    p.cu = i32(p.cu_np)
+    p.check(cq)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_pages_outside_the_pool(form):
+    """Keys of such a page count as masked; first, middle and last page of a request, for few rows and many."""
+    for lens in ([(1, 300), (1, 90)], [(100, 300), (2, 90)]):
+        for at, page in ((0, -1), (4, 1 << 30), (18, -(1 << 31))):
+            p = PagedMx(lens, 4, 2, 128, 16, "bf16", form)
+            p.table_np[0, at] = page
+            p.table = i32(p.table_np)
+            p.check(cq)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("lens", [[(1, 100), (3, 40)], [(90, 200), (40, 61)]])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_nan_blocks_that_rows_see_and_do_not_see(lens, D, form):
+    """A NaN block of V reaches the rows that see its key, in its 32 dimensions; one of K the rows that see its key."""
+    p = PagedMx(lens, 4, 2, D, 16, "bf16", form)
+    clean = p.run(cq)
+    r, key, block = 0, lens[0][1] - lens[0][0] // 2 - 1, D // 32 - 1
+    page, at = p.table_np[r, key // 16], key % 16
+    keep = p.vc_mx[1].clone()
+    p.vc_mx[1][page, 0, at, block] = 255
+    out = p.run(cq)
+    sees = torch.arange(lens[0][0], device="cuda") + lens[0][1] - lens[0][0] >= key
+    want = torch.zeros_like(out, dtype=torch.bool)
+    want[: lens[0][0], :2, 32 * block:] = sees[:, None, None]
+    assert want.any() and torch.equal(torch.isnan(out), want) and torch.equal(out[~want], clean[~want])
+    p.vc_mx[1].copy_(keep)
+    p.kc_mx[1][page, 1, at, block] = 255
+    out = p.run(cq)
+    want = torch.zeros_like(out, dtype=torch.bool)
+    want[: lens[0][0], 2:] = sees[:, None, None]
+    assert torch.equal(torch.isnan(out), want) and torch.equal(out[~want], clean[~want])
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_strides_and_orders(form):
+    """Token-major pages, strided q and out, a wide block table."""
+    for lens in ([(1, 90), (1, 17)], [(70, 90), (5, 17)]):
+        p = PagedMx(lens, 6, 3, 96, 8, "f16", form, order="nhd", table_extra=5)
+        T, H, D = p.q.shape
+        wide = torch.full((T, H, D + 16), float("nan"), dtype=p.q.dtype, device="cuda")
+        wide[:, :, :D] = p.q
+        hold = torch.full((H, T, D + 8), 3.0, dtype=p.q.dtype, device="cuda")
+        p.q = wide[:, :, :D]
+        p.check(cq, out=hold.transpose(0, 1)[:, :, :D])
+        assert (hold[:, :, D:] == 3).all()
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_every_code(form):
+    """Values that cover all codes at several scales, uniform weights: the sums of V come out."""
+    rng = np.random.default_rng(5)
+    p = PagedMx([(1, 512), (40, 512)], 2, 1, 128, 16, "bf16", form)
+    for name in ("kc", "vc"):
+        codes = rng.integers(0, 256, tuple(p.vc_mx[0].shape)).astype(np.uint8)
+        if form == "mxfp8":
+            codes = np.where((codes & 127) == 127, 0, codes)
+        scales = rng.integers(118, 122, tuple(p.vc_mx[1].shape)).astype(np.uint8)
+        setattr(p, name + "_np", mx.dequantize(codes, scales, form))
+        setattr(p, name + "_mx", [dev(codes), dev(scales)])
+    p.check(cq)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_padded_step(form):
+    """Tokens of no request in front and behind get zeros and -inf."""
+    for lens in ([(1, 40), (1, 70)], [(90, 100), (1, 500), (0, 3)]):
+        p = PagedMx(lens, 8, 2, 128, 16, "bf16", form)
+        n, T, front = p.q.shape[0], 700, 37
+        q, q_np = torch.full((T, 8, 128), float("nan"), dtype=p.q.dtype, device="cuda"), np.zeros((T, 8, 128))
+        q[front:front + n], q_np[front:front + n] = p.q, p.q_np
+        p.q, p.q_np, p.cu_np = q, q_np, p.cu_np + front
+        p.cu = i32(p.cu_np)
+        p.check(cq)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_cache_past_32_bits(form):
+    """Pages whose bytes lie beyond 2^32, in the requests' tables."""
+    D, page, Hkv = 256, 64, 2
+    width = D // 2 if form == "mxfp4" else D
+    n_pages = (1 << 32) // (Hkv * page * width) + 30
+    caches = [torch.zeros((n_pages, Hkv, page, w), dtype=torch.uint8, device="cuda") for w in (width, D // 32) * 2]
+    small = PagedMx([(1, 300), (40, 200)], 4, Hkv, D, page, "bf16", form)
+    have = small.kc_np.shape[0]
+    for c, s in zip(caches, small.kc_mx + small.vc_mx):
+        c[-have:] = s
+    table = torch.where(small.table < 0, small.table, small.table + (n_pages - have))
+    a = small.run(cq)
+    b = small.run(cq, k_cache=caches[0], k_scales=caches[1], v_cache=caches[2], v_scales=caches[3], block_table=table)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_write_then_attend(form):
+    """The path of a step: new keys and values are quantized into the pages, and attention reads them; the same as
+    attention over a 16-bit cache that holds the blocks' values."""
+    rng = np.random.default_rng(0)
+    Hkv, H, D, page = 2, 8, 128, 16
+    free = i32(rng.permutation(64))
+    n_free, table = i32([64]), torch.full((3, 20), -1, dtype=torch.int32, device="cuda")
+    width = D // 2 if form == "mxfp4" else D
+    caches = [torch.randint(0, 256, (64, Hkv, page, w), dtype=torch.uint8, device="cuda") for w in (width, D // 32) * 2]
+    wide = [torch.full((64, Hkv, page, D), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    ctx = i32([0, 0, 0])
+    for new in ([70, 33, 1], [1, 1, 1], [30, 0, 20], [1, 1, 1]):
+        T = sum(new)
+        m = cq.kv_block_map(ctx, i32(new), free, n_free, table, page, T)
+        qkv = torch.randn((T, H + 2 * Hkv, D), device="cuda").bfloat16()
+        k, v = qkv[:, H:H + Hkv], qkv[:, H + Hkv:]
+        cq.kv_cache_write_mx(k, v, *caches, m["slots"])
+        values = [cq.mx_dequantize(*cq.mx_quantize(t.contiguous(), form), form) for t in (k, v)]
+        cq.kv_cache_write(*values, *wide, m["slots"])
+        a = cq.paged_attention_mx(qkv[:, :H], *caches, table, m["cu_q"], m["kv_len"], max(new), 320)
+        b = cq.paged_attention(qkv[:, :H], *wide, table, m["cu_q"], m["kv_len"], max(new), 320)
+        torch.cuda.synchronize()
+        assert torch.isfinite(a).all() and (a.float() - b.float()).abs().max() <= 2.0 ** -7 * b.float().abs().max()
+        ctx, n_free = m["kv_len"].clone(), m["n_left"].clone()
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_stream_graph_and_workspace(form):
+    p = PagedMx([(1, 3000), (1, 70)], 4, 2, 128, 16, "bf16", form)
+    want = p.run(cq)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    need = cq.cq_paged_attention_workspace_size(2, 2, 1, 3000, 4, 2, 128)
+    got = p.run(cq, stream=side, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+    side.synchronize()
+    assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = p.run(cq)
+    for _ in range(4):
+        p.q.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, p.run(cq))
