@@ -207,6 +207,158 @@ hipError_t few(const MxLinearArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------------------------
+// Many rows: a workgroup takes BIG_M rows of x's codes and BIG_N rows of W (gated: half of them of the gate, the others of the
+// other half), 128 of k a step; its four waves 64 by 128 each, as 2 x 4 products of 32 x 32.  Codes and scales go from
+// memory straight into LDS, some steps ahead, one barrier a step.  16-byte pieces of a row lie turned in it by the row's
+// number, so that the rows which a quarter of a wave reads at once are in different banks.
+constexpr int BIG_M = 128, BIG_N = 256;
+
+template <int FORM>
+__device__ __forceinline__ f32x16 add_products_32(i32x8 w, int ws, i32x8 x, i32x8 large, int xs, f32x16 acc, bool high) {
+    if constexpr (FORM == MXFP4) {
+        if (high) return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc, 4, 4, 2, ws, 2, xs);
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc, 4, 4, 0, ws, 0, xs);
+    } else if (high) {
+        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc, 4, 0, 2, ws, 2, xs);
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, large, acc, 4, 0, 2, ws, 2, xs);
+    } else {
+        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc, 4, 0, 0, ws, 0, xs);
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, large, acc, 4, 0, 0, ws, 0, xs);
+    }
+}
+
+template <int FORM, bool F16>
+__global__ __launch_bounds__(256, 2) void many_rows_mx(MxLinearArgs a, int row_tiles, int col_tiles) {
+    constexpr int STAGES = FORM == MXFP4 ? 3 : 2;
+    constexpr int X_ROW = FORM == MXFP4 ? 64 : 128;  // bytes of a step's row of x; 64 of W
+    constexpr int X_LOADS = BIG_M * X_ROW / 1024 / 4, LOADS = 4 + X_LOADS + 2;  // a wave's a step
+    constexpr int LINE = BIG_N + 4;                                            // floats of a row in the epilogue
+    struct Stage {
+        uint8_t w[BIG_N * 64], x[BIG_M * X_ROW];
+        uint32_t ws[BIG_N], xs[2 * BIG_M];  // (the upper half: the same scales again, so that every wave loads as much)
+    };
+    constexpr int BYTES = STAGES * sizeof(Stage) > 64 * LINE * 4 ? STAGES * sizeof(Stage) : 64 * LINE * 4;
+    __shared__ __align__(1024) uint8_t lds[BYTES];
+    Stage* stage = reinterpret_cast<Stage*>(lds);
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 31, half = lane >> 5, wr = wave & 1, wc = wave >> 1;
+    // Workgroups go to the eight XCDs in turn: each XCD takes a run of tiles, in bands of 8 row tiles, so that the tiles
+    // it works on at a time share rows of x and W in its L2.
+    int64_t id = blockIdx.x;
+    {
+        const int64_t all = (int64_t)row_tiles * col_tiles, base = all / 8, more = all % 8, x = id % 8, j = id / 8;
+        id = x * base + (x < more ? x : more) + j;
+    }
+    const int64_t band = id / (8 * col_tiles), in_band = id % (8 * col_tiles);
+    const int64_t high = row_tiles - band * 8 < 8 ? row_tiles - band * 8 : 8;
+    const int64_t rt = band * 8 + in_band % high, ct = in_band / high;
+    const int per = a.gated ? BIG_N / 2 : BIG_N;  // outputs per workgroup
+    const int64_t m0 = rt * BIG_M, n0 = ct * per;
+    // row of W for row i of the tile; past the edge the last one
+    auto w_row = [&](int i) {
+        const bool up = a.gated && i >= BIG_N / 2;
+        const int64_t o = n0 + (up ? i - BIG_N / 2 : i);
+        return (o < a.out ? o : a.out - 1) + (up ? a.out : 0);
+    };
+    auto x_row = [&](int i) { return m0 + i < a.M ? m0 + i : a.M - 1; };
+    const int steps = (int)(a.in / 128);
+    const uint8_t *wp[4], *xp[X_LOADS], *wsp, *xsp;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 64 * wave + 16 * i + lane / 4;
+        wp[i] = a.w + w_row(row) * (a.in / 2) + 16 * ((lane & 3) ^ ((row >> 2) & 3));
+    }
+#pragma unroll
+    for (int i = 0; i < X_LOADS; ++i) {
+        if constexpr (FORM == MXFP4) {
+            const int row = 32 * wave + 16 * i + lane / 4;
+            xp[i] = static_cast<const uint8_t*>(a.x) + x_row(row) * a.ldx + 16 * ((lane & 3) ^ ((row >> 2) & 3));
+        } else {
+            const int row = 32 * wave + 8 * i + lane / 8;
+            xp[i] = static_cast<const uint8_t*>(a.x) + x_row(row) * a.ldx + 16 * ((lane & 7) ^ ((row >> 1) & 7));
+        }
+    }
+    wsp = a.ws + w_row(64 * wave + lane) * (a.in / MX_BLOCK);
+    xsp = a.xs + x_row(64 * (wave & 1) + lane) * a.ldxs;
+    auto ask = [&](int s) {
+        Stage& t = stage[s % STAGES];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_to_lds(wp[i] + (int64_t)s * 64, &t.w[(64 * wave + 16 * i) * 64]);
+#pragma unroll
+        for (int i = 0; i < X_LOADS; ++i)
+            load_to_lds(xp[i] + (int64_t)s * X_ROW, &t.x[(32 * wave + (FORM == MXFP4 ? 16 : 8) * i) * X_ROW]);
+        load_to_lds_4(wsp + 4 * s, &t.ws[64 * wave]);
+        load_to_lds_4(xsp + 4 * s, &t.xs[64 * wave]);
+    };
+    f32x16 acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    for (int s = 0; s < STAGES - 1 && s < steps; ++s) ask(s);
+    for (int s = 0; s < steps; ++s) {
+        if (s + STAGES - 2 < steps) loaded_to_lds<(STAGES - 2) * LOADS>();
+        else loaded_to_lds<0>();
+        __syncthreads();  // this step's codes are in LDS, and the previous step's have been read
+        if (s + STAGES - 1 < steps) ask(s + STAGES - 1);
+        const Stage& t = stage[s % STAGES];
+        int ws[4], xs[2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ws[i] = (int)(t.ws[128 * wc + 32 * i + r] >> (8 * half));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) xs[j] = (int)(t.xs[64 * wr + 32 * j + r] >> (8 * half));
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            i32x8 w[4], x[2], large[2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = operand(*reinterpret_cast<const uint4*>(&t.w[(128 * wc + 32 * i + r) * 64 + 16 * ((2 * ks + half) ^ ((r >> 2) & 3))]));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint8_t* row = &t.x[(64 * wr + 32 * j + r) * X_ROW];
+                if constexpr (FORM == MXFP4) {
+                    x[j] = operand(*reinterpret_cast<const uint4*>(row + 16 * ((2 * ks + half) ^ ((r >> 2) & 3))));
+                    large[j] = x[j];
+                } else {
+                    x[j] = operand(*reinterpret_cast<const uint4*>(row + 16 * ((4 * ks + half) ^ ((r >> 1) & 7))),
+                                   *reinterpret_cast<const uint4*>(row + 16 * ((4 * ks + 2 + half) ^ ((r >> 1) & 7))));
+                    large[j] = large_elements(x[j]);
+                    x[j] ^= large[j];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i][j] = add_products_32<FORM>(w[i], ws[i], x[j], large[j], xs[j], acc[i][j], ks);
+        }
+    }
+    // The epilogue, 32 rows of every wave at a time through LDS: a thread then has four neighbouring outputs of a row, and
+    // residual and y move in whole lines.
+    const bool wide = outputs_in_fours(a);
+    float* tile = reinterpret_cast<float*>(lds);  // [64][LINE]
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<f32x4*>(&tile[(32 * wr + r) * LINE + 128 * wc + 32 * i + 2 * e + 4 * half]) =
+                    f32x4{acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]};
+        __syncthreads();
+        const int n = 4 * (tid % (per / 4)), lines = 1024 / per;
+        for (int row = tid / (per / 4); row < 64; row += lines) {
+            const f32x4 z = *reinterpret_cast<const f32x4*>(&tile[row * LINE + n]);
+            f32x4 up = {0, 0, 0, 0};
+            if (a.gated) up = *reinterpret_cast<const f32x4*>(&tile[row * LINE + BIG_N / 2 + n]);
+            finish4<F16>(a, m0 + 64 * (row >> 5) + 32 * j + (row & 31), n0 + n, z, up, wide);
+        }
+    }
+}
+
 // Rows of x up to which its 16-bit values are quantized by the lanes that multiply them; above, once for all columns.
 constexpr int64_t WITHIN = 32;
 
@@ -218,6 +370,11 @@ hipError_t launch_few(const MxLinearArgs& a, hipStream_t st) {
 
 template <int FORM, bool F16>
 hipError_t launch_type(const MxLinearArgs& a, hipStream_t st) {
+    const int64_t rt = (a.M + BIG_M - 1) / BIG_M, ct = (a.out + (a.gated ? BIG_N / 2 : BIG_N) - 1) / (a.gated ? BIG_N / 2 : BIG_N);
+    if (a.xs && rt * ct >= 64) {
+        hipLaunchKernelGGL((many_rows_mx<FORM, F16>), dim3((unsigned)(rt * ct)), dim3(256), 0, st, a, (int)rt, (int)ct);
+        return hipGetLastError();
+    }
     if (a.xs) return launch_few<FORM, X_CODES, F16>(a, st);
     return launch_few<FORM, F16 ? X_F16 : X_BF16, F16>(a, st);
 }
