@@ -522,13 +522,13 @@ int32_t cq_mx_dequantize(const uint8_t *codes, int64_t ldc, const uint8_t *scale
  *   type       CQ_BF16 or CQ_F16: of bias and residual, of x where it is not codes, and of y unless y_type is CQ_F32.
  *   x_format   CQ_MXFP4 or CQ_MXFP8.
  *   x          x_scales NULL: [M] rows of `in` values, ldx elements apart (a multiple of 8).  Else [M] rows of codes, in / 2
- *              (CQ_MXFP8: in) bytes, ldx bytes apart (a multiple of 16).  16-byte aligned.
- *   x_scales   nullable, [M] rows of in / 32 bytes, ldxs apart.
- *   qweight    [cols] rows of in / 2 bytes without gaps, 16-byte aligned; scales [cols] rows of in / 32 bytes: W in
- *              MXFP4, as cq_mx_quantize gives them for [cols][in].  cols = out, or 2 out when gated (the gate's first).
+ *              (CQ_MXFP8: in) bytes, ldx bytes apart (a multiple of 16 up to 2^23).  16-byte aligned.
+ *   x_scales   nullable, [M] rows of in / 32 bytes, ldxs apart (a multiple of 4); 4-byte aligned.
+ *   qweight    [cols] rows of in / 2 bytes without gaps, 16-byte aligned; scales [cols] rows of in / 32 bytes, 4-byte
+ *              aligned: W in MXFP4, as cq_mx_quantize gives them for [cols][in].  cols = out, or 2 out when gated (the gate's first).
  *   bias, residual, y, activation, gated   as for cq_w4a16_linear.
  *   workspace  cq_mxfp4_linear_workspace_size(...) bytes for the same sizes (0: may be NULL); `codes`: whether x is.
- * in a positive multiple of 128 up to 2^24; cols <= 2^25, M * cols < 2^38, M * in < 2^35, M < 2^31; M == 0 or out == 0 enqueues nothing.
+ * in a positive multiple of 128 up to 2^22; cols <= 2^25, M * cols < 2^38, M * in < 2^35, M < 2^31; M == 0 or out == 0 enqueues nothing.
  */
 typedef struct cq_mxfp4_linear_args {
     const void *x;

@@ -471,7 +471,7 @@ int32_t cq_mx_dequantize(const uint8_t* codes, int64_t ldc, const uint8_t* scale
 
 static bool mx_linear_sizes_ok(int64_t M, int64_t out, int64_t in, int32_t gated, int32_t x_format) {
     if ((x_format != CQ_MXFP4 && x_format != CQ_MXFP8) || (gated != 0 && gated != 1)) return false;
-    if (M < 0 || out < 0 || in <= 0 || in % CQ_GROUP != 0 || in > (int64_t)1 << 24) return false;
+    if (M < 0 || out < 0 || in <= 0 || in % CQ_GROUP != 0 || in > (int64_t)1 << 22) return false;
     if (M > INT32_MAX || out > (int64_t)1 << (gated ? 24 : 25)) return false;
     return M * (gated ? 2 * out : out) < (int64_t)1 << 38 && M * in < (int64_t)1 << 35;
 }
@@ -491,11 +491,12 @@ int32_t cq_mxfp4_linear(const cq_mxfp4_linear_args* args, void* workspace, size_
     if (p.M == 0 || p.out == 0) return CQ_OK;
     if (!p.x || !p.qweight || !p.scales || !p.y) return CQ_EINVAL;
     const bool codes = p.x_scales != nullptr;
-    if (codes ? p.ldx < (p.x_format == CQ_MXFP4 ? p.in / 2 : p.in) || p.ldx % 16 != 0 || p.ldxs < p.in / CQ_MX_BLOCK
+    if (codes && p.ldx > (int64_t)1 << 23) return CQ_EINVAL;  // (a tile's rows are numbered by bytes in 32 bits)
+    if (codes ? p.ldx < (p.x_format == CQ_MXFP4 ? p.in / 2 : p.in) || p.ldx % 16 != 0 || p.ldxs < p.in / CQ_MX_BLOCK || p.ldxs % 4 != 0
               : p.ldx < p.in || p.ldx % 8 != 0)
         return CQ_EINVAL;
     if (p.ldy < p.out || (p.residual && p.ldr < p.out)) return CQ_EINVAL;
-    if (!aligned(p.x, 16) || !aligned(p.qweight, 16) || !aligned(p.bias, 2) || !aligned(p.residual, 2) ||
+    if (!aligned(p.x, 16) || !aligned(p.qweight, 16) || !aligned(p.x_scales, 4) || !aligned(p.scales, 4) || !aligned(p.bias, 2) || !aligned(p.residual, 2) ||
         !aligned(p.y, p.y_type == CQ_F32 ? 4 : 2))
         return CQ_EINVAL;
     const size_t need = cq_mxfp4_linear_workspace_size(p.M, p.out, p.in, p.gated, p.x_format, codes);

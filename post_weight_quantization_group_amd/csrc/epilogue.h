@@ -68,4 +68,96 @@ __device__ __forceinline__ void finish4(const Args& a, int64_t m, int64_t o, f32
     }
 }
 
+// Whether eight neighbouring outputs from a multiple of 8 on can be moved at once.
+template <typename Args>
+__device__ __forceinline__ bool outputs_in_eights(const Args& a) {
+    bool ok = a.out % 8 == 0 && a.ldy % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
+    if (a.residual) ok = ok && a.ldr % 8 == 0 && ((uintptr_t)a.residual & 15) == 0;
+    if (a.bias) ok = ok && ((uintptr_t)a.bias & 15) == 0;
+    return ok;
+}
+
+template <bool F16>
+__device__ __forceinline__ void eight(uint4 v, float* f) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[2 * i] = to_f32<F16>((uint16_t)w[i]), f[2 * i + 1] = to_f32<F16>((uint16_t)(w[i] >> 16));
+}
+
+__device__ __forceinline__ void activate8(int act, float* z) {
+    switch (act) {
+        case ACT_RELU:
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = activate<ACT_RELU>(z[e]);
+            break;
+        case ACT_SILU:
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = activate<ACT_SILU>(z[e]);
+            break;
+        case ACT_GELU:
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = activate<ACT_GELU>(z[e]);
+            break;
+        case ACT_GELU_TANH:
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = activate<ACT_GELU_TANH>(z[e]);
+            break;
+        default: break;
+    }
+}
+
+// finish() of ROWS rows of eight neighbouring outputs each, from column o on, z and (gated) up in LDS; the rows are
+// `row_of(i)`, their sums at `from(i)`, those of the other half UP floats further on.  All residuals are asked for before the
+// first is used: `early` holds them, from ask_residuals().
+template <int ROWS>
+struct Residuals {
+    uint4 v[ROWS];
+    template <typename Args, typename Row>
+    __device__ __forceinline__ void ask(const Args& a, int64_t o, Row row_of) {
+        if (!a.residual) return;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int64_t m = row_of(i);
+            v[i] = *reinterpret_cast<const uint4*>(a.residual + (m < a.M ? m : a.M - 1) * a.ldr + o);
+        }
+    }
+};
+template <bool F16, int UP, int ROWS, typename Args, typename Row, typename From>
+__device__ __forceinline__ void finish8(const Args& a, int64_t o, const float* bias, const float* up_bias,
+                                        const Residuals<ROWS>& residuals, Row row_of, From from) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int64_t m = row_of(i);
+        const __attribute__((address_space(3))) float* at = from(i);
+        float z[8], up[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = at[e] + bias[e];
+        activate8(a.act, z);
+        if (a.gated) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) up[e] = at[UP + e] + up_bias[e];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] *= up[e];
+        }
+        if (a.residual) {
+            float r[8];
+            eight<F16>(residuals.v[i], r);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] += r[e];
+        }
+        if (m >= a.M) continue;
+        if (a.y_f32) {
+            f32x4* to = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.y) + m * a.ldy + o);
+            to[0] = f32x4{z[0], z[1], z[2], z[3]};
+            to[1] = f32x4{z[4], z[5], z[6], z[7]};
+        } else {
+            uint32_t b[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) b[e] = from_f32<F16>(z[e]);
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.y) + m * a.ldy + o) =
+                make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16);
+        }
+    }
+}
+
 }  // namespace cqk

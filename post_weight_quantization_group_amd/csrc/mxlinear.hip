@@ -16,6 +16,8 @@
 // leading one: 2688 and -2688 beside 0.06 leave 0, and sums are off by up to 2^-13 of the sum of magnitudes.  So an e4m3
 // operand goes in twice: its elements of 2 and more (bit 6 of their codes), whose products with e2m1 ones span
 // the 15 bits from 2^11 to 2^-3, and the others, from 2^3 to 2^-10.  Both sums are then exact in a lane, and fp32 beyond.
+#include <type_traits>
+
 #include "epilogue.h"
 #include "mx.h"
 #include "serve_args.h"
@@ -208,41 +210,58 @@ hipError_t few(const MxLinearArgs& a, hipStream_t st) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// Many rows: a workgroup takes BIG_M rows of x's codes and BIG_N rows of W (gated: half of them of the gate, the others of the
-// other half), 128 of k a step; its four waves 64 by 128 each, as 2 x 4 products of 32 x 32.  Codes and scales go from
-// memory straight into LDS, some steps ahead, one barrier a step.  16-byte pieces of a row lie turned in it by the row's
+// Many rows: a workgroup takes BM rows of x's codes and BIG_N rows of W (gated: half of them of the gate, the others of the
+// other half), KB of k a step; its waves 64 by 128 each, as 2 x 4 products of 32 x 32.  Codes and scales go from memory
+// straight into LDS, STAGES - 1 steps ahead, one barrier a step.  16-byte pieces of a row lie turned in it by the row's
 // number, so that the rows which a quarter of a wave reads at once are in different banks.
-constexpr int BIG_M = 128, BIG_N = 256;
+constexpr int BIG_N = 256;
 
-template <int FORM>
-__device__ __forceinline__ f32x16 add_products_32(i32x8 w, int ws, i32x8 x, i32x8 large, int xs, f32x16 acc, bool high) {
+// The turn of a row of BYTES bytes in LDS: 16 rows read at one piece fall into all 64 banks.
+template <int BYTES>
+__device__ __forceinline__ int turn_of(int row) {
+    return BYTES == 64 ? (row >> 2) & 3 : (row >> 1) & 7;
+}
+// acc += W x, 32 by 32 over 64 of k, with the scales' byte 0, or (HIGH) 2.  x of MXFP8: its elements below 2, and `large`.
+template <int FORM, typename X>
+__device__ __forceinline__ f32x16 add_products_32(uint4 w, int ws, X x, X large, int xs, f32x16 acc, bool high) {
+    const i32x8 a = operand(w);
     if constexpr (FORM == MXFP4) {
-        if (high) return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc, 4, 4, 2, ws, 2, xs);
-        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc, 4, 4, 0, ws, 0, xs);
+        const i32x8 b = operand(x);
+        if (high) return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, 4, 4, 2, ws, 2, xs);
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, 4, 4, 0, ws, 0, xs);
     } else if (high) {
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc, 4, 0, 2, ws, 2, xs);
-        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, large, acc, 4, 0, 2, ws, 2, xs);
+        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, x, acc, 4, 0, 2, ws, 2, xs);
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, large, acc, 4, 0, 2, ws, 2, xs);
     } else {
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, acc, 4, 0, 0, ws, 0, xs);
-        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, large, acc, 4, 0, 0, ws, 0, xs);
+        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, x, acc, 4, 0, 0, ws, 0, xs);
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, large, acc, 4, 0, 0, ws, 0, xs);
     }
 }
 
-template <int FORM, bool F16>
-__global__ __launch_bounds__(256, 2) void many_rows_mx(MxLinearArgs a, int row_tiles, int col_tiles) {
-    constexpr int STAGES = FORM == MXFP4 ? 3 : 2;
-    constexpr int X_ROW = FORM == MXFP4 ? 64 : 128;  // bytes of a step's row of x; 64 of W
-    constexpr int X_LOADS = BIG_M * X_ROW / 1024 / 4, LOADS = 4 + X_LOADS + 2;  // a wave's a step
-    constexpr int LINE = BIG_N + 4;                                            // floats of a row in the epilogue
+// WHOLE: the scales of 512 of k of a row are 16 aligned bytes.
+template <int FORM, bool F16, bool WHOLE, int BM, int KB, int STAGES>
+__global__ __launch_bounds__(2 * BM, 2) void many_rows_mx(MxLinearArgs a, int row_tiles, int col_tiles) {
+    constexpr int WAVES = BM / 32, THREADS = 64 * WAVES, KS = KB / 64;
+    constexpr int W_ROW = KB / 2, X_ROW = FORM == MXFP4 ? KB / 2 : KB;  // bytes of a step's row
+    static_assert((W_ROW == 64 || W_ROW == 128) && (X_ROW == 64 || X_ROW == 128), "");
+    constexpr int W_LOADS = BIG_N * W_ROW / 1024 / WAVES, X_LOADS = BM * X_ROW / 1024 / WAVES;  // a wave's a step
+    constexpr int LINE = BIG_N + 4;                                                            // floats of a row in the epilogue
     struct Stage {
-        uint8_t w[BIG_N * 64], x[BIG_M * X_ROW];
-        uint32_t ws[BIG_N], xs[2 * BIG_M];  // (the upper half: the same scales again, so that every wave loads as much)
+        uint8_t w[BIG_N * W_ROW], x[BM * X_ROW];
     };
-    constexpr int BYTES = STAGES * sizeof(Stage) > 64 * LINE * 4 ? STAGES * sizeof(Stage) : 64 * LINE * 4;
-    __shared__ __align__(1024) uint8_t lds[BYTES];
-    Stage* stage = reinterpret_cast<Stage*>(lds);
+    constexpr int PASS = BM / 2;  // rows of the epilogue at a time
+    constexpr int BYTES = STAGES * sizeof(Stage) > PASS * LINE * 4 ? STAGES * sizeof(Stage) : PASS * LINE * 4;
+    // Scales, four dwords (512 of k) of a row at a time, those of x behind those of W.  MXFP8: two sets, read step by step;
+    // MXFP4: one, taken into registers.
+    constexpr int ROWS = BIG_N + BM, SET = 4 * ROWS, SETS = FORM == MXFP4 ? 1 : 2, CHUNK = 512 / KB;  // (steps)
+    __shared__ struct {
+        __align__(1024) uint32_t scales[SETS * SET];  // (in front: their offsets are constants of the reads)
+        __align__(1024) uint8_t stages[BYTES];
+    } lds;
+    uint32_t* scales_of = lds.scales;
+    Stage* stage = reinterpret_cast<Stage*>(lds.stages);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r = lane & 31, half = lane >> 5, wr = wave & 1, wc = wave >> 1;
+    const int r = lane & 31, half = lane >> 5, wr = wave % (BM / 64), wc = wave / (BM / 64);
     // Workgroups go to the eight XCDs in turn: each XCD takes a run of tiles, in bands of 8 row tiles, so that the tiles
     // it works on at a time share rows of x and W in its L2.
     int64_t id = blockIdx.x;
@@ -254,7 +273,7 @@ __global__ __launch_bounds__(256, 2) void many_rows_mx(MxLinearArgs a, int row_t
     const int64_t high = row_tiles - band * 8 < 8 ? row_tiles - band * 8 : 8;
     const int64_t rt = band * 8 + in_band % high, ct = in_band / high;
     const int per = a.gated ? BIG_N / 2 : BIG_N;  // outputs per workgroup
-    const int64_t m0 = rt * BIG_M, n0 = ct * per;
+    const int64_t m0 = rt * BM, n0 = ct * per;
     // row of W for row i of the tile; past the edge the last one
     auto w_row = [&](int i) {
         const bool up = a.gated && i >= BIG_N / 2;
@@ -262,34 +281,72 @@ __global__ __launch_bounds__(256, 2) void many_rows_mx(MxLinearArgs a, int row_t
         return (o < a.out ? o : a.out - 1) + (up ? a.out : 0);
     };
     auto x_row = [&](int i) { return m0 + i < a.M ? m0 + i : a.M - 1; };
-    const int steps = (int)(a.in / 128);
-    const uint8_t *wp[4], *xp[X_LOADS], *wsp, *xsp;
+    const int steps = (int)(a.in / KB), dwords = (int)(a.in / 128);
+    // a lane's pieces of the tile, as offsets from its first row (a wave's rows of W are all in one half)
+    const int w_first = BIG_N / WAVES * wave, x_first = BM / WAVES * wave;
+    const uint8_t* w_base = a.w + (n0 + (a.gated && w_first >= BIG_N / 2 ? a.out : 0)) * (a.in / 2);
+    const uint8_t* x_base = static_cast<const uint8_t*>(a.x) + m0 * a.ldx;
+    uint32_t w_at[W_LOADS], x_at[X_LOADS];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = 64 * wave + 16 * i + lane / 4;
-        wp[i] = a.w + w_row(row) * (a.in / 2) + 16 * ((lane & 3) ^ ((row >> 2) & 3));
+    for (int i = 0; i < W_LOADS; ++i) {
+        const int row = w_first + 1024 / W_ROW * i + lane / (W_ROW / 16), o = a.gated ? row % (BIG_N / 2) : row;
+        w_at[i] = (uint32_t)(n0 + o < a.out ? o : a.out - 1 - n0) * (uint32_t)(a.in / 2) + 16 * (lane % (W_ROW / 16) ^ turn_of<W_ROW>(row));
     }
 #pragma unroll
     for (int i = 0; i < X_LOADS; ++i) {
-        if constexpr (FORM == MXFP4) {
-            const int row = 32 * wave + 16 * i + lane / 4;
-            xp[i] = static_cast<const uint8_t*>(a.x) + x_row(row) * a.ldx + 16 * ((lane & 3) ^ ((row >> 2) & 3));
-        } else {
-            const int row = 32 * wave + 8 * i + lane / 8;
-            xp[i] = static_cast<const uint8_t*>(a.x) + x_row(row) * a.ldx + 16 * ((lane & 7) ^ ((row >> 1) & 7));
-        }
+        const int row = x_first + 1024 / X_ROW * i + lane / (X_ROW / 16);
+        x_at[i] = (uint32_t)(x_row(row) - m0) * (uint32_t)a.ldx + 16 * (lane % (X_ROW / 16) ^ turn_of<X_ROW>(row));
     }
-    wsp = a.ws + w_row(64 * wave + lane) * (a.in / MX_BLOCK);
-    xsp = a.xs + x_row(64 * (wave & 1) + lane) * a.ldxs;
-    auto ask = [&](int s) {
-        Stage& t = stage[s % STAGES];
+    // Scales go 16 bytes a row where they lie so, else as a dword of every 128 of k, [128 of k][row].
+    constexpr int GROUPS = ROWS / 64, SHARES = (GROUPS + WAVES - 1) / WAVES;
+    const uint8_t* sp[SHARES];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load_to_lds(wp[i] + (int64_t)s * 64, &t.w[(64 * wave + 16 * i) * 64]);
+    for (int i = 0; i < SHARES; ++i) {
+        const int row = 64 * (wave + WAVES * i) + lane;
+        sp[i] = row < BIG_N ? a.ws + w_row(row) * (a.in / MX_BLOCK) : a.xs + x_row(row - BIG_N) * a.ldxs;
+    }
+    auto ask_scales = [&](int chunk) {  // past the last one: that one again, where nothing reads it
+        const int q = 4 * chunk < dwords ? 4 * chunk : (dwords - 1) & ~3;
+        uint32_t* to = scales_of + (SETS == 2 ? chunk % 2 * SET : 0);
 #pragma unroll
-        for (int i = 0; i < X_LOADS; ++i)
-            load_to_lds(xp[i] + (int64_t)s * X_ROW, &t.x[(32 * wave + (FORM == MXFP4 ? 16 : 8) * i) * X_ROW]);
-        load_to_lds_4(wsp + 4 * s, &t.ws[64 * wave]);
-        load_to_lds_4(xsp + 4 * s, &t.xs[64 * wave]);
+        for (int i = 0; i < SHARES; ++i) {
+            const int group = wave + WAVES * i;
+            if (GROUPS % WAVES && group >= GROUPS) break;
+            if constexpr (WHOLE) {
+                load_to_lds(sp[i] + 4 * q, to + 256 * group);
+            } else {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) load_to_lds_4(sp[i] + 4 * (q + x < dwords ? q + x : dwords - 1), to + x * ROWS + 64 * group);
+            }
+        }
+    };
+    constexpr int SCALE_LOADS = WHOLE ? 1 : 4;  // a wave's, at least
+    // Scales of the lane's rows: of a whole chunk (MXFP4), of step s (MXFP8); `held` are those of the step in hand, the
+    // lane's own blocks at the bottom.
+    uint32_t scales[6][SETS == 1 ? 4 : 1], held[6];
+    auto take_scales = [&](int s) {
+        const uint32_t* from = scales_of + (SETS == 2 ? s / CHUNK % 2 * SET : 0);
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+            const int row = i < 4 ? 128 * wc + 32 * i + r : BIG_N + 64 * wr + 32 * (i - 4) + r;
+            if constexpr (SETS == 2) {
+                scales[i][0] = WHOLE ? from[4 * row + s % 4] : from[s % 4 * ROWS + row];
+            } else if constexpr (WHOLE) {
+                const uint4 v = *reinterpret_cast<const uint4*>(from + 4 * row);
+                scales[i][0] = v.x, scales[i][1] = v.y, scales[i][2] = v.z, scales[i][3] = v.w;
+            } else {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) scales[i][x] = from[x * ROWS + row];
+            }
+        }
+    };
+    constexpr int LOADS = W_LOADS + X_LOADS;
+    // load i of step k (past the last one: that one again, where nothing reads it) into place b
+    auto ask_one = [&](int k, int b, int i) {
+        Stage& t = stage[b];
+        const int64_t at = k < steps ? k : steps - 1;
+        if (i < W_LOADS) load_to_lds(w_base + at * W_ROW, w_at[i], &t.w[W_ROW * w_first + 1024 * i]);
+        else load_to_lds(x_base + at * X_ROW, x_at[i - W_LOADS], &t.x[X_ROW * x_first + 1024 * (i - W_LOADS)]);
     };
     f32x16 acc[4][2];
 #pragma unroll
@@ -298,65 +355,156 @@ __global__ __launch_bounds__(256, 2) void many_rows_mx(MxLinearArgs a, int row_t
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-    for (int s = 0; s < STAGES - 1 && s < steps; ++s) ask(s);
-    for (int s = 0; s < steps; ++s) {
-        if (s + STAGES - 2 < steps) loaded_to_lds<(STAGES - 2) * LOADS>();
-        else loaded_to_lds<0>();
-        __syncthreads();  // this step's codes are in LDS, and the previous step's have been read
-        if (s + STAGES - 1 < steps) ask(s + STAGES - 1);
-        const Stage& t = stage[s % STAGES];
-        int ws[4], xs[2];
+    // Operands of the 64 of k in hand.  A register is read again, for the next 64, as soon as its last product is issued.
+    // MXFP4: the products go by W's rows, and x, of which all is needed to the end, is read into `next`.  MXFP8: they go by
+    // x's rows, which take twice the registers and are split; the second is read beside the first one's products.
+    constexpr bool BY_X = FORM == MXFP8;
+    uint4 w[4];
+    typedef typename std::conditional<FORM == MXFP4, uint4, i32x8>::type X;
+    X x[2], large[2], next[BY_X ? 1 : 2];
+    auto read_w = [&](int i, int b, int ks) {
+        w[i] = *reinterpret_cast<const uint4*>(
+            &stage[b].w[(128 * wc + 32 * i + r) * W_ROW + 16 * ((2 * ks + half) ^ turn_of<W_ROW>(r))]);
+    };
+    auto read_x = [&](X& to, int j, int b, int ks) {
+        const uint8_t* row = &stage[b].x[(64 * wr + 32 * j + r) * X_ROW];
+        if constexpr (FORM == MXFP4)
+            to = *reinterpret_cast<const uint4*>(row + 16 * ((2 * ks + half) ^ turn_of<X_ROW>(r)));
+        else
+            to = operand(*reinterpret_cast<const uint4*>(row + 16 * ((4 * ks + half) ^ turn_of<X_ROW>(r))),
+                         *reinterpret_cast<const uint4*>(row + 16 * ((4 * ks + 2 + half) ^ turn_of<X_ROW>(r))));
+    };
+    ask_scales(0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ws[i] = (int)(t.ws[128 * wc + 32 * i + r] >> (8 * half));
+    for (int s = 0; s < STAGES; ++s)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) xs[j] = (int)(t.xs[64 * wr + 32 * j + r] >> (8 * half));
+        for (int i = 0; i < LOADS; ++i) ask_one(s, s, i);
+    loaded_and_read<(STAGES - 1) * LOADS>();
+    take_scales(0);
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            i32x8 w[4], x[2], large[2];
+    for (int j = 0; j < (BY_X ? 1 : 2); ++j) read_x(BY_X ? x[0] : next[j], j, 0, 0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = operand(*reinterpret_cast<const uint4*>(&t.w[(128 * wc + 32 * i + r) * 64 + 16 * ((2 * ks + half) ^ ((r >> 2) & 3))]));
+    for (int i = 0; i < 4; ++i) read_w(i, 0, 0);
+    // Step by step.  The barrier stands in the last 64 of k of a step, whose operands are in registers: behind it the next
+    // step's codes are read, and this step's place in LDS is asked for again, one load in a slot (all in a row they hold
+    // the wave up), those left over in front of the next barrier.
+    constexpr int APART = 8 * KS / LOADS;
+    constexpr int UNROLL = SETS == 1 ? CHUNK : 1;  // (a chunk's scales are in registers, by number)
+    int here = 0, before = STAGES - 1;             // places of this step and of the one before
+    for (int s0 = 0; s0 < steps; s0 += UNROLL) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint8_t* row = &t.x[(64 * wr + 32 * j + r) * X_ROW];
-                if constexpr (FORM == MXFP4) {
-                    x[j] = operand(*reinterpret_cast<const uint4*>(row + 16 * ((2 * ks + half) ^ ((r >> 2) & 3))));
-                    large[j] = x[j];
-                } else {
-                    x[j] = operand(*reinterpret_cast<const uint4*>(row + 16 * ((4 * ks + half) ^ ((r >> 1) & 7))),
-                                   *reinterpret_cast<const uint4*>(row + 16 * ((4 * ks + 2 + half) ^ ((r >> 1) & 7))));
-                    large[j] = large_elements(x[j]);
-                    x[j] ^= large[j];
+        for (int u = 0; u < UNROLL; ++u) {
+            const int s = s0 + u, c = SETS == 1 ? u : s % CHUNK;
+            if (u > 0 && s >= steps) break;
+            const int after = here + 1 < STAGES ? here + 1 : 0;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                if (SETS == 2 ? ks == 0 : ks % 2 == 0)
+#pragma unroll
+                    for (int i = 0; i < 6; ++i) held[i] = scales[i][SETS == 1 ? u * (KB / 128) + ks / 2 : 0] >> (8 * half);
+                if constexpr (!BY_X)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) x[j] = large[j] = next[j];
+                const bool last = ks == KS - 1;
+#pragma unroll
+                for (int slot = 0; slot < 8; ++slot) {
+                    const int i = BY_X ? slot % 4 : slot / 2, j = BY_X ? slot / 4 : slot % 2;
+                    if constexpr (BY_X)
+                        if (i == 0) {
+                            large[j] = large_elements(x[j]);
+                            x[j] ^= large[j];
+                        }
+                    acc[i][j] = add_products_32<FORM>(w[i], (int)held[i], x[j], large[j], (int)held[4 + j], acc[i][j], ks % 2);
+                    if (last && slot == 1) {
+                        // the next step's codes are needed, those behind them and scales asked for since may be on their way
+                        if (STAGES == 3 && c == 1) loaded_and_read<(STAGES - 2) * LOADS + SCALE_LOADS>();
+                        else loaded_and_read<(STAGES - 2) * LOADS>();
+                        if (c == 0) ask_scales(s / CHUNK + 1);
+                        if (SETS == 2 || c == CHUNK - 1) take_scales(s + 1);
+                    }
+                    const int from = last ? after : here, from_ks = last ? 0 : ks + 1;
+                    if constexpr (BY_X) {
+                        if (slot == 0) read_x(x[1], 1, here, ks);
+                        if (slot == 3) read_x(x[0], 0, from, from_ks);
+                    } else if (slot == 1 || slot == 2) {
+                        read_x(next[slot - 1], slot - 1, from, from_ks);
+                    }
+                    if (j == 1) read_w(i, from, from_ks);
+                    // slots since the barrier, this step's or the one before's (in the first step: loads done already)
+                    const bool since = last && slot >= 2;
+                    const int at = since ? slot - 2 : 6 + 8 * ks + slot;
+                    if (at % APART == 0 && at / APART < LOADS) ask_one(since ? s + STAGES : s + STAGES - 1, since ? here : before, at / APART);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[i][j] = add_products_32<FORM>(w[i], ws[i], x[j], large[j], xs[j], acc[i][j], ks);
+            before = here;
+            here = after;
         }
     }
-    // The epilogue, 32 rows of every wave at a time through LDS: a thread then has four neighbouring outputs of a row, and
-    // residual and y move in whole lines.
-    const bool wide = outputs_in_fours(a);
-    float* tile = reinterpret_cast<float*>(lds);  // [64][LINE]
-#pragma unroll
+    loaded_to_lds();  // what was asked for past the end
+    // The epilogue, 32 rows of every wave at a time through LDS: a thread then has eight neighbouring outputs of a row at a
+    // time, at the same columns, and residual and y move in whole lines.
+    float* tile = reinterpret_cast<float*>(lds.stages);  // [PASS][LINE]
+    const bool wide = outputs_in_eights(a);
+    const int n = 8 * (tid % (per / 8));
+    const bool there = n0 + n < a.out;
+    const int64_t o = there ? n0 + n : a.out - 8;
+    float bias[8] = {}, up_bias[8] = {};
+    if (wide && a.bias) {
+        eight<F16>(*reinterpret_cast<const uint4*>(a.bias + o), bias);
+        if (a.gated) eight<F16>(*reinterpret_cast<const uint4*>(a.bias + a.out + o), up_bias);
+    }
+    // a thread's rows, four at a time, every `apart`-th
+    const int apart = THREADS / (per / 8);
+    Residuals<4> now, next_rows;
+#pragma unroll 1
     for (int j = 0; j < 2; ++j) {
+        auto row_at = [&](int row) { return m0 + 64 * (row >> 5) + 32 * j + (row & 31); };
+        auto row_of = [&](int i) { return row_at(apart * i + tid / (per / 8)); };
+        if (wide) now.ask(a, o, row_of);
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int jj = 0; jj < 2; ++jj)
+            if (j == jj)
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<f32x4*>(&tile[(32 * wr + r) * LINE + 128 * wc + 32 * i + 2 * e + 4 * half]) =
-                    f32x4{acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]};
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        *reinterpret_cast<f32x4*>(&tile[(32 * wr + r) * LINE + 128 * wc + 32 * i + 2 * e + 4 * half]) =
+                            f32x4{acc[i][jj][e], acc[i][jj][e + 1], acc[i][jj][e + 2], acc[i][jj][e + 3]};
         __syncthreads();
-        const int n = 4 * (tid % (per / 4)), lines = 1024 / per;
-        for (int row = tid / (per / 4); row < 64; row += lines) {
-            const f32x4 z = *reinterpret_cast<const f32x4*>(&tile[row * LINE + n]);
-            f32x4 up = {0, 0, 0, 0};
-            if (a.gated) up = *reinterpret_cast<const f32x4*>(&tile[row * LINE + BIG_N / 2 + n]);
-            finish4<F16>(a, m0 + 64 * (row >> 5) + 32 * j + (row & 31), n0 + n, z, up, wide);
+        if (!wide) {
+            for (int at = tid; at < PASS * per; at += THREADS) {
+                const int row = at / per, c = at % per;
+                if (row_at(row) < a.M && n0 + c < a.out)
+                    finish<F16>(a, row_at(row), n0 + c, tile[row * LINE + c], a.gated ? tile[row * LINE + BIG_N / 2 + c] : 0.0f);
+            }
+            continue;
+        }
+#pragma unroll 1
+        for (int i0 = 0; i0 < PASS / apart; i0 += 4) {
+            if (i0 + 4 < PASS / apart) next_rows.ask(a, o, [&](int i) { return row_of(i0 + 4 + i); });
+            if (there)
+                finish8<F16, BIG_N / 2, 4>(
+                    a, o, bias, up_bias, now, [&](int i) { return row_of(i0 + i); },
+                    [&](int i) {
+                        return (const __attribute__((address_space(3))) float*)&tile[(apart * (i0 + i) + tid / (per / 8)) * LINE + n];
+                    });
+            now = next_rows;
         }
     }
+}
+
+template <int FORM, bool F16, int BM, int KB, int STAGES>
+hipError_t many(const MxLinearArgs& a, hipStream_t st) {
+    const int per = a.gated ? BIG_N / 2 : BIG_N;
+    const int64_t rt = (a.M + BM - 1) / BM, ct = (a.out + per - 1) / per;
+    const dim3 grid((unsigned)(rt * ct));
+    if (a.in % 512 == 0 && a.ldxs % 16 == 0 && ((uintptr_t)a.ws | (uintptr_t)a.xs) % 16 == 0)
+        hipLaunchKernelGGL((many_rows_mx<FORM, F16, true, BM, KB, STAGES>), grid, dim3(2 * BM), 0, st, a, (int)rt, (int)ct);
+    else
+        hipLaunchKernelGGL((many_rows_mx<FORM, F16, false, BM, KB, STAGES>), grid, dim3(2 * BM), 0, st, a, (int)rt, (int)ct);
+    return hipGetLastError();
 }
 
 // Rows of x up to which its 16-bit values are quantized by the lanes that multiply them; above, once for all columns.
@@ -370,10 +518,11 @@ hipError_t launch_few(const MxLinearArgs& a, hipStream_t st) {
 
 template <int FORM, bool F16>
 hipError_t launch_type(const MxLinearArgs& a, hipStream_t st) {
-    const int64_t rt = (a.M + BIG_M - 1) / BIG_M, ct = (a.out + (a.gated ? BIG_N / 2 : BIG_N) - 1) / (a.gated ? BIG_N / 2 : BIG_N);
-    if (a.xs && rt * ct >= 64) {
-        hipLaunchKernelGGL((many_rows_mx<FORM, F16>), dim3((unsigned)(rt * ct)), dim3(256), 0, st, a, (int)rt, (int)ct);
-        return hipGetLastError();
+    const int per = a.gated ? BIG_N / 2 : BIG_N;
+    const int64_t tiles = (a.M + 127) / 128 * ((a.out + per - 1) / per);
+    if (a.xs && tiles >= 64) {
+        if (FORM == MXFP8) return many<MXFP8, F16, 128, 128, 2>(a, st);
+        return many<MXFP4, F16, 128, 128, 3>(a, st);
     }
     if (a.xs) return launch_few<FORM, X_CODES, F16>(a, st);
     return launch_few<FORM, F16 ? X_F16 : X_BF16, F16>(a, st);

@@ -72,6 +72,11 @@ __device__ __forceinline__ void load_to_lds(const void* from, const void* lds) {
     const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "memory", "m0");
 }
+// The same from `base` (the same in all lanes) and a lane's own offset in bytes, below 2^32.
+__device__ __forceinline__ void load_to_lds(const void* base, uint32_t offset, const void* lds) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(offset), "s"(base) : "memory", "m0");
+}
 // The same with 4 bytes per lane.
 __device__ __forceinline__ void load_to_lds_4(const void* from, const void* lds) {
     const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds);
@@ -81,6 +86,12 @@ __device__ __forceinline__ void load_to_lds_4(const void* from, const void* lds)
 template <int LATER = 0>
 __device__ __forceinline__ void loaded_to_lds() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER) : "memory");
+}
+// The same, and until the wave's reads of LDS are done; then a barrier of the workgroup's waves.  Reads of LDS in front of it
+// see nothing of what is asked for behind it, those behind it all that the waves have waited for.
+template <int LATER>
+__device__ __forceinline__ void loaded_and_read() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LATER) : "memory");
 }
 
 }  // namespace cqk

@@ -109,11 +109,13 @@ def _linear(ws=None, ws_bytes=0, **kw):
 @pytest.mark.parametrize("kw", [
     dict(type=2), dict(type=-1), dict(y_type=cq.F16), dict(y_type=3), dict(activation=-1), dict(activation=5),
     dict(gated=2), dict(x_format=2), dict(x_format=5), dict(M=-1), dict(out=-1), dict(inp=0), dict(inp=160),
-    dict(inp=-128), dict(M=1 << 31), dict(out=(1 << 25) + 1), dict(out=(1 << 24) + 1, gated=1), dict(inp=1 << 25),
+    dict(inp=-128), dict(inp=(1 << 22) + 128, ldx=1 << 23), dict(x_scales=FAKE, ldxs=8, ldx=(1 << 23) + 16), dict(M=1 << 31),
+    dict(out=(1 << 25) + 1), dict(out=(1 << 24) + 1, gated=1), dict(inp=1 << 25),
     dict(M=1 << 20, out=1 << 18), dict(M=1 << 20, inp=1 << 15, ldx=1 << 15), dict(x=None), dict(qweight=None), dict(scales=None), dict(y=None), dict(ldx=128),
     dict(ldx=260), dict(ldy=7), dict(residual=FAKE, ldr=7), dict(x=FAKE + 8), dict(qweight=FAKE + 8),
     dict(bias=FAKE + 1), dict(residual=FAKE + 1, ldr=8), dict(y=FAKE + 1), dict(y=FAKE + 2, y_type=cq.F32),
-    dict(x_scales=FAKE, ldxs=7), dict(x_scales=FAKE, ldxs=8, ldx=255), dict(x_scales=FAKE, ldxs=8, ldx=264),
+    dict(x_scales=FAKE, ldxs=7), dict(x_scales=FAKE, ldxs=10), dict(x_scales=FAKE + 2, ldxs=8), dict(scales=FAKE + 1),
+    dict(x_scales=FAKE, ldxs=8, ldx=255), dict(x_scales=FAKE, ldxs=8, ldx=264),
     dict(x_scales=FAKE, ldxs=8, ldx=112, x_format=cq.MXFP4),
 ])
 def test_linear_rejects_before_launch(kw):
