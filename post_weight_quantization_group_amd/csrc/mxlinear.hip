@@ -474,11 +474,11 @@ __global__ __launch_bounds__(2 * BM, 2) void many_rows_mx(MxLinearArgs a, int ro
                             f32x4{acc[i][jj][e], acc[i][jj][e + 1], acc[i][jj][e + 2], acc[i][jj][e + 3]};
         __syncthreads();
         if (!wide) {
-            for (int at = tid; at < PASS * per; at += THREADS) {
-                const int row = at / per, c = at % per;
-                if (row_at(row) < a.M && n0 + c < a.out)
+            const int c = tid & (per - 1);
+            if (n0 + c < a.out)
+#pragma unroll 1
+                for (int row = tid / per; row < PASS && row_at(row) < a.M; row += THREADS / per)
                     finish<F16>(a, row_at(row), n0 + c, tile[row * LINE + c], a.gated ? tile[row * LINE + BIG_N / 2 + c] : 0.0f);
-            }
             continue;
         }
 #pragma unroll 1
@@ -507,25 +507,53 @@ hipError_t many(const MxLinearArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Rows of x up to which its 16-bit values are quantized by the lanes that multiply them; above, once for all columns.
-constexpr int64_t WITHIN = 32;
+int64_t up(int64_t n, int64_t of) { return (n + of - 1) / of; }
 
+// Whether x's 16-bit values are quantized by the lanes that multiply them (again for every tile of columns), or once,
+// before.  us, within | before (some 3 of them the other launch): 32 rows, 4096 -> 16,384 18.7 | 18; 64 rows, 4096 -> 4096
+// 13.7 | 13, 4096 -> 16,384 33 | 25, 1024 -> 2 x 3584 7.9 | 9.6; 16 rows never less within.
+bool within(int64_t M, int64_t cols) { return M <= 32 || (M <= 64 && up(M, 16) * up(cols, 64) <= 256); }
+
+// The smallest tile of rows and columns, and with it the most waves to a sum, with which the workgroups fit on the chip's 256
+// CUs at once: they take the time of their own chain of loads, and another round of them takes it again.  us, by rows and
+// columns of a tile in 16s:
+//                                     1x2     2x2     1x4     2x4     4x4
+//   1 row, 4096 -> 4096               6.8            10.3                    (16-bit x, MXFP4)
+//   16 rows, 1024 -> 2 x 3584         4.7             5.7
+//   64 rows, 4096 -> 4096            17.1    14.0    13.7    18.1
+//   203 rows, 4096 -> 809            13.1    10.0    11.9    14.6    21.5    (codes)
+//   128 rows, 4096 -> 4096           23.7    17.2    20.6    14.8    21.6
+//   1024 rows, 3584 -> 1024                                  19.6    17.6
+// 8 waves a tile; 16 in its place are as fast or slower up to 0.5 us.
 template <int FORM, int XT, bool F16>
 hipError_t launch_few(const MxLinearArgs& a, hipStream_t st) {
-    if (a.M <= 16) return few<FORM, XT, F16, 1, 2, 16>(a, st);
-    return few<FORM, XT, F16, 2, 4, 8>(a, st);
+    const int64_t cols = a.gated ? 2 * a.out : a.out;
+    if (up(a.M, 16) * up(cols, 32) <= 256) return few<FORM, XT, F16, 1, 2, 8>(a, st);
+    if (up(a.M, 32) * up(cols, 32) <= 256 && a.M > 16) return few<FORM, XT, F16, 2, 2, 8>(a, st);
+    if (up(a.M, 16) * up(cols, 64) <= 256 || a.M <= 16) return few<FORM, XT, F16, 1, 4, 8>(a, st);
+    if (XT != X_CODES || up(a.M, 32) * up(cols, 64) <= 256) return few<FORM, XT, F16, 2, 4, 8>(a, st);
+    if constexpr (XT == X_CODES) return few<FORM, XT, F16, 4, 4, 4>(a, st);
+    return hipErrorInvalidValue;
 }
 
 template <int FORM, bool F16>
 hipError_t launch_type(const MxLinearArgs& a, hipStream_t st) {
-    const int per = a.gated ? BIG_N / 2 : BIG_N;
-    const int64_t tiles = (a.M + 127) / 128 * ((a.out + per - 1) / per);
-    if (a.xs && tiles >= 64) {
-        if (FORM == MXFP8) return many<MXFP8, F16, 128, 128, 2>(a, st);
+    if (!a.xs) return launch_few<FORM, F16 ? X_F16 : X_BF16, F16>(a, st);
+    const int64_t cols = a.gated ? 2 * a.out : a.out;
+    // Where tiles of 64 by 64 no longer fit on the chip at once, the other kernel reads operands once for more products; with
+    // MXFP8, which takes its steps four times as long, from two rounds and a half of them on.  us, few | many: MXFP4 64 rows,
+    // 4096 -> 16,384 22.3 | 22.1, 512 rows, 4096 -> 4096 36 | 22; MXFP8 512 rows 44 | 55, 1024 rows 78 | 63, 203 rows,
+    // 4096 -> 16,384 70 | 63, 512 rows, 1024 -> 2 x 3584 31 | 21.
+    if (up(a.M, 64) * up(cols, 64) <= (FORM == MXFP4 ? 256 : 640)) return launch_few<FORM, X_CODES, F16>(a, st);
+    if constexpr (FORM == MXFP4) {
+        // 256 rows a workgroup and 256 of k a step, one workgroup a CU, where that leaves few CUs idle; us, 128 rows | 256:
+        // 2048 x 4096 x 4096 30.5 | 34.7, 2048 x 2 x 3584 x 1024 22.1 | 20.6, 4096 x 4096 x 4096 52 | 43, 4096 x 16,384 x
+        // 4096 189 | 159.
+        if (a.in % 256 == 0 && up(a.M, 256) * up(cols, 256) >= 192) return many<MXFP4, F16, 256, 256, 2>(a, st);
         return many<MXFP4, F16, 128, 128, 3>(a, st);
+    } else {
+        return many<MXFP8, F16, 128, 128, 2>(a, st);
     }
-    if (a.xs) return launch_few<FORM, X_CODES, F16>(a, st);
-    return launch_few<FORM, F16 ? X_F16 : X_BF16, F16>(a, st);
 }
 
 // Codes of the rows in the workspace, then their scales.
@@ -534,12 +562,12 @@ int64_t code_row(int64_t in, int form) { return form == MXFP4 ? in / 2 : in; }
 }  // namespace
 
 int64_t mx_linear_ws(int64_t M, int64_t out, int64_t in, int gated, int form, bool codes) {
-    return codes || M <= WITHIN ? 0 : M * (code_row(in, form) + in / MX_BLOCK);
+    return codes || within(M, gated ? 2 * out : out) ? 0 : M * (code_row(in, form) + in / MX_BLOCK);
 }
 
 hipError_t launch_mx_linear(const MxLinearArgs& args, hipStream_t st) {
     MxLinearArgs a = args;
-    if (!a.xs && a.M > WITHIN) {
+    if (!a.xs && !within(a.M, a.gated ? 2 * a.out : a.out)) {
         MxRowsArgs q{};
         q.values = const_cast<void*>(a.x);
         q.rows = a.M; q.len = a.in; q.ldx = a.ldx; q.ldc = code_row(a.in, a.form); q.lds = a.in / MX_BLOCK;

@@ -81,6 +81,27 @@ def test_many_tiles(M, out, inp, kw):
     _check(M, out, inp, **kw)
 
 
+@pytest.mark.parametrize("M,out,inp,kw", [
+    (4100, 3100, 512, dict(form="mxfp4", bias=True, res=True)), (4100, 3104, 768, dict(form="mxfp4", y="f32")),
+    (4097, 1553, 256, dict(form="mxfp4", gated=True, act="silu", bias=True, ready=True)),
+    (4200, 3073, 1280, dict(x="f16", form="mxfp4", act="gelu", res=True)),
+    (4100, 3104, 640, dict(form="mxfp4", bias=True)), (1100, 3100, 640, dict(form="mxfp8", res=True)),
+    (1300, 2304, 1536, dict(form="mxfp8", bias=True, act="relu", ready=True)),
+    (1025, 1160, 384, dict(x="f16", form="mxfp8", gated=True, act="gelu_tanh", res=True))])
+def test_larger_tiles(M, out, inp, kw):
+    """Tiles of 256 rows, rows of scales of whole and of odd lengths, steps of 256 and of 128, ends inside a tile."""
+    _check(M, out, inp, **kw)
+
+
+@pytest.mark.parametrize("M,out,inp", [(16, 4096, 256), (16, 4100, 256), (17, 4096, 256), (32, 8192, 128), (48, 5500, 128),
+                                       (64, 4096, 128), (64, 4200, 128), (100, 4096, 128), (128, 8192, 128),
+                                       (130, 8192, 128), (640, 4000, 128), (660, 4100, 128)])
+@pytest.mark.parametrize("form", ["mxfp4", "mxfp8"])
+def test_either_side_of_the_borders_between_the_tiles(M, out, inp, form):
+    _check(M, out, inp, x="f16" if M % 2 else "bf16", form=form, bias=True, y="f32")
+    _check(M, out // 2, inp, form=form, gated=True, act="silu", ready=True)
+
+
 @pytest.mark.parametrize("M", [1, 16, 17, 32, 33, 64, 65])
 @pytest.mark.parametrize("out,gated", [(14208, False), (7110, True), (24580, False), (12289, True)])
 def test_few_rows_and_many_columns(M, out, gated):
