@@ -635,7 +635,7 @@ def proxy_worst_env_wmse_multi(w, d_eval, scales, module_offsets, d_period=None,
 def _empty(shape, dtype, like, stream):
     """An output (or workspace) in the memory pool of the stream that the kernels run on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=like.device)
     with torch.cuda.stream(stream):
@@ -653,6 +653,13 @@ def _on(device: int, *named):
         else:
             ptrs.append(t.data_ptr())
     return ptrs
+
+
+def _same_gpu(device: int, **arrays):
+    """_on for the helpers on a hot path that take the pointers themselves."""
+    for name, t in arrays.items():
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}; all arrays must live on one GPU")
 
 
 def _gpu(t) -> int:
@@ -882,21 +889,22 @@ def mx_quantize(x, format="mxfp4", stream=None):
     four bits; "mxfp8": e4m3, [..., n] (view it as torch.float8_e4m3fn).  scales [..., n/32] hold powers of two with a
     bias of 127: 2^(floor(log2 of the block's largest magnitude) - 2) (mxfp8: - 8); 255 (NaN) for a block with an
     infinity or a NaN.  Elements are rounded to nearest even and saturate at 6 (448)."""
-    form = _mx_format(format)
-    if x.dim() < 1 or x.dtype not in _TYPES or x.shape[-1] % MX_BLOCK or not x.shape[-1]:
+    form, kind, shape = _mx_format(format), _TYPES.get(x.dtype), x.shape
+    n = shape[-1] if len(shape) else 0
+    if kind is None or n % MX_BLOCK or not n:
         raise ValueError("x must be bfloat16, float16 or float32 [..., n], n a multiple of 32")
-    n = x.shape[-1]
     rows, ldx = _mx_rows(x, "x")
     device = _gpu(x)
     if device != _device_now():
         with torch.cuda.device(device):
             return mx_quantize(x, format, stream)
     width = n // 2 if form == MXFP4 else n
-    codes = _empty(x.shape[:-1] + (width,), torch.uint8, x, stream)
-    scales = _empty(x.shape[:-1] + (n // MX_BLOCK,), torch.uint8, x, stream)
-    _check((_lib or load()).cq_mx_quantize(x.data_ptr(), ldx, _TYPES[x.dtype], rows, n, form, codes.data_ptr(), width,
-                                           scales.data_ptr(), n // MX_BLOCK, _stream_on(stream, device)),
-           "cq_mx_quantize")
+    codes = _empty((*shape[:-1], width), torch.uint8, x, stream)
+    scales = _empty((*shape[:-1], n // MX_BLOCK), torch.uint8, x, stream)
+    status = (_lib or load()).cq_mx_quantize(x.data_ptr(), ldx, kind, rows, n, form, codes.data_ptr(), width,
+                                             scales.data_ptr(), n // MX_BLOCK, _stream_on(stream, device))
+    if status:
+        raise CQError(status, "cq_mx_quantize")
     return codes, scales
 
 
@@ -924,10 +932,12 @@ def mx_dequantize(codes, scales, format="mxfp4", out_dtype=torch.bfloat16, strea
     if device != _device_now():
         with torch.cuda.device(device):
             return mx_dequantize(codes, scales, format, out_dtype, stream)
-    y = _empty(codes.shape[:-1] + (n,), out_dtype, codes, stream)
-    pc, ps = _on(device, ("codes", codes), ("scales", scales))
-    _check((_lib or load()).cq_mx_dequantize(pc, ldc, ps, lds, form, rows, n, y.data_ptr(), n, _TYPES[out_dtype],
-                                             _stream_on(stream, device)), "cq_mx_dequantize")
+    y = _empty((*codes.shape[:-1], n), out_dtype, codes, stream)
+    _same_gpu(device, scales=scales)
+    status = (_lib or load()).cq_mx_dequantize(codes.data_ptr(), ldc, scales.data_ptr(), lds, form, rows, n,
+                                               y.data_ptr(), n, _TYPES[out_dtype], _stream_on(stream, device))
+    if status:
+        raise CQError(status, "cq_mx_dequantize")
     return y
 
 
@@ -977,9 +987,8 @@ def mxfp4_linear(x, qweight, scales, x_scales=None, x_format="mxfp8", bias=None,
     act = _ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
-    _contiguous(qweight=qweight, scales=scales)
-    if bias is not None:
-        _contiguous(bias=bias)
+    if not (qweight.is_contiguous() and scales.is_contiguous() and (bias is None or bias.is_contiguous())):
+        raise ValueError("qweight, scales and bias must be contiguous")
     device = _gpu(x)
     if device != _device_now():
         with torch.cuda.device(device):
@@ -995,15 +1004,18 @@ def mxfp4_linear(x, qweight, scales, x_scales=None, x_format="mxfp8", bias=None,
     need = lib.cq_mxfp4_linear_workspace_size(M, n, inp, int(gated), form, int(x_scales is not None))
     if need and workspace is None:
         workspace = _empty(need, torch.uint8, x, stream)
-    px, pxs, pq, ps, pb, pr, py, pw = _on(
-        device, ("x", x), ("x_scales", x_scales), ("qweight", qweight), ("scales", scales), ("bias", bias),
-        ("residual", residual), ("out", out), ("workspace", workspace))
+    _same_gpu(device, x_scales=x_scales, qweight=qweight, scales=scales, bias=bias, residual=residual, out=out,
+              workspace=workspace)
     args = Mxfp4LinearArgs.from_buffer_copy(_MXFP4_LINEAR.pack(
-        px, pxs or 0, pq, ps, pb or 0, pr or 0, py, _ld(x), 0 if x_scales is None else _ld(x_scales),
-        0 if residual is None else _ld(residual), _ld(out), M, n, inp, _TYPES[dt], form, _TYPES[out.dtype], act,
-        int(gated)))
-    _check(lib.cq_mxfp4_linear(args, pw, 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                               _stream_on(stream, device)), "cq_mxfp4_linear")
+        x.data_ptr(), 0 if x_scales is None else x_scales.data_ptr(), qweight.data_ptr(), scales.data_ptr(),
+        0 if bias is None else bias.data_ptr(), 0 if residual is None else residual.data_ptr(), out.data_ptr(), _ld(x),
+        0 if x_scales is None else _ld(x_scales), 0 if residual is None else _ld(residual), _ld(out), M, n, inp,
+        _TYPES[dt], form, _TYPES[out.dtype], act, int(gated)))
+    status = lib.cq_mxfp4_linear(args, None if workspace is None else workspace.data_ptr(),
+                                 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                 _stream_on(stream, device))
+    if status:
+        raise CQError(status, "cq_mxfp4_linear")
     return out
 
 
@@ -1011,33 +1023,45 @@ _MX_CACHE = struct.Struct("@4P6q5i4x")  # MxCache, field by field
 assert _MX_CACHE.size == ctypes.sizeof(MxCache)
 
 
-def _like(a, b):
-    """Whether b has a's shape and, where it matters, its strides."""
-    return a.shape == b.shape and (a.stride() == b.stride() or
-                                   all(n == 1 or i == j for n, i, j in zip(a.shape, a.stride(), b.stride())))
+def _strides_like(a, b, shape):
+    """a's strides, which b must share where they matter."""
+    st, other = a.stride(), b.stride()
+    if st != other and any(n > 1 and i != j for n, i, j in zip(shape, st, other)):
+        raise ValueError("the caches of keys and of values must be strided alike, and so their scales")
+    return st
 
 
 def _mx_cache(k_cache, k_scales, v_cache, v_scales, heads, D, device):
     """The cache that a call reads or writes: its format follows from the width of its rows."""
     shape, sshape = k_cache.shape, k_scales.shape
-    if len(shape) != 4 or not _like(k_cache, v_cache) or shape[3] not in (D, D // 2) or shape[1] != heads:
+    if len(shape) != 4 or v_cache.shape != shape or shape[1] != heads or (shape[3] != D and shape[3] * 2 != D):
         raise ValueError("k_cache and v_cache must be [pages, kv_heads, page_size, head_dim (mxfp8) or head_dim / 2 "
-                         "(mxfp4)], strided alike")
+                         "(mxfp4)]")
     form = MXFP8 if shape[3] == D else MXFP4
     if D % MX_BLOCK or not 0 < D <= MAX_HEAD_DIM:
         raise ValueError("head_dim must be a multiple of 32 up to 256")
-    if sshape != shape[:3] + (D // MX_BLOCK,) or not _like(k_scales, v_scales):
-        raise ValueError("k_scales and v_scales must be [pages, kv_heads, page_size, head_dim / 32], strided alike")
-    for c, e in ((k_cache, k_scales), (v_cache, v_scales)):
-        if c.dtype not in _MX_CODES or (form == MXFP4 and c.dtype != torch.uint8) or e.dtype not in _MX_SCALES:
-            raise ValueError("caches must be uint8 (mxfp8: or float8_e4m3fn), their scales uint8 or float8_e8m0fnu")
-    if k_cache.stride(3) != 1 or (sshape[3] > 1 and k_scales.stride(3) != 1):
+    pages, _, page, _ = shape
+    if sshape != (pages, heads, page, D // MX_BLOCK) or v_scales.shape != sshape:
+        raise ValueError("k_scales and v_scales must be [pages, kv_heads, page_size, head_dim / 32]")
+    u8 = torch.uint8
+    if k_cache.dtype != u8 or v_cache.dtype != u8 or k_scales.dtype != u8 or v_scales.dtype != u8:
+        for c, e in ((k_cache, k_scales), (v_cache, v_scales)):
+            if c.dtype not in _MX_CODES or (form == MXFP4 and c.dtype != u8) or e.dtype not in _MX_SCALES:
+                raise ValueError("caches must be uint8 (mxfp8: or float8_e4m3fn), their scales uint8 or float8_e8m0fnu")
+    a, b, c, d = _strides_like(k_cache, v_cache, shape)
+    sa, sb, sc, sd = _strides_like(k_scales, v_scales, sshape)
+    if d != 1 or (sd != 1 and sshape[3] > 1):
         raise ValueError("the rows of caches and scales must be contiguous")
-    pk, pv, pks, pvs = _on(device, ("k_cache", k_cache), ("v_cache", v_cache), ("k_scales", k_scales),
-                           ("v_scales", v_scales))
-    st = [k_cache.stride(i) if shape[i] > 1 else 0 for i in range(3)]
-    st += [k_scales.stride(i) if shape[i] > 1 else 0 for i in range(3)]
-    return MxCache.from_buffer_copy(_MX_CACHE.pack(pk, pv, pks, pvs, *st, form, shape[0], shape[2], heads, D))
+    _same_gpu(device, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales)
+    if pages < 2:  # (a dimension of one entry has no stride)
+        a = sa = 0
+    if heads < 2:
+        b = sb = 0
+    if page < 2:
+        c = sc = 0
+    return MxCache.from_buffer_copy(_MX_CACHE.pack(
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), a, b, c, sa, sb, sc, form,
+        pages, page, heads, D))
 
 
 def kv_cache_write_mx(k, v, k_cache, k_scales, v_cache, v_scales, slots, stream=None):
@@ -1045,24 +1069,30 @@ def kv_cache_write_mx(k, v, k_cache, k_scales, v_cache, v_scales, slots, stream=
     codes uint8 [pages, kv_heads, page_size, head_dim] (mxfp8) or [.., head_dim / 2] (mxfp4) and of scales uint8 [..,
     head_dim / 32], each block as by mx_quantize, at slots int32 [T] (page * page_size + offset; a negative slot is
     skipped)."""
-    if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in (torch.bfloat16, torch.float16):
+    shape, dt = k.shape, k.dtype
+    if len(shape) != 3 or v.shape != shape or v.dtype != dt or (dt != torch.bfloat16 and dt != torch.float16):
         raise ValueError("k and v must be bfloat16 or float16 [T, kv_heads, head_dim]")
-    T, heads, D = k.shape
-    _int32(slots=slots)
-    if slots.numel() != T:
-        raise ValueError("slots must be int32 [T]")
-    if k.stride(2) != 1 or v.stride(2) != 1:
+    T, heads, D = shape
+    if slots.dtype != torch.int32 or slots.numel() != T or not slots.is_contiguous():
+        raise ValueError("slots must be int32 [T], contiguous")
+    kt, kh, kd = k.stride()
+    vt, vh, vd = v.stride()
+    if kd != 1 or vd != 1:
         raise ValueError("head_dim must be contiguous")
-    _contiguous(slots=slots)
+    if T < 2:  # (a dimension of one entry has no stride)
+        kt = vt = 0
+    if heads < 2:
+        kh = vh = 0
     device = _gpu(k_cache)
     if device != _device_now():
         with torch.cuda.device(device):
             return kv_cache_write_mx(k, v, k_cache, k_scales, v_cache, v_scales, slots, stream)
     cache = _mx_cache(k_cache, k_scales, v_cache, v_scales, heads, D, device)
-    pk, pv, ps = _on(device, ("k", k), ("v", v), ("slots", slots))
-    _check((_lib or load()).cq_kv_cache_write_mx(pk, _step(k, 0), _step(k, 1), pv, _step(v, 0), _step(v, 1),
-                                                 _TYPES[k.dtype], cache, ps, T, _stream_on(stream, device)),
-           "cq_kv_cache_write_mx")
+    _same_gpu(device, k=k, v=v, slots=slots)
+    status = (_lib or load()).cq_kv_cache_write_mx(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _TYPES[dt], cache,
+                                                   slots.data_ptr(), T, _stream_on(stream, device))
+    if status:
+        raise CQError(status, "cq_kv_cache_write_mx")
 
 
 def paged_attention_mx(q, k_cache, k_scales, v_cache, v_scales, block_table, cu_q, kv_len, max_q, max_kv, scale=None,
@@ -1070,19 +1100,19 @@ def paged_attention_mx(q, k_cache, k_scales, v_cache, v_scales, block_table, cu_
     """paged_attention over a cache of microscaled blocks, as kv_cache_write_mx fills it: codes uint8 [pages, kv_heads,
     page_size, head_dim] (mxfp8) or [.., head_dim / 2] (mxfp4), scales uint8 [.., head_dim / 32]; head_dim a multiple of
     32.  Everything else as there."""
-    dt = q.dtype
-    if q.dim() != 3 or dt not in (torch.bfloat16, torch.float16) or q.stride(2) != 1:
+    dt, shape, i32 = q.dtype, q.shape, torch.int32
+    if len(shape) != 3 or (dt != torch.bfloat16 and dt != torch.float16) or q.stride(2) != 1:
         raise ValueError("q must be bfloat16 or float16 [T, heads, head_dim], head_dim contiguous")
-    _int32(block_table=block_table, cu_q=cu_q, kv_len=kv_len)
-    T, H, D = q.shape
+    if block_table.dtype != i32 or cu_q.dtype != i32 or kv_len.dtype != i32:
+        raise ValueError("block_table, cu_q and kv_len must be int32")
+    T, H, D = shape
     R = kv_len.numel()
     if cu_q.numel() != R + 1 or block_table.dim() != 2 or block_table.shape[0] != R:
         raise ValueError("cu_q must be [R + 1], kv_len [R], block_table [R, max_pages]")
-    _contiguous(cu_q=cu_q, kv_len=kv_len)
-    if lse is not None:
-        if lse.shape != (T, H) or lse.dtype != torch.float32:
-            raise ValueError("lse must be float32 [T, heads]")
-        _contiguous(lse=lse)
+    if not (cu_q.is_contiguous() and kv_len.is_contiguous()):
+        raise ValueError("cu_q and kv_len must be contiguous")
+    if lse is not None and (lse.shape != (T, H) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse must be float32 [T, heads], contiguous")
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [pages, kv_heads, page_size, head_dim (mxfp8) or head_dim / 2 (mxfp4)]")
     device = _gpu(q)
@@ -1100,15 +1130,17 @@ def paged_attention_mx(q, k_cache, k_scales, v_cache, v_scales, block_table, cu_
     need = lib.cq_paged_attention_workspace_size(T, R, max_q, max_kv, H, Hkv, D)
     if need and workspace is None:
         workspace = _empty(need, torch.uint8, q, stream)
-    pq, pt, pcu, pkv, po, pl, pw = _on(device, ("q", q), ("block_table", block_table), ("cu_q", cu_q),
-                                       ("kv_len", kv_len), ("out", out), ("lse", lse), ("workspace", workspace))
+    _same_gpu(device, block_table=block_table, cu_q=cu_q, kv_len=kv_len, out=out, lse=lse, workspace=workspace)
     args = PagedAttentionArgs.from_buffer_copy(_ATTENTION_ARGS.pack(
-        pq, 0, 0, pt, pcu, pkv, po, pl or 0, _step(q, 0), _step(q, 1), _step(out, 0), _step(out, 1), 0, 0, 0,
+        q.data_ptr(), 0, 0, block_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), out.data_ptr(),
+        0 if lse is None else lse.data_ptr(), _step(q, 0), _step(q, 1), _step(out, 0), _step(out, 1), 0, 0, 0,
         _ld(block_table), _TYPES[dt], T, R, max_q, max_kv, H, Hkv, D, page, pages, block_table.shape[1], int(causal),
         window, D ** -0.5 if scale is None else scale))
-    _check(lib.cq_paged_attention_mx(args, cache, pw,
-                                     0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                     _stream_on(stream, device)), "cq_paged_attention_mx")
+    status = lib.cq_paged_attention_mx(args, cache, None if workspace is None else workspace.data_ptr(),
+                                       0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                       _stream_on(stream, device))
+    if status:
+        raise CQError(status, "cq_paged_attention_mx")
     return out
 
 

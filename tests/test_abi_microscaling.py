@@ -204,7 +204,7 @@ def test_attention_helper_refuses():
     _refused("lse", cq.paged_attention_mx, q, c, e, c, e, t, cu, kv, 2, 64, lse=torch.zeros(3, 4).half())
     _refused("k_cache", cq.paged_attention_mx, q, c[0], e, c, e, t, cu, kv, 2, 64)
     _refused("GPU", cq.paged_attention_mx, q, c, e, c, e, t, cu, kv, 2, 64)
-    _refused("strided alike", cq._mx_cache, c, e, c[:8], e, 2, 64, -1)
+    _refused("k_cache and v_cache", cq._mx_cache, c, e, c[:8], e, 2, 64, -1)
     _refused("strided alike", cq._mx_cache, c, e, c.transpose(1, 2).contiguous().transpose(1, 2), e, 2, 64, -1)
     _refused("mxfp8", cq._mx_cache, c, e, c, e, 2, 256, -1)
     _refused("multiple of 32", cq._mx_cache, c[..., :48], e, c[..., :48], e, 2, 48, -1)
