@@ -572,8 +572,11 @@ int32_t cq_kv_cache_write_mx(const void *k, int64_t k_token_stride, int64_t k_he
  * bfloat16; where type is CQ_F16, what it cannot hold is an infinity or rounded (values quantized from binary16 are exact).
  *   args   as for cq_paged_attention, whose k_cache, v_cache and their strides are not read; kv_heads, head_dim, page_size
  *          and n_pages are the cache's.
- * Masks, outputs, workspace, limits and errors as there; a NaN block has no effect on a row that does not see it.
+ * Masks, outputs, limits and errors as there; a NaN block has no effect on a row that does not see it.  The workspace is of
+ * cq_paged_attention_mx_workspace_size(...) bytes for the same sizes.
  */
+size_t cq_paged_attention_mx_workspace_size(int32_t n_tokens, int32_t n_requests, int32_t max_q, int32_t max_kv,
+                                            int32_t heads, int32_t kv_heads, int32_t head_dim);
 int32_t cq_paged_attention_mx(const cq_paged_attention_args *args, const cq_mx_cache *cache, void *workspace,
                               size_t workspace_bytes, void *stream);
 

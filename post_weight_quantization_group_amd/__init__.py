@@ -43,7 +43,7 @@ __all__ = [
     "paged_attention",
     "MXFP4", "MXFP8", "MX_BLOCK", "MxCache", "cq_mx_quantize", "mx_quantize", "cq_mx_dequantize", "mx_dequantize",
     "cq_kv_cache_write_mx", "kv_cache_write_mx", "Mxfp4LinearArgs", "cq_mxfp4_linear_workspace_size", "cq_mxfp4_linear",
-    "mxfp4_linear", "cq_paged_attention_mx", "paged_attention_mx",
+    "mxfp4_linear", "cq_paged_attention_mx_workspace_size", "cq_paged_attention_mx", "paged_attention_mx",
 ]
 
 GROUP = 128
@@ -74,7 +74,7 @@ EXPORTED_SYMBOLS = ("cq_abi_version", "cq_status_string", "cq_workspace_size", "
                     "cq_w4a16_matmul", "cq_probe_valu_fma", "cq_w4a16_linear", "cq_kv_block_map",
                     "cq_kv_cache_write", "cq_paged_attention_workspace_size", "cq_paged_attention",
                     "cq_mx_quantize", "cq_mx_dequantize", "cq_kv_cache_write_mx", "cq_mxfp4_linear_workspace_size",
-                    "cq_mxfp4_linear", "cq_paged_attention_mx")
+                    "cq_mxfp4_linear", "cq_paged_attention_mx_workspace_size", "cq_paged_attention_mx")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lib = None
@@ -190,6 +190,8 @@ def load():
         lib.cq_mxfp4_linear_workspace_size.argtypes = [I64, I64, I64, I32, I32, I32]
         lib.cq_mxfp4_linear.restype = I32
         lib.cq_mxfp4_linear.argtypes = [ctypes.POINTER(Mxfp4LinearArgs), P, SZ, P]
+        lib.cq_paged_attention_mx_workspace_size.restype = SZ
+        lib.cq_paged_attention_mx_workspace_size.argtypes = [I32] * 7
         lib.cq_paged_attention_mx.restype = I32
         lib.cq_paged_attention_mx.argtypes = [ctypes.POINTER(PagedAttentionArgs), ctypes.POINTER(MxCache), P, SZ, P]
         _lib = lib
@@ -469,6 +471,11 @@ def cq_mxfp4_linear_workspace_size(M: int, out: int, inp: int, gated: int, x_for
 def cq_mxfp4_linear(args: Mxfp4LinearArgs, workspace=None, stream=None):
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(load().cq_mxfp4_linear(args, _p(workspace), ws_bytes, _stream(stream)), "cq_mxfp4_linear")
+
+
+def cq_paged_attention_mx_workspace_size(n_tokens: int, n_requests: int, max_q: int, max_kv: int, heads: int,
+                                         kv_heads: int, head_dim: int) -> int:
+    return load().cq_paged_attention_mx_workspace_size(n_tokens, n_requests, max_q, max_kv, heads, kv_heads, head_dim)
 
 
 def cq_paged_attention_mx(args: PagedAttentionArgs, cache: MxCache, workspace=None, stream=None):
@@ -1127,7 +1134,7 @@ def paged_attention_mx(q, k_cache, k_scales, v_cache, v_scales, block_table, cu_
     elif out.shape != q.shape or out.dtype != dt or out.stride(2) != 1:
         raise ValueError("out must be [T, heads, head_dim] of q's type, head_dim contiguous")
     lib = _lib or load()
-    need = lib.cq_paged_attention_workspace_size(T, R, max_q, max_kv, H, Hkv, D)
+    need = lib.cq_paged_attention_mx_workspace_size(T, R, max_q, max_kv, H, Hkv, D)
     if need and workspace is None:
         workspace = _empty(need, torch.uint8, q, stream)
     _same_gpu(device, block_table=block_table, cu_q=cu_q, kv_len=kv_len, out=out, lse=lse, workspace=workspace)

@@ -553,12 +553,19 @@ static bool attention_sizes_ok(int32_t T, int32_t R, int32_t max_q, int32_t max_
 size_t cq_paged_attention_workspace_size(int32_t n_tokens, int32_t n_requests, int32_t max_q, int32_t max_kv,
                                          int32_t heads, int32_t kv_heads, int32_t head_dim) {
     if (!attention_sizes_ok(n_tokens, n_requests, max_q, max_kv, heads, kv_heads, head_dim)) return 0;
-    return (size_t)cqk::attention_ws(n_requests, n_tokens, max_q, max_kv, heads, kv_heads, head_dim) * 4u;
+    return (size_t)cqk::attention_ws(n_requests, n_tokens, max_q, max_kv, heads, kv_heads, head_dim, false) * 4u;
+}
+
+size_t cq_paged_attention_mx_workspace_size(int32_t n_tokens, int32_t n_requests, int32_t max_q, int32_t max_kv,
+                                            int32_t heads, int32_t kv_heads, int32_t head_dim) {
+    if (!attention_sizes_ok(n_tokens, n_requests, max_q, max_kv, heads, kv_heads, head_dim) || head_dim % CQ_MX_BLOCK != 0)
+        return 0;
+    return (size_t)cqk::attention_ws(n_requests, n_tokens, max_q, max_kv, heads, kv_heads, head_dim, true) * 4u;
 }
 
 // Checks of what both attentions take (the cache's own arrays and strides apart) and the kernels' arguments; `nothing`:
 // there is no token.
-static int32_t attention_args(const cq_paged_attention_args& p, void* workspace, size_t workspace_bytes,
+static int32_t attention_args(const cq_paged_attention_args& p, bool mx, void* workspace, size_t workspace_bytes,
                               cqk::AttentionArgs& a, bool& nothing) {
     nothing = false;
     if (p.type != CQ_BF16 && p.type != CQ_F16) return CQ_EINVAL;
@@ -580,8 +587,8 @@ static int32_t attention_args(const cq_paged_attention_args& p, void* workspace,
         return CQ_EINVAL;
     if (!cqk::attention_fits(p.n_requests, p.n_tokens, p.max_q, p.max_kv, p.heads, p.kv_heads, p.head_dim))
         return CQ_EUNSUPPORTED;
-    const size_t need = cq_paged_attention_workspace_size(p.n_tokens, p.n_requests, p.max_q, p.max_kv, p.heads,
-                                                          p.kv_heads, p.head_dim);
+    const auto size = mx ? cq_paged_attention_mx_workspace_size : cq_paged_attention_workspace_size;
+    const size_t need = size(p.n_tokens, p.n_requests, p.max_q, p.max_kv, p.heads, p.kv_heads, p.head_dim);
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, ALIGN))) return CQ_EWORKSPACE;
     a = cqk::AttentionArgs{};
     a.q = (const uint16_t*)p.q; a.out = (uint16_t*)p.out; a.lse = p.lse;
@@ -606,7 +613,7 @@ int32_t cq_paged_attention(const cq_paged_attention_args* args, void* workspace,
     }
     cqk::AttentionArgs a;
     bool nothing;
-    const int32_t status = attention_args(p, workspace, workspace_bytes, a, nothing);
+    const int32_t status = attention_args(p, false, workspace, workspace_bytes, a, nothing);
     if (status != CQ_OK || nothing) return status;
     a.kc = (const uint16_t*)p.k_cache; a.vc = (const uint16_t*)p.v_cache;
     a.c_page = p.page_stride; a.c_head = p.head_stride; a.c_row = p.row_stride;
@@ -625,7 +632,7 @@ int32_t cq_paged_attention_mx(const cq_paged_attention_args* args, const cq_mx_c
         return CQ_EINVAL;
     cqk::AttentionArgs a;
     bool nothing;
-    const int32_t status = attention_args(p, workspace, workspace_bytes, a, nothing);
+    const int32_t status = attention_args(p, true, workspace, workspace_bytes, a, nothing);
     if (status != CQ_OK || nothing) return status;
     const cqk::MxCache m = mx_cache(c);
     a.kc = (const uint16_t*)m.kc; a.vc = (const uint16_t*)m.vc; a.ks = m.ks; a.vs = m.vs;

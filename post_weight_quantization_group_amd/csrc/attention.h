@@ -270,8 +270,8 @@ struct Share {
 #pragma unroll
         for (int i = 0; i < L::PIECES; ++i) scale[i] = 0;
     }
-    // row, scales: of this key and head; D: the row's length
-    __device__ __forceinline__ void load(const uint8_t* row, const uint8_t* scales, int quad, int D) {
+    // row + at, scales + scale_at: of this key and head; D: the row's length
+    __device__ __forceinline__ void load(const uint8_t* row, uint32_t at, const uint8_t* scales, uint32_t scale_at, int quad, int D) {
         constexpr int N = L::STEPS * L::WORDS;  // words a piece
         typedef uint32_t words __attribute__((ext_vector_type(N)));
 #pragma unroll
@@ -279,13 +279,13 @@ struct Share {
             const int d = 4 * L::PIECE * j + L::PIECE * quad;
             if (D != DP && d >= D) continue;
             if constexpr (N == 1) {
-                w[j] = *reinterpret_cast<const uint32_t*>(row + d / 2);
+                w[j] = *reinterpret_cast<const uint32_t*>(row + (at + d / 2));
             } else {
-                const words v = *reinterpret_cast<const words*>(row + (KIND == MXFP4 ? d / 2 : d));
+                const words v = *reinterpret_cast<const words*>(row + (at + (KIND == MXFP4 ? d / 2 : d)));
 #pragma unroll
                 for (int i = 0; i < N; ++i) w[N * j + i] = v[i];
             }
-            scale[j] = scales[d / MX_BLOCK];
+            scale[j] = scales[scale_at + d / MX_BLOCK];
         }
     }
     __device__ __forceinline__ uint4 step(int ks) const {
@@ -328,16 +328,28 @@ __device__ __forceinline__ uint2 four_of_value(const AttentionArgs& a, int kvh, 
 // which three loads that wait for each other (lengths, table, keys) take the most, and 4.0 for the join.  D = 256 (one wave
 // per SIMD): the same 64 requests 646 us, 5.3 TB/s.  Four waves a workgroup | eight, us: one request of 100 keys 6.5 | 6.6,
 // at D = 256 8.7 | 11.4, the 64 requests at D = 256 646 | 757 (eight spill), at D = 128 and 64 the same.
-template <int KIND, bool F16, int DP>
-__global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl) {
+//
+// Microscaled blocks (KIND): a lane's pieces are smaller, so that more of the time is the chain of a tile's steps, and waves
+// beside each other hide it: three per SIMD up to 128 dimensions (four up to 64), two above.  The same 64 requests, us, MXFP8 |
+// MXFP4: 204 | 119 (256 dimensions 406 | 216, without that bound on registers 458 | 311).  Two tiles on their way in
+// place of one: 234 | 130, with fewer waves.
+template <int KIND, int DP, bool PAGE16>
+constexpr int few_waves_per_simd() { return KIND == CACHE_16 ? 1 : (DP <= 64 ? 4 : DP <= 128 ? 3 : 2) - (PAGE16 ? 0 : 1); }
+
+// W waves: 4, or 8 where the keys are not divided over workgroups.
+template <int KIND, bool F16, int DP, bool PAGE16, int W>
+__global__ __launch_bounds__(64 * W, (W == 8 ? 2 : few_waves_per_simd<KIND, DP, PAGE16>())) void few_rows_kernel(AttentionArgs a, Plan pl) {
     typedef Lanes<KIND, DP> L;
     constexpr int BM = FEW, BN = 32, KS = DP / 32, DT = DP / 16;
-    constexpr int VS = DP + ((DP / 2) % 64 == 16 || (DP / 2) % 64 == 48 ? 0 : 32);  // rows 16 banks apart (mod 64)
+    // Rows of V 16 banks apart (mod 64); of microscaled blocks an odd multiple of 8, with which 8 rows written at one
+    // dimension miss each other too: a fourth of the cycles that LDS loses to them otherwise.
+    constexpr int VS = KIND != CACHE_16 ? DP + 16 : DP + ((DP / 2) % 64 == 16 || (DP / 2) % 64 == 48 ? 0 : 32);
     constexpr int OS = DP + 4;
     constexpr int WAVE_BYTES = BN * VS * 2 > BM * OS * 4 ? BN * VS * 2 : BM * OS * 4;
-    __shared__ __align__(16) uint8_t lds[4 * WAVE_BYTES];
-    __shared__ float wave_m[4][BM], wave_l[4][BM];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, quad = lane >> 4;
+    __shared__ __align__(16) uint8_t lds[W * WAVE_BYTES];
+    __shared__ float wave_m[W][BM], wave_l[W][BM];
+    const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, quad = lane >> 4;
+    const int wave = PAGE16 ? __builtin_amdgcn_readfirstlane(tid >> 6) : tid >> 6;
     const int G = pl.G, kvh = blockIdx.x, r = blockIdx.y, split = blockIdx.z;
     if (pl.zero_rest) zero_rest<DP>(a);
     if (a.R == 0 || split >= pl.splits) return;
@@ -373,10 +385,17 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
     const int t0 = t_begin + split * per, t1 = min(t_end, t0 + per);
     const int32_t* table = a.table + r * a.table_stride;
 
+    const uint32_t col_at = PAGE16 ? col * (uint32_t)a.c_row : 0, col_scale = PAGE16 ? col * (uint32_t)a.s_row : 0;
     int page_id[2];
     auto fetch_ids = [&](int t) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            if constexpr (PAGE16) {  // the 16 keys are in one page
+                const int key = t * BN + 16 * h;
+                page_id[h] = -1;
+                if (t < t1 && key + 16 > w.key_begin && key < w.key_end) page_id[h] = table[page_of(pl, key)];
+                continue;
+            }
             const int key = t * BN + 16 * h + col;
             page_id[h] = -1;
             if (t < t1 && key >= w.key_begin && key < w.key_end) page_id[h] = table[page_of(pl, key)];
@@ -388,9 +407,19 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int key = t * BN + 16 * h + col;
-            ok_next[h] = page_id[h] >= 0 && page_id[h] < a.n_pages;
             kr[h].clear();
             vr[h].clear();
+            if constexpr (PAGE16) {
+                const int id = __builtin_amdgcn_readfirstlane(page_id[h]), first = t * BN + 16 * h, in_page = first - page_of(pl, first) * a.page;
+                ok_next[h] = id >= 0 && id < a.n_pages && key >= w.key_begin && key < w.key_end;
+                if (!ok_next[h]) continue;
+                const int64_t at = id * a.c_page + kvh * a.c_head + in_page * a.c_row;
+                const int64_t sat = id * a.s_page + kvh * a.s_head + in_page * a.s_row;
+                kr[h].load(reinterpret_cast<const uint8_t*>(a.kc) + at, col_at, a.ks + sat, col_scale, quad, a.D);
+                vr[h].load(reinterpret_cast<const uint8_t*>(a.vc) + at, col_at, a.vs + sat, col_scale, quad, a.D);
+                continue;
+            }
+            ok_next[h] = page_id[h] >= 0 && page_id[h] < a.n_pages;
             if constexpr (KIND == CACHE_16) {
                 const int64_t at = page_id[h] * a.c_page + kvh * a.c_head + (int64_t)(key - page_of(pl, key) * a.page) * a.c_row + 8 * quad;
                 if (!ok_next[h]) continue;
@@ -412,8 +441,8 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
                 const int in_page = key - page_of(pl, key) * a.page;
                 const int64_t at = page_id[h] * a.c_page + kvh * a.c_head + (int64_t)in_page * a.c_row;
                 const int64_t sat = page_id[h] * a.s_page + kvh * a.s_head + (int64_t)in_page * a.s_row;
-                kr[h].load(reinterpret_cast<const uint8_t*>(a.kc) + at, a.ks + sat, quad, a.D);
-                vr[h].load(reinterpret_cast<const uint8_t*>(a.vc) + at, a.vs + sat, quad, a.D);
+                kr[h].load(reinterpret_cast<const uint8_t*>(a.kc) + at, 0, a.ks + sat, 0, quad, a.D);
+                vr[h].load(reinterpret_cast<const uint8_t*>(a.vc) + at, 0, a.vs + sat, 0, quad, a.D);
             }
         }
     };
@@ -427,8 +456,8 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
     int t = t0 + wave;
     fetch_ids(t);
     fetch_kv(t);
-    fetch_ids(t + 4);
-    for (; t < t1; t += 4) {
+    fetch_ids(t + W);
+    for (; t < t1; t += W) {
         f32x4 s[2];
         const bool mixed = t * BN < same_lo || (t + 1) * BN > same_hi;
         uint64_t there[2];
@@ -457,8 +486,8 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
                     *at = finite_part<F16>(*at);
                 }
         }
-        fetch_kv(t + 4);
-        fetch_ids(t + 8);
+        fetch_kv(t + W);
+        fetch_ids(t + 2 * W);
         // masks, running maximum
         float top = -INFINITY;
         const bool all_there = (there[0] & there[1] & 0xffff) == 0xffff;
@@ -517,7 +546,7 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
 
-    // join the four waves
+    // join the waves
     float* ol = reinterpret_cast<float*>(lds + wave * WAVE_BYTES);
     __syncthreads();
     if (quad == 0) {
@@ -532,16 +561,16 @@ __global__ __launch_bounds__(256) void few_rows_kernel(AttentionArgs a, Plan pl)
     __syncthreads();
     const int live_rows = rows;
     const int64_t part = ((int64_t)r * a.Hkv + kvh) * pl.splits + split;
-    for (int i = tid; i < live_rows * (DP / 4); i += 256) {
+    for (int i = tid; i < live_rows * (DP / 4); i += 64 * W) {
         const int c = i / (DP / 4), d = i % (DP / 4) * 4;
         float M = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) M = fmaxf(M, wave_m[x][c]);
+        for (int x = 0; x < W; ++x) M = fmaxf(M, wave_m[x][c]);
         const float Mc = M == -INFINITY ? 0.0f : M * pl.c;
         float L = 0.0f;
         f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < W; ++x) {
             const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(wave_m[x][c], pl.c, -Mc));  // 0: it saw no key of the row
             L = __builtin_fmaf(f, wave_l[x][c], L);
             const f32x4 v = *reinterpret_cast<const f32x4*>(lds + x * WAVE_BYTES + (c * OS + d) * 4);
@@ -1059,10 +1088,15 @@ __global__ __launch_bounds__(256) void join_kernel(AttentionArgs a, Plan pl) {
 struct Parts {
     int64_t few_tiles, many_tiles;
     int few_splits, many_splits;  // 0: not launched
+    int few_waves;                // of a workgroup
     int many_each;                // Plan::each
 };
 
 int padded_dim(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : D <= 192 ? 192 : 256; }
+// That of few_rows_kernel: a lane's fourth of 96 microscaled values would go in pieces of 8, which at 128 are 32 (or 16).  64
+// requests of up to 8,192 keys (24 heads over 8, D = 96), us, 96 | 128: MXFP8 186 | 158, MXFP4 161 | 105.
+template <int KIND>
+constexpr int few_dim(int padded) { return KIND != CACHE_16 && padded == 96 ? 128 : padded; }
 
 int splits_for(int64_t groups, int64_t want, int max_kv, int least_keys) {
     int64_t s = groups < 1 ? 1 : want / groups, most = max_kv / least_keys;
@@ -1070,15 +1104,24 @@ int splits_for(int64_t groups, int64_t want, int max_kv, int least_keys) {
     return s < 1 ? 1 : s > 256 ? 256 : (int)s;
 }
 
-Parts divide(int R, int T, int max_q, int max_kv, int H, int Hkv, int D) {
+Parts divide(int R, int T, int max_q, int max_kv, int H, int Hkv, int D, bool mx) {
     const int64_t G = H / Hkv, rows = max_q * G;
     Parts p{};
+    p.few_waves = 4;
     p.few_tiles = R > 0 ? R : 1;
     if (rows <= FEW || (int64_t)R * max_q != T) {  // some requests may have few rows
         // A workgroup per CU, two up to 64 dimensions; D = 128 (64), us: 32 requests of 4,000 keys 31.0 (21.9) at 256
         // workgroups, 31.4 (19.3) at 512, 33.1 (19.6) at 768; 100 of 9,000: 166 (125), 193 (97), 192 (108).  64 keys at
         // least: one request of 1,000 keys 10.3 us, at 128 11.7, at 256 14.1.
         p.few_splits = splits_for(p.few_tiles * Hkv, D <= 64 ? 512 : 256, max_kv, 64);
+        // Microscaled blocks, up to 768 keys with workgroups for no more than every CU: eight waves take them all in the time
+        // of the parts and their join, in one launch.  8 heads over 2, D = 128, us, 8 waves | parts, MXFP8 (MXFP4): 200 keys
+        // 7.8 (7.4) | 9.8 (9.5), 450 10.0 (8.9) | 9.7 (9.3), 950 13.6 (10.6) | 10.2 (9.7); a call of the 450 from Python
+        // 12.3 | 16.4.
+        if (mx && max_kv <= 768 && p.few_tiles * Hkv <= 256 && p.few_splits > 1) {
+            p.few_splits = 1;
+            p.few_waves = 8;
+        }
     }
     if (rows > FEW && R > 0) {
         // Whichever numbering of the row tiles takes fewer: by the tokens in front of a request, or as many for each as
@@ -1114,10 +1157,21 @@ hipError_t launch_dim(const AttentionArgs& a, Plan pl, const Parts& p, hipStream
         pl.rows_hi = FEW;
         pl.tiles = p.few_tiles;
         const unsigned more = parts_to_zero(a, p.few_tiles * a.Hkv, p.few_splits);
-        hipLaunchKernelGGL((few_rows_kernel<KIND, F16, DP>), dim3(a.Hkv, (unsigned)p.few_tiles, p.few_splits + more), dim3(256),
-                           0, st, a, pl);
+        const dim3 grid(a.Hkv, (unsigned)p.few_tiles, p.few_splits + more);
+        constexpr int FP = few_dim<KIND>(DP);
+        // 16 keys that start at a multiple of 16 are in one page: its place is worked out once for the wave, and a lane's share
+        // of it is an offset of 32 bits.
+        const bool page16 = KIND != CACHE_16 && a.page % 16 == 0 && (a.c_row | a.s_row) < 1 << 26;
+        if constexpr (KIND != CACHE_16) {
+            if (p.few_waves == 8 && page16)
+                hipLaunchKernelGGL((few_rows_kernel<KIND, F16, FP, true, 8>), grid, dim3(512), 0, st, a, pl);
+            else if (page16)
+                hipLaunchKernelGGL((few_rows_kernel<KIND, F16, FP, true, 4>), grid, dim3(256), 0, st, a, pl);
+        }
+        if (!page16)
+            hipLaunchKernelGGL((few_rows_kernel<KIND, F16, FP, false, 4>), grid, dim3(256), 0, st, a, pl);
         if (p.few_splits > 1)
-            hipLaunchKernelGGL((join_kernel<F16, DP, FEW, 256>), dim3((unsigned)(p.few_tiles * a.Hkv * FEW)), dim3(256), 0,
+            hipLaunchKernelGGL((join_kernel<F16, FP, FEW, 256>), dim3((unsigned)(p.few_tiles * a.Hkv * FEW)), dim3(256), 0,
                                st, a, pl);
         pl.zero_rest = 0;
     }
@@ -1160,7 +1214,7 @@ hipError_t launch_kind(const AttentionArgs& args, hipStream_t st) {
     pl.magic = (uint32_t)((((uint64_t)1 << (31 + bits)) + a.page - 1) / a.page);
     pl.shift = 31 + bits;
     pl.G = a.H / a.Hkv;
-    const Parts p = divide(a.R, a.T, a.max_q, a.max_kv, a.H, a.Hkv, a.D);
+    const Parts p = divide(a.R, a.T, a.max_q, a.max_kv, a.H, a.Hkv, a.D, KIND != CACHE_16);
     return a.f16 ? launch_type<KIND, true>(a, pl, p, st) : launch_type<KIND, false>(a, pl, p, st);
 }
 

@@ -98,7 +98,7 @@ struct AttentionArgs {
 // Whether the grid for these sizes (its threads numbered in 32 bits) can be launched.
 bool attention_fits(int32_t R, int32_t T, int32_t max_q, int32_t max_kv, int32_t H, int32_t Hkv, int32_t D);
 // Floats of workspace the launch for these sizes uses (0: none).
-int64_t attention_ws(int32_t R, int32_t T, int32_t max_q, int32_t max_kv, int32_t H, int32_t Hkv, int32_t D);
+int64_t attention_ws(int32_t R, int32_t T, int32_t max_q, int32_t max_kv, int32_t H, int32_t Hkv, int32_t D, bool mx);
 hipError_t launch_attention(const AttentionArgs& a, hipStream_t st);
 hipError_t launch_attention_mx(const AttentionArgs& a, int form, hipStream_t st);
 

@@ -243,7 +243,7 @@ def test_stream_graph_and_workspace(form):
     want = p.run(cq)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    need = cq.cq_paged_attention_workspace_size(2, 2, 1, 3000, 4, 2, 128)
+    need = cq.cq_paged_attention_mx_workspace_size(2, 2, 1, 3000, 4, 2, 128)
     got = p.run(cq, stream=side, workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
     side.synchronize()
     assert torch.equal(got, want)
