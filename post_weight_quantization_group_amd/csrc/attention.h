@@ -642,8 +642,10 @@ __device__ const uint4 zeros[1] = {};  // what a lane reads for a key or a dimen
 // wave per SIMD and the next scores between the exponentials (792 us); 128 rows a workgroup (766); two groups of waves
 // in turns (712 to 740).
 template <int KIND, bool F16, int DP, int BN>
-__global__ __launch_bounds__(2 * MANY, 2) void many_rows_kernel(AttentionArgs a, Plan pl) {
+__global__ __launch_bounds__(2 * MANY, (KIND != CACHE_16 && DP <= 64 ? 4 : 2)) void many_rows_kernel(AttentionArgs a, Plan pl) {
     constexpr int BM = MANY, KS = DP / 16, DT = DP / 32, KT = BN / 32;
+    // no registers to spare: what can be is worked out anew where it is needed
+    constexpr bool TIGHT = KIND != CACHE_16 && (DP > 192 || DP <= 64);
     constexpr int RUNS = BN * DP / 8 / 64, WAVES = MANY / 32;  // loads of 64 16-byte pieces a tile of K or V takes
     constexpr int PIECES = (RUNS + WAVES - 1) / WAVES;         // of them, per wave
     constexpr int STAGES = KIND == CACHE_16 ? 4 : 2;           // tiles in LDS
@@ -740,7 +742,7 @@ __global__ __launch_bounds__(2 * MANY, 2) void many_rows_kernel(AttentionArgs a,
     uint32_t raw_scale[SHARES];
     auto ask = [&](int t) {
         int me = lane;
-        if constexpr (DP > 128) asm volatile("" : "+v"(me));  // (as in fetch)
+        if constexpr (DP > 128 || TIGHT) asm volatile("" : "+v"(me));  // (as in fetch)
         const int64_t* rows_at = &row_at[t * BN / BLOCK & 1][t * BN % BLOCK];
         const int64_t* srows_at = &scales_at[t * BN / BLOCK & 1][t * BN % BLOCK];
 #pragma unroll
@@ -766,7 +768,7 @@ __global__ __launch_bounds__(2 * MANY, 2) void many_rows_kernel(AttentionArgs a,
     };
     auto put = [&](int t) {
         int me = lane;
-        if constexpr (DP > 128) asm volatile("" : "+v"(me));
+        if constexpr (DP > 128 || TIGHT) asm volatile("" : "+v"(me));
 #pragma unroll
         for (int i = 0; i < SHARES; ++i) {
             const int u = BLOCK * i + 64 * wave;
@@ -829,7 +831,7 @@ __global__ __launch_bounds__(2 * MANY, 2) void many_rows_kernel(AttentionArgs a,
         bool special = false;
         if (t * BN < same_lo || (t + 1) * BN > same_hi) {  // the rows' masks differ here
             int me = lane;
-            if constexpr (KIND != CACHE_16 && DP > 192) asm volatile("" : "+v"(me));
+            if constexpr (TIGHT) asm volatile("" : "+v"(me));
 #pragma unroll 1
             for (int i = 64 * wave + me; i < 64 * RUNS; i += 64 * WAVES) {
                 uint16_t* at = &vtile[t % STAGES][8 * i];
@@ -861,7 +863,7 @@ __global__ __launch_bounds__(2 * MANY, 2) void many_rows_kernel(AttentionArgs a,
                 s[kt] = mfma32<F16>(*(lds_s16x8)at, q[ks], s[kt]);
             }
         // four operands ahead of their products (the compiler reads each just before it), two where registers are short
-        constexpr int AHEAD = KIND == CACHE_16 || DP <= 192 ? 4 : 2;
+        constexpr int AHEAD = TIGHT && DP > 64 ? 2 : 4;
         __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
 #pragma unroll
         for (int x = 0; x < (KS * KT - AHEAD) / 2; ++x) {
@@ -940,7 +942,7 @@ __global__ __launch_bounds__(2 * MANY, 2) void many_rows_kernel(AttentionArgs a,
     l += __shfl_xor(l, 32);
     // the lane's row once more: there are no registers to keep it through the tiles
     int me = lane;
-    if constexpr (KIND != CACHE_16 && DP > 192) asm volatile("" : "+v"(me));
+    if constexpr (TIGHT) asm volatile("" : "+v"(me));
     const int end_col = me & 31, end_half = me >> 5, end_row = first + 32 * wave + end_col, end_tok = end_row / G;
     const bool end_live = end_row < rows;
     if (pl.splits > 1) {
