@@ -502,7 +502,7 @@ int32_t cq_paged_attention(const cq_paged_attention_args *args, void *workspace,
  *   x       x_type (CQ_BF16, CQ_F16 or CQ_F32) [rows] of `len`, ldx elements apart; 16-byte aligned, ldx a multiple of 8.
  *   codes   out, [rows] of len / 2 bytes (CQ_MXFP8: len), ldc bytes apart; 16-byte aligned, ldc a multiple of 16.
  *   scales  out, [rows] of len / 32 bytes, lds apart.
- * len a positive multiple of 32; rows * len < 2^35; rows == 0 enqueues nothing.
+ * len a positive multiple of 32; rows * len < 2^34; rows == 0 enqueues nothing.
  */
 int32_t cq_mx_quantize(const void *x, int64_t ldx, int32_t x_type, int64_t rows, int64_t len, int32_t format,
                        uint8_t *codes, int64_t ldc, uint8_t *scales, int64_t lds, void *stream);
@@ -528,7 +528,7 @@ int32_t cq_mx_dequantize(const uint8_t *codes, int64_t ldc, const uint8_t *scale
  *              aligned: W in MXFP4, as cq_mx_quantize gives them for [cols][in].  cols = out, or 2 out when gated (the gate's first).
  *   bias, residual, y, activation, gated   as for cq_w4a16_linear.
  *   workspace  cq_mxfp4_linear_workspace_size(...) bytes for the same sizes (0: may be NULL); `codes`: whether x is.
- * in a positive multiple of 128 up to 2^22; cols <= 2^25, M * cols < 2^38, M * in < 2^35, M < 2^31; M == 0 or out == 0 enqueues nothing.
+ * in a positive multiple of 128 up to 2^22; cols <= 2^25, M * cols < 2^38, M * in < 2^34, M < 2^31; M == 0 or out == 0 enqueues nothing.
  */
 typedef struct cq_mxfp4_linear_args {
     const void *x;

@@ -437,8 +437,8 @@ int32_t cq_kv_cache_write(const void* k, int64_t k_token_stride, int64_t k_head_
 static bool mx_rows_ok(const void* values, int64_t ldx, int32_t type, int64_t rows, int64_t len, int32_t format,
                        const void* codes, int64_t ldc, const void* scales, int64_t lds) {
     if ((type != CQ_BF16 && type != CQ_F16 && type != CQ_F32) || (format != CQ_MXFP4 && format != CQ_MXFP8)) return false;
-    if (rows < 0 || len <= 0 || len % CQ_MX_BLOCK != 0 || len >= (int64_t)1 << 35) return false;
-    if (rows > 0 && rows > (((int64_t)1 << 35) - 1) / len) return false;
+    if (rows < 0 || len <= 0 || len % CQ_MX_BLOCK != 0 || len >= (int64_t)1 << 34) return false;
+    if (rows > (((int64_t)1 << 34) - 1) / len) return false;  // (a thread for 8 values: a launch has less than 2^32 of them)
     if (rows == 0) return true;
     if (!values || !codes || !scales || !aligned(values, 16) || !aligned(codes, 16)) return false;
     return ldx >= len && ldx % 8 == 0 && ldc >= (format == CQ_MXFP4 ? len / 2 : len) && ldc % 16 == 0 &&
@@ -473,7 +473,7 @@ static bool mx_linear_sizes_ok(int64_t M, int64_t out, int64_t in, int32_t gated
     if ((x_format != CQ_MXFP4 && x_format != CQ_MXFP8) || (gated != 0 && gated != 1)) return false;
     if (M < 0 || out < 0 || in <= 0 || in % CQ_GROUP != 0 || in > (int64_t)1 << 22) return false;
     if (M > INT32_MAX || out > (int64_t)1 << (gated ? 24 : 25)) return false;
-    return M * (gated ? 2 * out : out) < (int64_t)1 << 38 && M * in < (int64_t)1 << 35;
+    return M * (gated ? 2 * out : out) < (int64_t)1 << 38 && M * in < (int64_t)1 << 34;
 }
 
 size_t cq_mxfp4_linear_workspace_size(int64_t M, int64_t out, int64_t in, int32_t gated, int32_t x_format,

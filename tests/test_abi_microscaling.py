@@ -22,7 +22,7 @@ def _rows(entry, **kw):
 @pytest.mark.parametrize("entry", ["quantize", "dequantize"])
 @pytest.mark.parametrize("kw", [
     dict(xt=3), dict(xt=-1), dict(form=2), dict(form=5), dict(rows=-1), dict(len=0), dict(len=-32), dict(len=48),
-    dict(len=1 << 35, ldx=1 << 35, ldc=1 << 34, lds=1 << 30), dict(rows=1 << 28), dict(rows=1 << 62), dict(x=None),
+    dict(len=1 << 34, ldx=1 << 34, ldc=1 << 33, lds=1 << 29), dict(rows=1 << 27), dict(rows=1 << 62), dict(x=None),
     dict(codes=None), dict(scales=None), dict(x=FAKE + 8), dict(codes=FAKE + 8), dict(ldx=120), dict(ldx=132),
     dict(ldc=48), dict(ldc=72), dict(lds=3), dict(form=cq.MXFP8),
 ])
@@ -111,7 +111,7 @@ def _linear(ws=None, ws_bytes=0, **kw):
     dict(gated=2), dict(x_format=2), dict(x_format=5), dict(M=-1), dict(out=-1), dict(inp=0), dict(inp=160),
     dict(inp=-128), dict(inp=(1 << 22) + 128, ldx=1 << 23), dict(x_scales=FAKE, ldxs=8, ldx=(1 << 23) + 16), dict(M=1 << 31),
     dict(out=(1 << 25) + 1), dict(out=(1 << 24) + 1, gated=1), dict(inp=1 << 25),
-    dict(M=1 << 20, out=1 << 18), dict(M=1 << 20, inp=1 << 15, ldx=1 << 15), dict(x=None), dict(qweight=None), dict(scales=None), dict(y=None), dict(ldx=128),
+    dict(M=1 << 20, out=1 << 18), dict(M=1 << 19, inp=1 << 15, ldx=1 << 15), dict(x=None), dict(qweight=None), dict(scales=None), dict(y=None), dict(ldx=128),
     dict(ldx=260), dict(ldy=7), dict(residual=FAKE, ldr=7), dict(x=FAKE + 8), dict(qweight=FAKE + 8),
     dict(bias=FAKE + 1), dict(residual=FAKE + 1, ldr=8), dict(y=FAKE + 1), dict(y=FAKE + 2, y_type=cq.F32),
     dict(x_scales=FAKE, ldxs=7), dict(x_scales=FAKE, ldxs=10), dict(x_scales=FAKE + 2, ldxs=8), dict(scales=FAKE + 1),
