@@ -690,6 +690,8 @@ def _int32(**arrays):
 
 def _ld(t):
     """Leading dimension of a row-major matrix; that of a single row is its length."""
+    if t.is_contiguous():
+        return t.shape[1]
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError("the rows of x, residual, out and block_table must be contiguous")
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
