@@ -320,14 +320,15 @@ __device__ __forceinline__ uint2 four_of_value(const AttentionArgs& a, int kvh, 
 }
 
 // ---------------------------------------------------------------------------------------------
-// Few rows (generation): a workgroup takes a request's rows (at most 16) and one part of the keys; its four waves take
-// tiles of 32 keys in turn, each with its own running maximum, and join at the end.  Bound by reading K and V: both go
-// from memory to registers in pieces of 16 bytes a lane, the next tile's while this one is worked on; V passes through
-// the wave's own LDS to be transposed, so the waves never wait for each other.  64 requests of up to 8,192 keys (32
-// heads over 8, D = 128): 323 us, 5.3 TB/s (a copy of 2 GiB reaches 4.9).  One request of some 400 keys: 7.2 us, of
-// which three loads that wait for each other (lengths, table, keys) take the most, and 4.0 for the join.  D = 256 (one wave
-// per SIMD): the same 64 requests 646 us, 5.3 TB/s.  Four waves a workgroup | eight, us: one request of 100 keys 6.5 | 6.6,
-// at D = 256 8.7 | 11.4, the 64 requests at D = 256 646 | 757 (eight spill), at D = 128 and 64 the same.
+// Few rows (generation): a workgroup takes a request's rows (at most 16) and one part of the keys; its four (or eight,
+// see divide) waves take tiles of 32 keys in turn, each with its own running maximum, and join at the end.  Bound by
+// reading K and V: both go from memory to registers in pieces of 16 bytes a lane, the next tile's while this one is
+// worked on; V passes through the wave's own LDS to be transposed, so the waves never wait for each other.  64 requests
+// of up to 8,192 keys (32 heads over 8, D = 128): 323 us, 5.3 TB/s (a copy of 2 GiB reaches 4.9).  One request of some
+// 400 keys: 7.2 us, of which three loads that wait for each other (lengths, table, keys) take the most, and 4.0 for the
+// join.  D = 256 (one wave per SIMD): the same 64 requests 646 us, 5.3 TB/s.  Four waves a workgroup | eight, us: one
+// request of 100 keys 6.5 | 6.6, at D = 256 8.7 | 11.4, the 64 requests at D = 256 646 | 757 (eight spill), at D = 128
+// and 64 the same.
 //
 // Microscaled blocks (KIND): a lane's pieces are smaller, so that more of the time is the chain of a tile's steps, and waves
 // beside each other hide it: three per SIMD up to 128 dimensions (four up to 64), two above.  The same 64 requests, us, MXFP8 |
@@ -641,6 +642,11 @@ __device__ const uint4 zeros[1] = {};  // what a lane reads for a key or a dimen
 // TFLOP/s; 32 requests of 256 tokens (8 heads over 2, D = 256): 44 us.  LDS is busy 19 % of the time, without conflicts.  Measured and not kept: 64 rows a wave with one
 // wave per SIMD and the next scores between the exponentials (792 us); 128 rows a workgroup (766); two groups of waves
 // in turns (712 to 740).
+//
+// Microscaled blocks (KIND): codes do not go straight into LDS, which holds 16-bit values: a thread loads those of the tile
+// after next, converts what it has of the next one, and writes them where the loads above would (two tiles in LDS).  The
+// same 2 requests, us, MXFP8 | MXFP4 | 16-bit values: 785 | 750 | 770 (D = 64, four waves a SIMD: 472 | 463 | 420, with two
+// 531 | 550).  The 32 requests at D = 256: 44 to 46 MXFP4, of 8 tiles at most a workgroup, one after the other.
 template <int KIND, bool F16, int DP, int BN>
 __global__ __launch_bounds__(2 * MANY, (KIND != CACHE_16 && DP <= 64 ? 4 : 2)) void many_rows_kernel(AttentionArgs a, Plan pl) {
     constexpr int BM = MANY, KS = DP / 16, DT = DP / 32, KT = BN / 32;
