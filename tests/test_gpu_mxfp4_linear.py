@@ -218,3 +218,41 @@ def test_weights_past_32_bits():
     q = cq.mx_dequantize(*cq.mx_quantize(x, "mxfp8"), "mxfp8", torch.float32)
     assert torch.equal(y[:, -1], 0.5 * q[:, 10] + q[:, 11]) and torch.equal(y[:, 3], 6 * q[:, 14])
     assert not y[:, 4:-1].any()
+
+
+@pytest.mark.parametrize("form", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("M,out,gated", [(3, 40, False), (70, 520, True), (300, 8320, False)])
+def test_rows_far_apart(M, out, gated, form):
+    """Codes, their scales, residual and result with rows 2^23 bytes or elements apart: as with rows one behind the other."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    apart, inp = 1 << 23, 512
+    w, s = cq.mx_quantize(torch.randn((out * (2 if gated else 1), inp), generator=g, device="cuda"), "mxfp4")
+    x, e = cq.mx_quantize(torch.randn((M, inp), generator=g, device="cuda"), form)
+    r = torch.randn((M, out), generator=g, device="cuda").bfloat16()
+
+    def far(t):
+        v = torch.empty((M, apart), dtype=t.dtype, device="cuda")[:, : t.shape[1]]
+        return v.copy_(t)
+
+    kw = dict(x_format=form, gated=gated, activation="silu" if gated else "none")
+    want = cq.mxfp4_linear(x, w, s, x_scales=e, residual=r, **kw)
+    y = far(torch.full_like(r, 9.0))
+    cq.mxfp4_linear(far(x), w, s, x_scales=far(e), residual=far(r), out=y, **kw)
+    assert torch.equal(y, want)
+    assert torch.equal(cq.mxfp4_linear(far(x), w, s, x_scales=e, out=far(r), residual=r, **kw), want)
+
+
+@pytest.mark.parametrize("M,out", [(5, 70), (130, 700), (300, 8320)])
+def test_nan_codes(M, out):
+    """An element of x that is NaN makes its row NaN, and no other."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    w, s = cq.mx_quantize(torch.randn((out, 256), generator=g, device="cuda"), "mxfp4")
+    x, e = cq.mx_quantize(torch.randn((M, 256), generator=g, device="cuda"), "mxfp8")
+    clean = cq.mxfp4_linear(x, w, s, x_scales=e, out_dtype=torch.float32)
+    for row, k, code in ((0, 255, 0x7F), (M - 1, 3, 0xFF), (M // 2, 130, 0x7F)):
+        bad = x.clone()
+        bad[row, k] = code
+        y = cq.mxfp4_linear(bad, w, s, x_scales=e, out_dtype=torch.float32)
+        assert torch.isnan(y[row]).all()
+        others = torch.arange(M, device="cuda") != row
+        assert torch.equal(y[others], clean[others])

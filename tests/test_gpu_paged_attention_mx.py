@@ -255,3 +255,75 @@ def test_stream_graph_and_workspace(form):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, p.run(cq))
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("lens", [[(1, 3000), (2, 70)], [(60, 700), (1, 900)]])
+def test_more_keys_than_max_kv_says(lens, form):
+    """max_kv chooses how the keys are divided, not which are read."""
+    p = PagedMx(lens, 4, 2, 128, 16, "bf16", form)
+    q_max = max(n for n, _ in lens)
+    want = cq.paged_attention_mx(p.q, *p.kc_mx, *p.vc_mx, p.table, p.cu, p.kv, q_max, max(kv for _, kv in lens)).float()
+    for most in (0, 1, 500):
+        got = cq.paged_attention_mx(p.q, *p.kc_mx, *p.vc_mx, p.table, p.cu, p.kv, q_max, most).float()
+        # each side rounds weights and outputs to bf16, 2^-8 of the largest value at most each
+        assert (got - want).abs().max() <= 2.0 ** -6 * np.nanmax(np.abs(p.vc_np))
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("lens", [[(1, 100), (3, 40)], [(90, 200), (40, 61)]])
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+def test_values_beyond_binary16(lens, D, form):
+    """Blocks of values that binary16 cannot hold: infinities of either sign (and with e4m3 NaN elements), in keys that
+    some rows see and others do not; the same places as over a binary16 cache of those values."""
+    p = PagedMx(lens, 4, 2, D, 16, "f16", form)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    page = p.table_np[0, (lens[0][1] - 1 - lens[0][0] // 2) // 16]
+    codes, scales = p.vc_mx
+    codes[page, 0, :, : codes.shape[3] // 2] = torch.randint(0, 256, codes[page, 0, :, : codes.shape[3] // 2].shape,
+                                                            generator=g, device="cuda", dtype=torch.uint8)
+    scales[page, 0, :, 0] = 141  # 2^14
+    wide = [cq.mx_dequantize(*c, form, torch.float16) for c in (p.kc_mx, p.vc_mx)]
+    assert torch.isinf(wide[1]).any()
+    q_max, kv_max = max(n for n, _ in lens), max(kv for _, kv in lens)
+    a = p.run(cq)
+    b = cq.paged_attention(p.q, *wide, p.table, p.cu, p.kv, q_max, kv_max)
+    assert not torch.isfinite(b).all() and torch.isfinite(b).any()
+    assert torch.equal(torch.isnan(a), torch.isnan(b)) and torch.equal(torch.isinf(a), torch.isinf(b))
+    assert torch.equal(a[torch.isinf(a)], b[torch.isinf(b)])
+    # each side rounds weights and outputs to binary16, 2^-11 of a dimension's largest value at most each
+    top = torch.where(torch.isfinite(wide[1]), wide[1], 0).float().abs().amax((0, 2)).repeat_interleave(2, 0)
+    ok = torch.isfinite(b)
+    assert ((a.float() - b.float()).abs() <= 2.0 ** -9 * top)[ok].all()
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_rows_far_apart(form):
+    """Pages innermost: the rows of a page are 2^26 bytes apart, in codes and in scales."""
+    D, page, Hkv = 128, 16, 2
+    apart = 1 << 26
+    for lens in ([(1, 300), (1, 40)], [(40, 200), (1, 33)]):
+        p = PagedMx(lens, 4, Hkv, D, page, "bf16", form)
+        far = []
+        for t in p.kc_mx + p.vc_mx:
+            n, h, _, w = t.shape
+            hold = torch.zeros(apart * page, dtype=torch.uint8, device="cuda")
+            v = hold.as_strided(t.shape, (h * w, w, apart, 1))
+            v.copy_(t)
+            far.append(v)
+        p.check(cq, k_cache=far[0], k_scales=far[1], v_cache=far[2], v_scales=far[3])
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_nothing_to_attend(form):
+    """No token, no request, no page, no place in the block table."""
+    D, Hkv = 64, 2
+    width = D // 2 if form == "mxfp4" else D
+    for pages, entries, R, T in ((0, 3, 1, 4), (5, 0, 1, 4), (5, 3, 0, 4), (5, 3, 2, 0), (0, 0, 0, 0)):
+        caches = [torch.full((pages, Hkv, 16, w), 255, dtype=torch.uint8, device="cuda") for w in (width, D // 32) * 2]
+        q = torch.randn((T, 4, D), device="cuda").bfloat16()
+        lse = torch.full((T, 4), 5.0, device="cuda")
+        cu = torch.tensor([0] + [T] * R, dtype=torch.int32, device="cuda")
+        table = torch.zeros((R, entries), dtype=torch.int32, device="cuda")
+        out = cq.paged_attention_mx(q, *caches, table, cu, i32([9] * R), 4, 64, lse=lse)
+        assert out.shape == q.shape and (out == 0).all() and (lse == float("-inf")).all()
