@@ -53,18 +53,17 @@ __device__ __forceinline__ f32x4 add_products(i32x8 w, int ws, i32x8 x, int xs, 
 
 // ---------------------------------------------------------------------------------------------
 // Few rows, or few tiles: a workgroup takes 16 MT rows and 16 CT columns (gated: half of them of the gate, the others
-// of the other half), its W waves every W-th 128 of k; their sums join in LDS in the order of the waves.  Weights and
+// of the other half), its W waves a W-th of k each; their sums join in LDS in the order of the waves.  Weights and
 // x go straight into the lanes that multiply them.  x of 16 bits is quantized there, each block by the lane, or
-// the two lanes, that hold it.  What it takes is a launch and a wave's chain of steps, the next one's loads beside this one's
-// products: in graphs, 1 row 3584 -> 1024 5.5 us (MXFP8 6.5; 1.9 MB), 16 rows 1024 -> 2 x 3584 4.6 (4.9), 16 rows 4096 ->
-// 16,384 13.9 (14.3; 36 MB, 2.6 TB/s).  Two or four steps' loads on their way in place of one: 0.1 to 2 us slower.
+// the two lanes, that hold it.  What it takes is a launch and a wave's chain of loads, two or four steps of them on their way
+// at a time: in graphs, 1 row 3584 -> 1024 5.4 us (MXFP8 6.7; 1.9 MB), 16 rows 1024 -> 2 x 3584 4.7 (5.0), codes of 16 rows 4096
+// -> 16,384 9.5 (11.0; 36 MB, 3.8 TB/s), codes of 203 rows 4096 -> 809 7.9 (10.4).
 enum { X_BF16 = 0, X_F16 = 1, X_CODES = 2 };
 
 // A row tile's x operand of 128 k: what is loaded, and what the matrix cores take.
 template <int FORM, int XT>
 struct XPart {
     uint4 v[XT == X_CODES ? (FORM == MXFP4 ? 1 : 2) : 4];
-    uint8_t byte;
     __device__ __forceinline__ void load(const MxLinearArgs& a, int64_t m, int step, int quad) {
         if constexpr (XT == X_CODES) {
             const uint8_t* x = static_cast<const uint8_t*>(a.x) + m * a.ldx;
@@ -74,7 +73,6 @@ struct XPart {
                 v[0] = *reinterpret_cast<const uint4*>(x + (int64_t)step * 128 + 16 * quad);
                 v[1] = *reinterpret_cast<const uint4*>(x + (int64_t)step * 128 + 64 + 16 * quad);
             }
-            byte = a.xs[m * a.ldxs + 4 * step + quad];
         } else {
             const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + m * a.ldx + (int64_t)step * 128);
             if constexpr (FORM == MXFP4) {  // the lane's own block
@@ -88,10 +86,10 @@ struct XPart {
             }
         }
     }
+    // scale: of codes in, of values out
     __device__ __forceinline__ i32x8 take(int quad, int& scale) const {
         constexpr bool F16 = XT == X_F16;
         if constexpr (XT == X_CODES) {
-            scale = byte;
             if constexpr (FORM == MXFP4) return operand(v[0]);
             else return operand(v[0], v[1]);
         } else if constexpr (FORM == MXFP4) {
@@ -125,7 +123,7 @@ struct XPart {
 template <int FORM, int XT, bool F16, int MT, int CT, int W>
 __global__ __launch_bounds__(64 * W) void few_rows_mx(MxLinearArgs a, int col_tiles) {
     __shared__ __align__(16) float sums[W * MT * 16 * CT * 16];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, quad = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 15, quad = lane >> 4;
     const int64_t ct = blockIdx.x % col_tiles, rt = blockIdx.x / col_tiles;
     const int per = a.gated ? 8 * CT : 16 * CT;  // outputs per workgroup
     const int64_t n0 = ct * per, m0 = rt * (16 * MT);
@@ -136,7 +134,7 @@ __global__ __launch_bounds__(64 * W) void few_rows_mx(MxLinearArgs a, int col_ti
         const int64_t o = n0 + 16 * (up ? t - CT / 2 : t) + col;
         const int64_t c = (o < a.out ? o : a.out - 1) + (up ? a.out : 0);  // (past the edge: the last one)
         wp[t] = a.w + c * (a.in / 2) + 16 * quad;
-        sp[t] = a.ws + c * (a.in / MX_BLOCK) + quad;
+        sp[t] = a.ws + c * (a.in / MX_BLOCK);
     }
     int64_t row[MT];
 #pragma unroll
@@ -145,42 +143,69 @@ __global__ __launch_bounds__(64 * W) void few_rows_mx(MxLinearArgs a, int col_ti
         row[i] = m < a.M ? m : a.M - 1;
     }
     const int steps = (int)(a.in / 128);
-    uint4 w[CT];
-    uint8_t ws[CT];
-    XPart<FORM, XT> x[MT];
-    auto fetch = [&](int s) {
-        if (s >= steps) return;
+    // The wave's steps [s0, s1), AHEAD of them on their way at a time.  ALWAYS: also past the end (the last one again), so that
+    // the compiler knows how many loads a wait may leave.  Smaller tiles lose more by the loads; us (MXFP4
+    // codes), without | with: 16 rows 5120 -> 4096 (tiles 1x2) 7.2 | 8.9, 32 rows 4096 -> 16,384 (1x4) 18.5 | 11.8, 128 rows 4096
+    // -> 4096 (2x4) 15.2 | 11.3.
+    const int per_wave = (steps + W - 1) / W, s0 = wave * per_wave, s1 = min(steps, s0 + per_wave);
+    constexpr int AHEAD = XT == X_CODES && CT + MT * (FORM == MXFP4 ? 1 : 2) <= 8 ? 4 : 2;
+    constexpr bool ALWAYS = MT * CT > 2;
+    uint4 w[AHEAD][CT];
+    XPart<FORM, XT> x[AHEAD][MT];
+    auto fetch = [&](int j, int s) {
 #pragma unroll
-        for (int t = 0; t < CT; ++t) {
-            w[t] = *reinterpret_cast<const uint4*>(wp[t] + (int64_t)s * 64);
-            ws[t] = sp[t][4 * s];
-        }
+        for (int t = 0; t < CT; ++t) w[j][t] = *reinterpret_cast<const uint4*>(wp[t] + (int64_t)s * 64);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) x[i].load(a, row[i], s, quad);
+        for (int i = 0; i < MT; ++i) x[j][i].load(a, row[i], s, quad);
+    };
+    // Scales of AHEAD steps at a time, those of step s + i as a dword of the lanes of quad i.  A byte a lane for each step
+    // touches as many lines as its codes and took a third of the time: 203 rows 4096 -> 809 9.9 us in place of 7.9.
+    uint32_t next[CT + MT];
+    auto fetch_scales = [&](int s) {
+        const int64_t at = 4 * (int64_t)min(s + quad % AHEAD, steps - 1);
+#pragma unroll
+        for (int t = 0; t < CT; ++t) next[t] = *reinterpret_cast<const uint32_t*>(sp[t] + at);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) next[CT + i] = XT == X_CODES ? *reinterpret_cast<const uint32_t*>(a.xs + row[i] * a.ldxs + at) : 0;
     };
     f32x4 acc[MT][CT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int t = 0; t < CT; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
-    fetch(wave);
-    for (int s = wave; s < steps; s += W) {
-        uint4 wn[CT];
-        int wsn[CT];
-        XPart<FORM, XT> xn[MT];
+    auto multiply = [&](int j, const uint32_t* scales) {
+        auto scale = [&](uint32_t v) { return (int)((uint32_t)__builtin_amdgcn_ds_bpermute(4 * (col + 16 * j), (int)v) >> (8 * quad)); };
+        int ws[CT];
 #pragma unroll
-        for (int t = 0; t < CT; ++t) wn[t] = w[t], wsn[t] = ws[t];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) xn[i] = x[i];
-        fetch(s + W);
+        for (int t = 0; t < CT; ++t) ws[t] = scale(scales[t]);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            int xs;
-            const i32x8 b = xn[i].take(quad, xs);
+            int xs = XT == X_CODES ? scale(scales[CT + i]) : 0;
+            const i32x8 b = x[j][i].take(quad, xs);
 #pragma unroll
-            for (int t = 0; t < CT; ++t)
-                acc[i][t] = add_products<FORM>(operand(wn[t]), wsn[t], b, xs, acc[i][t]);
+            for (int t = 0; t < CT; ++t) acc[i][t] = add_products<FORM>(operand(w[j][t]), ws[t], b, xs, acc[i][t]);
         }
+    };
+    if (s0 < s1) {
+        uint32_t scales[CT + MT];
+        fetch_scales(s0);
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+            if (s0 + j < s1) fetch(j, s0 + j);
+        int s = s0;
+        for (; s + AHEAD < s1; s += AHEAD) {
+#pragma unroll
+            for (int i = 0; i < CT + MT; ++i) scales[i] = next[i];
+            fetch_scales(s + AHEAD);
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                multiply(j, scales);
+                if (ALWAYS || s + AHEAD + j < s1) fetch(j, min(s + AHEAD + j, s1 - 1));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+            if (s + j < s1) multiply(j, next);
     }
     // sums[wave][row][16 t + column]
 #pragma unroll
@@ -518,30 +543,34 @@ hipError_t many(const MxLinearArgs& a, hipStream_t st) {
 int64_t up(int64_t n, int64_t of) { return (n + of - 1) / of; }
 
 // Whether x's 16-bit values are quantized by the lanes that multiply them (again for every tile of columns), or once,
-// before.  us, within | before (some 3 of them the other launch): 32 rows, 4096 -> 16,384 18.7 | 18; 64 rows, 4096 -> 4096
-// 13.7 | 13, 4096 -> 16,384 33 | 25, 1024 -> 2 x 3584 7.9 | 9.6; 16 rows never less within.
-bool within(int64_t M, int64_t cols) { return M <= 32 || (M <= 64 && up(M, 16) * up(cols, 64) <= 256); }
+// before.  us in graphs, within | before (some 2.6 of them the other launch): 16 rows, 1024 -> 2 x 3584 4.7 | 6.7, 4096 ->
+// 16,384 12.7 | 12.1; 32 rows, 4096 -> 4096 8.9 | 8.7, 4096 -> 16,384 18.4 | 14.4; 64 rows, 3584 -> 1024 7.6 | 7.9, 4096 ->
+// 4096 13.6 | 10.4.
+bool within(int64_t M, int64_t cols) { return M <= 16 || (M <= 64 && up(M, 16) * up(cols, 64) <= 128); }
 
 // The smallest tile of rows and columns, and with it the most waves to a sum, with which the workgroups fit on the chip's 256
 // CUs at once: they take the time of their own chain of loads, and another round of them takes it again.  us, by rows and
 // columns of a tile in 16s:
 //                                     1x2     2x2     1x4     2x4     4x4
-//   1 row, 4096 -> 4096               6.8            10.3                    (16-bit x, MXFP4)
-//   16 rows, 1024 -> 2 x 3584         4.7             5.7
-//   64 rows, 4096 -> 4096            17.1    14.0    13.7    18.1
-//   203 rows, 4096 -> 809            13.1    10.0    11.9    14.6    21.5    (codes)
-//   128 rows, 4096 -> 4096           23.7    17.2    20.6    14.8    21.6
-//   1024 rows, 3584 -> 1024                                  19.6    17.6
+//   1 row, 4096 -> 4096               6.2             9.1                    (16-bit x, MXFP4)
+//   16 rows, 1024 -> 2 x 3584         4.8             5.8
+//   203 rows, 4096 -> 809            10.7     7.9     9.2    11.2    17.4    (codes)
+//   128 rows, 4096 -> 4096           20.3    12.2    17.1    11.3    17.4
+//   1024 rows, 3584 -> 1024          33.5    17.4    28.2    18.5    16.6
+//   64 rows, 4096 -> 16,384          40.7    21.4    33.7    21.9    17.9
 // 8 waves a tile; 16 in its place are as fast or slower up to 0.5 us.
 template <int FORM, int XT, bool F16>
 hipError_t launch_few(const MxLinearArgs& a, hipStream_t st) {
     const int64_t cols = a.gated ? 2 * a.out : a.out;
     if (up(a.M, 16) * up(cols, 32) <= 256) return few<FORM, XT, F16, 1, 2, 8>(a, st);
-    if (up(a.M, 32) * up(cols, 32) <= 256 && a.M > 16) return few<FORM, XT, F16, 2, 2, 8>(a, st);
-    if (up(a.M, 16) * up(cols, 64) <= 256 || a.M <= 16) return few<FORM, XT, F16, 1, 4, 8>(a, st);
-    if (XT != X_CODES || up(a.M, 32) * up(cols, 64) <= 256) return few<FORM, XT, F16, 2, 4, 8>(a, st);
-    if constexpr (XT == X_CODES) return few<FORM, XT, F16, 4, 4, 4>(a, st);
-    return hipErrorInvalidValue;
+    if constexpr (XT == X_CODES) {
+        if (up(a.M, 32) * up(cols, 32) <= 256 && a.M > 16) return few<FORM, XT, F16, 2, 2, 8>(a, st);
+        if (up(a.M, 16) * up(cols, 64) <= 256 || a.M <= 16) return few<FORM, XT, F16, 1, 4, 8>(a, st);
+        if (up(a.M, 32) * up(cols, 64) <= 256) return few<FORM, XT, F16, 2, 4, 8>(a, st);
+        return few<FORM, XT, F16, 4, 4, 4>(a, st);
+    } else {  // (at most 16 rows: see within)
+        return few<FORM, XT, F16, 1, 4, 8>(a, st);
+    }
 }
 
 template <int FORM, bool F16>
@@ -550,7 +579,7 @@ hipError_t launch_type(const MxLinearArgs& a, hipStream_t st) {
     const int64_t cols = a.gated ? 2 * a.out : a.out;
     // Where tiles of 64 by 64 no longer fit on the chip at once, the other kernel reads operands once for more products; with
     // MXFP8, which takes its steps four times as long, from two rounds and a half of them on.  us, few | many: MXFP4 64 rows,
-    // 4096 -> 16,384 22.3 | 22.1, 512 rows, 4096 -> 4096 36 | 22; MXFP8 512 rows 44 | 55, 1024 rows 78 | 63, 203 rows,
+    // 4096 -> 16,384 17.9 | 22.1, 512 rows, 4096 -> 4096 36 | 22; MXFP8 512 rows 44 | 55, 1024 rows 78 | 63, 203 rows,
     // 4096 -> 16,384 70 | 63, 512 rows, 1024 -> 2 x 3584 31 | 21.
     if (up(a.M, 64) * up(cols, 64) <= (FORM == MXFP4 ? 256 : 640)) return launch_few<FORM, X_CODES, F16>(a, st);
     if constexpr (FORM == MXFP4) {
