@@ -439,11 +439,13 @@ __global__ __launch_bounds__(64 * W, (W == 8 ? 2 : few_waves_per_simd<KIND, DP, 
                 }
             } else {
                 if (!ok_next[h]) continue;
+                int me = lane;
+                if constexpr (W == 8 && DP > 192) asm volatile("" : "+v"(me));  // (no register to keep what follows from it)
                 const int in_page = key - page_of(pl, key) * a.page;
                 const int64_t at = page_id[h] * a.c_page + kvh * a.c_head + (int64_t)in_page * a.c_row;
                 const int64_t sat = page_id[h] * a.s_page + kvh * a.s_head + (int64_t)in_page * a.s_row;
-                kr[h].load(reinterpret_cast<const uint8_t*>(a.kc) + at, 0, a.ks + sat, 0, quad, a.D);
-                vr[h].load(reinterpret_cast<const uint8_t*>(a.vc) + at, 0, a.vs + sat, 0, quad, a.D);
+                kr[h].load(reinterpret_cast<const uint8_t*>(a.kc) + at, 0, a.ks + sat, 0, me >> 4, a.D);
+                vr[h].load(reinterpret_cast<const uint8_t*>(a.vc) + at, 0, a.vs + sat, 0, me >> 4, a.D);
             }
         }
     };
@@ -1122,11 +1124,21 @@ Parts divide(int R, int T, int max_q, int max_kv, int H, int Hkv, int D, bool mx
         // workgroups, 31.4 (19.3) at 512, 33.1 (19.6) at 768; 100 of 9,000: 166 (125), 193 (97), 192 (108).  64 keys at
         // least: one request of 1,000 keys 10.3 us, at 128 11.7, at 256 14.1.
         p.few_splits = splits_for(p.few_tiles * Hkv, D <= 64 ? 512 : 256, max_kv, 64);
-        // Microscaled blocks, up to 768 keys with workgroups for no more than every CU: eight waves take them all in the time
-        // of the parts and their join, in one launch.  8 heads over 2, D = 128, us, 8 waves | parts, MXFP8 (MXFP4): 200 keys
-        // 7.8 (7.4) | 9.8 (9.5), 450 10.0 (8.9) | 9.7 (9.3), 950 13.6 (10.6) | 10.2 (9.7); a call of the 450 from Python
-        // 12.3 | 16.4.
-        if (mx && max_kv <= 768 && p.few_tiles * Hkv <= 256 && p.few_splits > 1) {
+        // Microscaled blocks, up to 768 keys: eight waves of one workgroup take all of a request's keys in one launch, where
+        // that gives a wave not many more tiles than the parts do, whose join takes 3 to 4 us.  32 heads over 8, us in
+        // graphs, 8 waves | parts, MXFP8 (MXFP4), pages of 16 tokens:
+        //                          256 keys                    512                       768
+        //   D =  64, 1 request    5.8 |  8.3 (5.6 |  8.3)   6.9 |  8.3 (6.8 |  8.2)   8.1 |  8.4 (7.9 |  8.4)
+        //   D = 128, 1            7.3 |  8.9 (6.5 |  8.6)   9.5 |  9.0 (8.1 |  8.7)  11.6 |  9.3 (9.6 |  9.0)
+        //            8            7.5 |  9.7 (6.7 |  9.4)   9.6 | 10.2 (8.3 |  9.5)  11.7 | 11.5 (9.8 | 10.6)
+        //   D = 192, 1            8.3 |  9.7 (7.9 |  9.6)  10.6 | 10.1 (9.9 | 10.0)  13.6 | 10.2 (12.5 | 10.1)
+        //   D = 256, 1           11.1 | 10.8 (8.7 |  9.8)  15.5 | 11.1 (11.1 | 10.3) 20.6 | 11.3 (13.5 | 10.5)
+        //            16          11.2 | 13.7 (8.9 | 12.2)  17.6 | 18.1 (11.4 | 14.3) 22.9 | 22.4 (13.9 | 16.5)
+        // Pages of 8 or 24 are within 10 % of these on both sides.  Called from Python, where parts cost an allocation and a
+        // launch, 10.4 | 14.8 at D = 128 with 450 keys and 11.6 | 14.8 (10.4 | 14.8) with 768: up to 128 dimensions all 768
+        // stay in one launch.
+        const int more_tiles = (max_kv + 255) / 256 - (max_kv + 128 * p.few_splits - 1) / (128 * p.few_splits);  // a wave's
+        if (mx && max_kv <= 768 && p.few_splits > 1 && more_tiles <= (D <= 128 ? 2 : D <= 192 ? 1 : 0)) {
             p.few_splits = 1;
             p.few_waves = 8;
         }
@@ -1173,10 +1185,12 @@ hipError_t launch_dim(const AttentionArgs& a, Plan pl, const Parts& p, hipStream
         if constexpr (KIND != CACHE_16) {
             if (p.few_waves == 8 && page16)
                 hipLaunchKernelGGL((few_rows_kernel<KIND, F16, FP, true, 8>), grid, dim3(512), 0, st, a, pl);
+            else if (p.few_waves == 8)
+                hipLaunchKernelGGL((few_rows_kernel<KIND, F16, FP, false, 8>), grid, dim3(512), 0, st, a, pl);
             else if (page16)
                 hipLaunchKernelGGL((few_rows_kernel<KIND, F16, FP, true, 4>), grid, dim3(256), 0, st, a, pl);
         }
-        if (!page16)
+        if (!page16 && p.few_waves == 4)
             hipLaunchKernelGGL((few_rows_kernel<KIND, F16, FP, false, 4>), grid, dim3(256), 0, st, a, pl);
         if (p.few_splits > 1)
             hipLaunchKernelGGL((join_kernel<F16, FP, FEW, 256>), dim3((unsigned)(p.few_tiles * a.Hkv * FEW)), dim3(256), 0,

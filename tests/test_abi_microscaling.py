@@ -212,3 +212,16 @@ def test_attention_helper_refuses():
     _refused("k_scales", cq._mx_cache, c, e, c, e[:, :, :8], 2, 64, -1)
     _refused("uint8", cq._mx_cache, c.view(torch.int8), e, c, e, 2, 64, -1)
     _refused("contiguous", cq._mx_cache, *[torch.zeros((9, 2, 64, 16), dtype=torch.uint8).transpose(2, 3), e] * 2, 2, 64, -1)
+
+
+def test_attention_in_parts_goes_by_what_a_wave_takes():
+    """Where a wave would take more tiles of 32 keys than in parts, by one at 256 dimensions and by two at 192, up to 768 keys
+    are divided (a workspace is asked for); with fewer dimensions, fewer keys or many requests they are not."""
+    size = cq.cq_paged_attention_mx_workspace_size
+    for kv in (130, 256):
+        assert all(size(1, 1, 1, kv, 32, 8, D) == 0 for D in (32, 64, 96, 128, 160, 192, 224, 256))
+    for kv in (257, 512):
+        assert all(size(1, 1, 1, kv, 32, 8, D) == 0 for D in (64, 128, 192)) and size(1, 1, 1, kv, 32, 8, 256) > 0
+    assert size(1, 1, 1, 768, 32, 8, 128) == 0 and size(1, 1, 1, 768, 32, 8, 160) > 0 and size(1, 1, 1, 768, 32, 8, 256) > 0
+    assert all(size(16, 16, 1, 768, 32, 8, D) == 0 for D in (64, 128, 192, 256))
+    assert size(1, 1, 1, 769, 32, 8, 64) > 0

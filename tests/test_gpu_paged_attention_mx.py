@@ -327,3 +327,41 @@ def test_nothing_to_attend(form):
         table = torch.zeros((R, entries), dtype=torch.int32, device="cuda")
         out = cq.paged_attention_mx(q, *caches, table, cu, i32([9] * R), 4, 64, lse=lse)
         assert out.shape == q.shape and (out == 0).all() and (lse == float("-inf")).all()
+
+
+def _paged_anew(pages, table, lens, page):
+    """The keys of pages [n, heads, old page, width] in pages of `page` tokens, and their block table."""
+    n, heads, old, width = pages.shape
+    per = [-(-kv // page) for _, kv in lens]
+    out = torch.full((sum(per), heads, page, width), 255, dtype=pages.dtype, device="cuda")
+    new_table, at = torch.full((len(lens), max(per)), -1, dtype=torch.int32, device="cuda"), 0
+    for r, (_, kv) in enumerate(lens):
+        j = torch.arange(kv, device="cuda")
+        own = torch.arange(at, at + per[r], device="cuda").flip(0)
+        new_table[r, : per[r]] = own.int()
+        out[own[j // page], :, j % page] = pages[table[r].long()[j // old], :, j % old]
+        at += per[r]
+    return out, new_table
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("lens", [[(1, 200)], [(1, 768), (1, 90)], [(2, 450), (1, 1), (1, 513)], [(1, 256)] * 3])
+def test_sums_do_not_depend_on_the_page_size(lens, D, form):
+    """Few rows, up to 768 keys: how the keys are divided over waves and parts goes by the sizes of the call, and the same
+    division has the same sums, whatever the pages' size and order."""
+    p = PagedMx(lens, 4, 2, D, 16, "bf16", form, seed=D)
+    want = p.run(cq)
+    for page in (8, 24, 31, 48):
+        k, table = _paged_anew(p.kc_mx[0], p.table, lens, page)
+        ks, v, vs = (_paged_anew(t, p.table, lens, page)[0] for t in (p.kc_mx[1], *p.vc_mx))
+        assert torch.equal(p.run(cq, k_cache=k, k_scales=ks, v_cache=v, v_scales=vs, block_table=table), want), page
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("page", [16, 24])
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+@pytest.mark.parametrize("kv", [255, 257, 512, 513, 768, 769])
+def test_either_side_of_the_borders_of_eight_waves(kv, D, page, form):
+    PagedMx([(1, kv)], 4, 2, D, page, "bf16", form, seed=kv).check(cq)
+    PagedMx([(1, kv)] + [(1, 40)] * 15, 8, 8, D, page, "f16", form, seed=kv).check(cq)
