@@ -580,8 +580,13 @@ hipError_t launch_type(const MxLinearArgs& a, hipStream_t st) {
     // Where tiles of 64 by 64 no longer fit on the chip at once, the other kernel reads operands once for more products; with
     // MXFP8, which takes its steps four times as long, from two rounds and a half of them on.  us, few | many: MXFP4 64 rows,
     // 4096 -> 16,384 17.9 | 22.1, 512 rows, 4096 -> 4096 36 | 22; MXFP8 512 rows 44 | 55, 1024 rows 78 | 63, 203 rows,
-    // 4096 -> 16,384 70 | 63, 512 rows, 1024 -> 2 x 3584 31 | 21.
-    if (up(a.M, 64) * up(cols, 64) <= (FORM == MXFP4 ? 256 : 640)) return launch_few<FORM, X_CODES, F16>(a, st);
+    // 4096 -> 16,384 70 | 63, 512 rows, 1024 -> 2 x 3584 31 | 21.  Few rows stay with tiles of 16 of them whatever the columns,
+    // of which the other kernel would multiply 128: 1 row, 4096 -> 24,576 MXFP4 14.7 | 21.0, 4096 -> 41,024 23.0 | 22.7 (MXFP8
+    // 26 | 62), 4096 -> 128,256 61 | 73 (69 | 102); 8 rows, 4096 -> 41,024 24.9 | 24.0 (28 | 62), 1024 -> 128,256 31.6 | 32.0
+    // (34.1 | 32.5); 16 rows MXFP4 17.6 | 21.8, 27.2 | 24.6 and, 1024 -> 128,256, 35.7 | 32.7, MXFP8 31 | 63, 82 | 106 and 38.6 |
+    // 33.1.
+    if (up(a.M, 64) * up(cols, 64) <= (FORM == MXFP4 ? 256 : 640) || a.M <= (FORM == MXFP4 ? 8 : 16))
+        return launch_few<FORM, X_CODES, F16>(a, st);
     if constexpr (FORM == MXFP4) {
         // 256 rows a workgroup and 256 of k a step, one workgroup a CU, where that leaves few CUs idle; us, 128 rows | 256:
         // 2048 x 4096 x 4096 30.5 | 34.7, 2048 x 2 x 3584 x 1024 22.1 | 20.6, 4096 x 4096 x 4096 52 | 43, 4096 x 16,384 x

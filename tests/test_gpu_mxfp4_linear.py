@@ -256,3 +256,22 @@ def test_nan_codes(M, out):
         assert torch.isnan(y[row]).all()
         others = torch.arange(M, device="cuda") != row
         assert torch.equal(y[others], clean[others])
+
+
+@pytest.mark.parametrize("M,out,gated", [(1, 16448, False), (8, 24600, False), (9, 16448, False), (1, 41024, False),
+                                         (8, 20520, True), (16, 41027, False), (16, 20513, True), (17, 41024, False)])
+@pytest.mark.parametrize("form", ["mxfp4", "mxfp8"])
+def test_codes_of_few_rows_and_many_columns(M, out, gated, form):
+    _check(M, out, 128, form=form, gated=gated, act="silu" if gated else "none", bias=True, ready=True)
+
+
+@pytest.mark.parametrize("M,form", [(1, "mxfp4"), (8, "mxfp4"), (1, "mxfp8"), (5, "mxfp8"), (8, "mxfp8"), (16, "mxfp8")])
+def test_few_rows_have_the_same_sums_from_values_and_from_codes(M, form):
+    """Through many columns as well: up to 8 rows (MXFP8: 16) are multiplied alike, in the same order."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    xt = torch.randn((M, 2048), generator=g, device="cuda").bfloat16()
+    w, s = cq.mx_quantize(torch.randn((41024, 2048), generator=g, device="cuda"), "mxfp4")
+    c, e = cq.mx_quantize(xt, form)
+    a = cq.mxfp4_linear(xt, w, s, x_format=form, out_dtype=torch.float32)
+    b = cq.mxfp4_linear(c, w, s, x_scales=e, x_format=form, out_dtype=torch.float32)
+    assert torch.equal(a, b)
