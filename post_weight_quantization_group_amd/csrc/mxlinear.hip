@@ -543,10 +543,16 @@ hipError_t many(const MxLinearArgs& a, hipStream_t st) {
 int64_t up(int64_t n, int64_t of) { return (n + of - 1) / of; }
 
 // Whether x's 16-bit values are quantized by the lanes that multiply them (again for every tile of columns), or once,
-// before.  us in graphs, within | before (some 2.6 of them the other launch): 16 rows, 1024 -> 2 x 3584 4.7 | 6.7, 4096 ->
-// 16,384 12.7 | 12.1; 32 rows, 4096 -> 4096 8.9 | 8.7, 4096 -> 16,384 18.4 | 14.4; 64 rows, 3584 -> 1024 7.6 | 7.9, 4096 ->
-// 4096 13.6 | 10.4.
-bool within(int64_t M, int64_t cols) { return M <= 16 || (M <= 64 && up(M, 16) * up(cols, 64) <= 128); }
+// before.  us in graphs, within | before (some 2 of them the other launch): 16 rows, 1024 -> 2 x 3584 4.7 | 6.7, 4096 ->
+// 4096 8.9 | 7.9 (MXFP8 9.5 | 9.1; called from Python 9.0 | 11.6, for the workspace and the launch), 4096 -> 16,384 12.7 | 11.8
+// (15.3 | 13.3); 32 rows, 4096 -> 4096 8.9 | 8.7, 4096 -> 16,384 18.4 | 14.4; 64 rows, 3584 -> 1024 7.6 | 7.9, 4096 -> 4096
+// 13.6 | 10.4.  Through more than 16,384 columns, MXFP8: 1 row, 4096 -> 41,024 28.3 | 28.4, 4 rows 30.3 | 29.5, 8 rows 33.2 | 30.6,
+// 16 rows 42.5 | 33.7, 4096 -> 128,256 114 | 85, 1024 -> 41,024 16.6 | 16.7; MXFP4, whose conversion is half as long: 16 rows,
+// 4096 -> 41,024 31.1 | 29.6, 1024 -> 41,024 11.7 | 15.5.
+bool within(int64_t M, int64_t cols, int form) {
+    if (M <= 16) return form == MXFP4 || M <= 4 || up(cols, 64) <= 256;
+    return M <= 64 && up(M, 16) * up(cols, 64) <= 128;
+}
 
 // The smallest tile of rows and columns, and with it the most waves to a sum, with which the workgroups fit on the chip's 256
 // CUs at once: they take the time of their own chain of loads, and another round of them takes it again.  us, by rows and
@@ -605,12 +611,12 @@ int64_t code_row(int64_t in, int form) { return form == MXFP4 ? in / 2 : in; }
 }  // namespace
 
 int64_t mx_linear_ws(int64_t M, int64_t out, int64_t in, int gated, int form, bool codes) {
-    return codes || within(M, gated ? 2 * out : out) ? 0 : M * (code_row(in, form) + in / MX_BLOCK);
+    return codes || within(M, gated ? 2 * out : out, form) ? 0 : M * (code_row(in, form) + in / MX_BLOCK);
 }
 
 hipError_t launch_mx_linear(const MxLinearArgs& args, hipStream_t st) {
     MxLinearArgs a = args;
-    if (!a.xs && !within(a.M, a.gated ? 2 * a.out : a.out)) {
+    if (!a.xs && !within(a.M, a.gated ? 2 * a.out : a.out, a.form)) {
         MxRowsArgs q{};
         q.values = const_cast<void*>(a.x);
         q.rows = a.M; q.len = a.in; q.ldx = a.ldx; q.ldc = code_row(a.in, a.form); q.lds = a.in / MX_BLOCK;

@@ -225,3 +225,14 @@ def test_attention_in_parts_goes_by_what_a_wave_takes():
     assert size(1, 1, 1, 768, 32, 8, 128) == 0 and size(1, 1, 1, 768, 32, 8, 160) > 0 and size(1, 1, 1, 768, 32, 8, 256) > 0
     assert all(size(16, 16, 1, 768, 32, 8, D) == 0 for D in (64, 128, 192, 256))
     assert size(1, 1, 1, 769, 32, 8, 64) > 0
+
+
+def test_linear_quantizes_before_where_columns_are_many():
+    """5 to 16 rows of values as MXFP8 through more than 16,384 columns are quantized once, into the workspace, not by every tile
+    of columns; fewer rows or columns, and MXFP4, are not."""
+    size = cq.cq_mxfp4_linear_workspace_size
+    for M in (5, 16):
+        assert size(M, 16385, 4096, 0, cq.MXFP8, 0) >= M * 4096 * 33 // 32 and size(M, 8193, 4096, 1, cq.MXFP8, 0) > 0
+        assert size(M, 16384, 4096, 0, cq.MXFP8, 0) == 0 and size(M, 8192, 4096, 1, cq.MXFP8, 0) == 0
+        assert size(M, 128256, 4096, 0, cq.MXFP4, 0) == 0 and size(M, 128256, 4096, 0, cq.MXFP8, 1) == 0
+    assert size(4, 128256, 4096, 0, cq.MXFP8, 0) == 0 and size(1, 128256, 4096, 0, cq.MXFP8, 0) == 0
