@@ -53,28 +53,41 @@ def dequantize(codes, scales, form):
     return v * np.repeat(s, 32, axis=-1)
 
 
+def _orders(n):
+    """The orders in which n 128s of k may be summed: lists of runs, a sum each, that are added up one by one.
+
+    All in one sum, or neighbours to one sum of 4 or 8, the same number to each but the last ones."""
+    steps = list(range(n))
+    orders = [[steps]]
+    for w in (4, 8):
+        each = -(-n // w)
+        orders.append([steps[i:i + each] for i in range(0, n, each)])
+    return orders
+
+
 def _sum_error(x, W):
     """(z, bound): z = x W^T and how far sums of its products in fp32 on the matrix cores may be off.
 
-    Products of elements with their scales are exact.  128 of them are added to a sum by one instruction or two: at most
-    130 additions, in whatever order, each within 2^-23 (they need not round to nearest) of what the sum can reach on the
-    way, |S| + A with S the sum in front of the 128 and A the sum of their |x| |W|.  The 128s go one after the other to
-    one sum, or in turn to 2, 4, 8 or 16 of them, which are then added up one by one; the bound is the largest of these
-    orders'."""
-    z, bound = x @ W.T, np.zeros((x.shape[0], W.shape[0]))
-    steps = range(0, x.shape[1], 128)
-    parts = [x[:, k:k + 128] @ W[:, k:k + 128].T for k in steps]
-    sizes = [np.abs(x[:, k:k + 128]) @ np.abs(W[:, k:k + 128]).T for k in steps]
-    for n in (1, 2, 4, 8, 16):
+    Products of elements with their scales are exact.  128 of them are added to a sum by one instruction, or by up to four
+    (64 of k each, or an operand in two parts, whose zeros change nothing): 128 additions and, where an instruction rounds what
+    it adds up before it adds it to the sum, four more.  Each is within 2^-23 (they need not round to nearest) of what the sum can
+    reach on the way, |S| + A with S the sum in front of the 128 and A the sum of their |x| |W|.  The bound is the largest
+    of those of the orders in which the 128s are summed."""
+    n = x.shape[1] // 128
+    z = x @ W.T
+    parts = [x[:, 128 * k:128 * k + 128] @ W[:, 128 * k:128 * k + 128].T for k in range(n)]
+    sizes = [np.abs(x[:, 128 * k:128 * k + 128]) @ np.abs(W[:, 128 * k:128 * k + 128]).T for k in range(n)]
+    bound = np.zeros_like(z)
+    for order in _orders(n):
         err, joined, size = np.zeros_like(z), np.zeros_like(z), np.zeros_like(z)
-        for w in range(min(n, len(parts))):
+        for run in order:
             S = np.zeros_like(z)
-            for part, A in zip(parts[w::n], sizes[w::n]):
-                err += 130 * 2.0 ** -23 * (np.abs(S) + A)
-                S = S + part
+            for k in run:
+                err += 132 * 2.0 ** -23 * (np.abs(S) + sizes[k])
+                S = S + parts[k]
             joined = joined + S
             size += np.abs(joined)
-        bound = np.maximum(bound, err + 2.0 ** -24 * (size if n > 1 else 0.0))
+        bound = np.maximum(bound, err + 2.0 ** -24 * (size if len(order) > 1 else 0.0))
     return z, (1 + 2.0 ** -10) * bound
 
 

@@ -84,3 +84,37 @@ def test_sums_beyond_the_bound_are_seen():
     W2[:, 17] += 0.5 * np.abs(W).max() / 6
     assert np.any(np.abs(x @ W2.T - y) > tol)
     assert np.all(tol < 1e-2 * np.abs(x) @ np.abs(W).T)
+
+
+def _sums_as_runs(parts, sizes, per):
+    """How far sums may be off where neighbouring 128s of k, `per` of them, go to one sum each (132 roundings a 128)."""
+    err, joined, joins = 0.0, 0.0, 0.0
+    for first in range(0, len(parts), per):
+        S = 0.0
+        for part, size in zip(parts[first:first + per], sizes[first:first + per]):
+            err += 132 * 2.0 ** -23 * (abs(S) + size)
+            S += part
+        joined += S
+        joins += abs(joined)
+    return err + (2.0 ** -24 * joins if per < len(parts) else 0.0)
+
+
+@pytest.mark.parametrize("steps", [1, 3, 8, 9, 17, 28, 40])
+def test_bound_of_sums_holds_for_runs_of_neighbours(steps):
+    """A wave takes a run of neighbouring steps of k, an eighth or a fourth of them.  Where large parts of either sign lie at
+    the two sides of a border between runs, the sums of the runs stay large while the running sum over all does not."""
+    rng = np.random.default_rng(steps)
+    x, W = np.zeros((6, 128 * steps)), np.zeros((1, 128 * steps))
+    W[0, ::128] = 1.0
+    for row in range(6):
+        x[row, ::128] = rng.standard_normal(steps)
+    for row, waves in enumerate((4, 8)):
+        per = -(-steps // waves)
+        x[row] = 0.0
+        for border in range(per, steps, per):
+            x[row, 128 * (border - 1)], x[row, 128 * border] = 1000.0, -1000.0
+    bound = mx._sum_error(x, W)[1][:, 0]
+    for row in range(6):
+        parts = [float(x[row, 128 * k]) for k in range(steps)]
+        for waves in (1, 4, 8):
+            assert bound[row] >= _sums_as_runs(parts, [abs(p) for p in parts], -(-steps // waves)), (row, waves)
