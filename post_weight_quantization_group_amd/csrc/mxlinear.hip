@@ -530,6 +530,7 @@ __global__ __launch_bounds__(2 * BM, 2) void many_rows_mx(MxLinearArgs a, int ro
 
 template <int FORM, bool F16, int BM, int KB, int STAGES>
 hipError_t many(const MxLinearArgs& a, hipStream_t st) {
+    if (a.in % KB != 0) return hipErrorInvalidValue;  // (a kernel of whole steps: what is left would be lost, or read in front of k)
     const int per = a.gated ? BIG_N / 2 : BIG_N;
     const int64_t rt = (a.M + BM - 1) / BM, ct = (a.out + per - 1) / per;
     const dim3 grid((unsigned)(rt * ct));
