@@ -248,9 +248,8 @@ __device__ __forceinline__ float max_of_halves(float x) {
 // loads PIECE neighbouring ones at a time (16 bytes where the row's width allows), which feed STEPS steps of 32.
 template <int KIND, int DP>
 struct Lanes {
-    static constexpr int PIECE = KIND == CACHE_16 ? 8
-                                 : KIND == MXFP8  ? (DP % 64 == 0 ? 16 : 8)
-                                                  : (DP % 128 == 0 ? 32 : DP % 64 == 0 ? 16 : 8);
+    static_assert(KIND == CACHE_16 || DP % 64 == 0, "");  // (see few_dim)
+    static constexpr int PIECE = KIND == CACHE_16 ? 8 : KIND == MXFP8 || DP % 128 != 0 ? 16 : 32;
     static constexpr int STEPS = PIECE / 8, PIECES = DP / 4 / PIECE;
     static constexpr int WORDS = KIND == MXFP8 ? 2 : 1;  // of codes, for eight values
     // The first of the eight dimensions of step ks that the lanes of `quad` hold.
@@ -278,13 +277,9 @@ struct Share {
         for (int j = 0; j < L::PIECES; ++j) {
             const int d = 4 * L::PIECE * j + L::PIECE * quad;
             if (D != DP && d >= D) continue;
-            if constexpr (N == 1) {
-                w[j] = *reinterpret_cast<const uint32_t*>(row + (at + d / 2));
-            } else {
-                const words v = *reinterpret_cast<const words*>(row + (at + (KIND == MXFP4 ? d / 2 : d)));
+            const words v = *reinterpret_cast<const words*>(row + (at + (KIND == MXFP4 ? d / 2 : d)));
 #pragma unroll
-                for (int i = 0; i < N; ++i) w[N * j + i] = v[i];
-            }
+            for (int i = 0; i < N; ++i) w[N * j + i] = v[i];
             scale[j] = scales[scale_at + d / MX_BLOCK];
         }
     }
