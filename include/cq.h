@@ -568,8 +568,9 @@ int32_t cq_kv_cache_write_mx(const void *k, int64_t k_token_stride, int64_t k_he
                              const int32_t *slots, int32_t n_tokens, void *stream);
 
 /*
- * cq_paged_attention over such a cache.  Keys and values are those the blocks stand for, in q's 16-bit type: exact in
- * bfloat16; where type is CQ_F16, what it cannot hold is an infinity or rounded (values quantized from binary16 are exact).
+ * cq_paged_attention over such a cache.  Keys and values are those the blocks stand for, in q's 16-bit type: exact where they
+ * were quantized from values of that type; what it cannot hold is an infinity or rounded (in bfloat16 values from 2^128 on
+ * and bits below 2^-133).
  *   args   as for cq_paged_attention, whose k_cache, v_cache and their strides are not read; kv_heads, head_dim, page_size
  *          and n_pages are the cache's.
  * Masks, outputs, limits and errors as there; a NaN block has no effect on a row that does not see it.  The workspace is of

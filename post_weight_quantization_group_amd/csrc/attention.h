@@ -27,7 +27,8 @@
 // either sign seen; both: NaN) that are applied at the end.
 //
 // The cache holds 16-bit values (KIND = CACHE_16) or microscaled blocks (MXFP4, MXFP8), whose values go into the
-// same products: they are exact in 16 bits (bf16; f16 within its range) and converted as they arrive, two an instruction.
+// same products: they are exact in the 16-bit type that they were quantized from, and converted as they arrive, two an
+// instruction.
 #pragma once
 #include "mx.h"
 #include "serve_args.h"
@@ -327,8 +328,8 @@ __device__ __forceinline__ uint2 four_of_value(const AttentionArgs& a, int kvh, 
 //
 // Microscaled blocks (KIND): a lane's pieces are smaller, so that more of the time is the chain of a tile's steps, and waves
 // beside each other hide it: three per SIMD up to 128 dimensions (four up to 64), two above.  The same 64 requests, us, MXFP8 |
-// MXFP4: 204 | 119 (256 dimensions 406 | 216, without that bound on registers 458 | 311).  Two tiles on their way in
-// place of one: 234 | 130, with fewer waves.
+// MXFP4: 175 | 104 back to back (256 dimensions 349 | 186).  In short runs, whose clock is lower, 204 | 118 (256 dimensions 403 |
+// 211, without that bound on registers 458 | 311); two tiles on their way in place of one, with fewer waves: 234 | 130.
 template <int KIND, int DP, bool PAGE16>
 constexpr int few_waves_per_simd() { return KIND == CACHE_16 ? 1 : (DP <= 64 ? 4 : DP <= 128 ? 3 : 2) - (PAGE16 ? 0 : 1); }
 
@@ -642,8 +643,9 @@ __device__ const uint4 zeros[1] = {};  // what a lane reads for a key or a dimen
 //
 // Microscaled blocks (KIND): codes do not go straight into LDS, which holds 16-bit values: a thread loads those of the tile
 // after next, converts what it has of the next one, and writes them where the loads above would (two tiles in LDS).  The
-// same 2 requests, us, MXFP8 | MXFP4 | 16-bit values: 785 | 750 | 770 (D = 64, four waves a SIMD: 472 | 463 | 420, with two
-// 531 | 550).  The 32 requests at D = 256: 44 to 46 MXFP4, of 8 tiles at most a workgroup, one after the other.
+// same 2 requests, us, MXFP8 | MXFP4 | 16-bit values, back to back on one card: 758 | 747 | 686 (D = 64, four waves a SIMD: 466 |
+// 460 | 407; with two 531 | 550).  The 32 requests at D = 256: 46 | 44 | 43, of 8 tiles at most a workgroup, one after the
+// other.
 template <int KIND, bool F16, int DP, int BN>
 __global__ __launch_bounds__(2 * MANY, (KIND != CACHE_16 && DP <= 64 ? 4 : 2)) void many_rows_kernel(AttentionArgs a, Plan pl) {
     constexpr int BM = MANY, KS = DP / 16, DT = DP / 32, KT = BN / 32;
@@ -1099,7 +1101,7 @@ struct Parts {
 
 int padded_dim(int D) { return D <= 64 ? 64 : D <= 96 ? 96 : D <= 128 ? 128 : D <= 192 ? 192 : 256; }
 // That of few_rows_kernel: a lane's fourth of 96 microscaled values would go in pieces of 8, which at 128 are 32 (or 16).  64
-// requests of up to 8,192 keys (24 heads over 8, D = 96), us, 96 | 128: MXFP8 186 | 158, MXFP4 161 | 105.
+// requests of up to 8,192 keys (24 heads over 8, D = 96), us in short runs, 96 | 128: MXFP8 186 | 158, MXFP4 161 | 105.
 template <int KIND>
 constexpr int few_dim(int padded) { return KIND != CACHE_16 && padded == 96 ? 128 : padded; }
 

@@ -108,7 +108,7 @@ __device__ __forceinline__ void activate8(int act, float* z) {
 
 // finish() of ROWS rows of eight neighbouring outputs each, from column o on, z and (gated) up in LDS; the rows are
 // `row_of(i)`, their sums at `from(i)`, those of the other half UP floats further on.  All residuals are asked for before the
-// first is used: `early` holds them, from ask_residuals().
+// first is used: `residuals` holds them, from Residuals::ask.
 template <int ROWS>
 struct Residuals {
     uint4 v[ROWS];

@@ -6,7 +6,8 @@
 //
 // Bound by memory.  8192 rows of 4096 bf16 values to MXFP4 14.4 us (84 MB with the codes: 5.8 TB/s, part of them from the
 // caches; a copy of 1 GiB reaches 5.1 to 5.5), to MXFP8 17; f16 there and back, 8192 x 3584 by MXFP8, 15.0 us each way
-// (89 MB, 5.9 TB/s).  Few rows take a launch: 2.3 us, 3.8 there and back in a graph.
+// (89 MB, 5.9 TB/s).  Rows with gaps between them take as long (8192 x 4096 of rows of 3 x 4096 to MXFP4 12.9 us, to MXFP8 15.9,
+// back into such rows 14.0 and 16.2; without gaps 14.3, 16.2, 13.7 and 16.2).  Few rows take a launch: 2.3 us, 3.8 there and back in a graph.
 #include "mx.h"
 #include "serve_args.h"
 

@@ -254,7 +254,7 @@ template <int BYTES>
 __device__ __forceinline__ int turn_of(int row) {
     return BYTES == 64 ? (row >> 2) & 3 : (row >> 1) & 7;
 }
-// acc += W x, 32 by 32 over 64 of k, with the scales' byte 0, or (HIGH) 2.  x of MXFP8: its elements below 2, and `large`.
+// acc += W x, 32 by 32 over 64 of k, with the scales' byte 0, or (`high`) 2.  x of MXFP8: its elements below 2, and `large`.
 template <int FORM, typename X>
 __device__ __forceinline__ f32x16 add_products_32(uint4 w, int ws, X x, X large, int xs, f32x16 acc, bool high) {
     const i32x8 a = operand(w);
@@ -565,7 +565,7 @@ bool within(int64_t M, int64_t cols, int form) {
 //   128 rows, 4096 -> 4096           20.3    12.2    17.1    11.3    17.4
 //   1024 rows, 3584 -> 1024          33.5    17.4    28.2    18.5    16.6
 //   64 rows, 4096 -> 16,384          40.7    21.4    33.7    21.9    17.9
-// 8 waves a tile; 16 in its place are as fast or slower up to 0.5 us.
+// 8 waves a tile (4x4: 4); 16 in place of 8 are as fast or slower up to 0.5 us.
 template <int FORM, int XT, bool F16>
 hipError_t launch_few(const MxLinearArgs& a, hipStream_t st) {
     const int64_t cols = a.gated ? 2 * a.out : a.out;
