@@ -1077,7 +1077,7 @@ def kv_cache_write_mx(k, v, k_cache, k_scales, v_cache, v_scales, slots, stream=
     """Quantizes k, v [T, kv_heads, head_dim] (bfloat16 or float16, strided views allowed) in blocks of 32 into caches of
     codes uint8 [pages, kv_heads, page_size, head_dim] (mxfp8) or [.., head_dim / 2] (mxfp4) and of scales uint8 [..,
     head_dim / 32], each block as by mx_quantize, at slots int32 [T] (page * page_size + offset; a negative slot is
-    skipped)."""
+    skipped, and none may occur twice)."""
     shape, dt = k.shape, k.dtype
     if len(shape) != 3 or v.shape != shape or v.dtype != dt or (dt != torch.bfloat16 and dt != torch.float16):
         raise ValueError("k and v must be bfloat16 or float16 [T, kv_heads, head_dim]")
