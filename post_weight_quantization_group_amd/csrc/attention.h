@@ -18,7 +18,7 @@
 //
 // The weights are rounded to the 16-bit type for the product with V, which the matrix cores take at 16 times the rate of
 // fp32 operands; scores, maxima, sums (of the weights before that rounding) and outputs are fp32.  Their rounding is of the
-// size of the output's own: relative to 64 bits the outputs are off by 2.1e-3 to 2.3e-3 (bf16; f16 2.5e-4), an fp32
+// size of the output's own: relative to 64 bits the outputs are off by 2.0e-3 to 2.4e-3 (bf16; f16 2.5e-4), an fp32
 // evaluation that is rounded at the end by 1.7e-3 (2.0e-4).
 //
 // A masked key has weight 0, and 0 times an infinity or a NaN in V would be a NaN: keys that no row
@@ -1134,10 +1134,12 @@ Parts divide(int R, int T, int max_q, int max_kv, int H, int Hkv, int D, bool mx
         // Pages of 8 or 24 are within 10 % of these on both sides.  Called from Python, where parts cost an allocation and a
         // launch, 10.4 | 14.8 at D = 128 with 450 keys and 11.6 | 14.8 (10.4 | 14.8) with 768: up to 128 dimensions all 768
         // stay in one launch.
-        const int more_tiles = (max_kv + 255) / 256 - (max_kv + 128 * p.few_splits - 1) / (128 * p.few_splits);  // a wave's
-        if (mx && max_kv <= 768 && p.few_splits > 1 && more_tiles <= (D <= 128 ? 2 : D <= 192 ? 1 : 0)) {
-            p.few_splits = 1;
-            p.few_waves = 8;
+        if (mx && max_kv <= 768 && p.few_splits > 1) {
+            const int parts = 128 * p.few_splits, more_tiles = (max_kv + 255) / 256 - (max_kv + parts - 1) / parts;  // a wave's
+            if (more_tiles <= (D <= 128 ? 2 : D <= 192 ? 1 : 0)) {
+                p.few_splits = 1;
+                p.few_waves = 8;
+            }
         }
     }
     if (rows > FEW && R > 0) {

@@ -224,7 +224,7 @@ def test_attention_in_parts_goes_by_what_a_wave_takes():
         assert all(size(1, 1, 1, kv, 32, 8, D) == 0 for D in (64, 128, 192)) and size(1, 1, 1, kv, 32, 8, 256) > 0
     assert size(1, 1, 1, 768, 32, 8, 128) == 0 and size(1, 1, 1, 768, 32, 8, 160) > 0 and size(1, 1, 1, 768, 32, 8, 256) > 0
     assert all(size(16, 16, 1, 768, 32, 8, D) == 0 for D in (64, 128, 192, 256))
-    assert size(1, 1, 1, 769, 32, 8, 64) > 0
+    assert size(1, 1, 1, 769, 32, 8, 64) > 0 and size(1, 1, 1, (1 << 31) - 1, 32, 8, 64) > 0
 
 
 def test_linear_quantizes_before_where_columns_are_many():
